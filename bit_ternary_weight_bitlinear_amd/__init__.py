@@ -19,19 +19,30 @@ Functions mirror the C entry points:
   ffn_sparse(x, gate, up, down_t)      -> ffn() for m <= 4 with an input-major down matrix
   gemm_i32(q, packed)                  -> acc int32 [m][n]
   workspace_size(op, m, k, n)          -> bytes
-Activations may be float32 or bfloat16 CUDA (HIP) tensors, contiguous, [m][k].
+  attention(q, k, v, cu_seqlens)       -> out [m][q_heads * head_dim]: causal attention over packed prompts
+  cache_alloc(pages, kv_heads, head_dim) -> KVCache: int8 codes and fp32 scales of 64-token pages
+  cache_append(cache, k, v, block_table, lens, cu_seqlens=None)   quantizes new tokens into the cache
+  cache_read(cache, block_table, begin, cu_seqlens, m) -> (k, v) [m][kv_heads][head_dim]
+  attention_cached(q, cache, block_table, lens, cu_seqlens=None, weights=None) -> out of new tokens over the cache
+  cache_evict(block_table, lens, weights, keep) -> (block_table, lens, weights, evicted, evicted_count)
+Activations may be float32 or bfloat16 CUDA (HIP) tensors, contiguous, [m][k]; q, k and v are
+[m][heads][head_dim] and may be slices of a fused projection's rows (any stride between tokens).
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+from typing import NamedTuple
 
 import torch
 
 __all__ = ["pack_weights", "pack_weights_threshold", "quant_act", "quant_act_norm", "forward_norm", "forward", "ffn", "gemm_i32", "workspace_size",
            "library_path", "load_library", "BitLinearError", "OP_FORWARD", "OP_FFN", "OP_PACK",
            "OP_GEMM_I32", "OP_PACK_THRESHOLD", "OP_FORWARD_NORM", "OP_FFN_SPARSE", "OP_FORWARD_A4",
-           "pack_kmajor", "ffn_sparse", "quant_act_a4", "forward_a4"]
+           "pack_kmajor", "ffn_sparse", "quant_act_a4", "forward_a4",
+           "attention", "attention_cached", "KVCache", "cache_alloc", "cache_append", "cache_read", "cache_evict",
+           "attention_workspace_size", "attention_cached_workspace_size", "CACHE_BLOCK"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbitlinear.so")
@@ -66,6 +77,19 @@ _SIGNATURES = {
     "bitlinear_ffn_sparse": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p,
                                       _c_p, _c_p, _c_p, _c_p, _c_p, _c_size, _c_p]),
     "bitlinear_gemm_i32": (_c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_size, _c_p]),
+    "bitlinear_attention_workspace_size": (_c_size, [_c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64]),
+    "bitlinear_attention": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64,
+                                     _c_p, _c_i64, ctypes.c_float, _c_p, _c_p, _c_size, _c_p]),
+    "bitlinear_cache_append": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
+                                        _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p]),
+    "bitlinear_cache_read": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_int, _c_i64,
+                                      _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+    "bitlinear_attention_cached_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_int]),
+    "bitlinear_attention_cached": (_c_int, [_c_p, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
+                                            _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, ctypes.c_float, _c_p, _c_p,
+                                            _c_p, _c_size, _c_p]),
+    "bitlinear_cache_evict": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p,
+                                       _c_p, _c_p, _c_p]),
 }
 
 _lib = None
@@ -375,3 +399,234 @@ def gemm_i32(q: torch.Tensor, packed: torch.Tensor):
     _check(lib.bitlinear_gemm_i32(_dev(q, "q", torch.int8), m, k, _dev(packed, "packed", torch.uint8), n,
                                   acc.data_ptr(), wp, wn, _stream(q.device)), "bitlinear_gemm_i32")
     return acc
+
+
+# ---------------------------------------------------------------- attention and the 8-bit cache
+CACHE_BLOCK = 64  # BL_CACHE_BLOCK in include/bitlinear.h
+
+
+class KVCache(NamedTuple):
+    """Pages of CACHE_BLOCK tokens: int8 codes [pages][kv_heads][64 * head_dim] in the order that
+    include/bitlinear.h gives, and one fp32 scale per page and head [pages][kv_heads], for K and V."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def cache_alloc(pages: int, kv_heads: int, head_dim: int, device="cuda") -> KVCache:
+    """An empty cache (head_dim 64 or 128)."""
+    if head_dim not in (64, 128) or pages < 1 or kv_heads < 1:
+        raise BitLinearError("a cache needs pages >= 1, kv_heads >= 1 and a head_dim of 64 or 128")
+    codes = [torch.zeros((pages, kv_heads, CACHE_BLOCK * head_dim), dtype=torch.int8, device=device) for _ in range(2)]
+    scales = [torch.zeros((pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales)
+
+
+def _on_its_device(fn):
+    """Runs a call with its first tensor's device as the current one: a kernel is launched on the
+    current device, and the stream taken for it has to be that device's."""
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        t = args[0] if args else None
+        t = t[0] if isinstance(t, tuple) and t else t
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index == torch.cuda.current_device():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(t.device):
+            return fn(*args, **kwargs)
+    return call
+
+
+def _heads(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
+    """(address, elements between tokens) of q, k or v [m][heads][head_dim]: heads of a token adjacent."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise BitLinearError(f"{name} must be a device (HIP) tensor")
+    if t.dim() != 3 or t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] != 1):
+        raise BitLinearError(f"{name} must be [m][heads][head_dim] with a token's heads adjacent")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise BitLinearError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    # the stride of a single token means nothing; torch may report any
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _ints(t: torch.Tensor, name: str, shape, device) -> int:
+    p = _dev(t, name, torch.int32)
+    if tuple(t.shape) != shape or t.device != device:
+        raise BitLinearError(f"{name} must have shape {shape} on {device}, got {tuple(t.shape)} on {t.device}")
+    return p
+
+
+def _starts(cu: torch.Tensor, device):
+    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 2:
+        raise BitLinearError("cu_seqlens must be int32 [seqs + 1]")
+    return _ints(cu, "cu_seqlens", (cu.shape[0],), device), cu.shape[0] - 1
+
+
+def _cache_args(cache, kv_heads: int | None, head_dim: int, device):
+    if len(cache) != 4:
+        raise BitLinearError("cache must be a KVCache")
+    k, v, ks, vs = cache
+    addresses = (_dev(k, "cache.k", torch.int8), _dev(v, "cache.v", torch.int8),
+                 _dev(ks, "cache.k_scale", torch.float32), _dev(vs, "cache.v_scale", torch.float32))
+    if k.dim() != 3 or v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != ks.shape or \
+            k.shape[2] != CACHE_BLOCK * head_dim or (kv_heads is not None and k.shape[1] != kv_heads):
+        raise BitLinearError(f"cache does not hold heads of {head_dim} (and {kv_heads} of them)")
+    if any(t.device != device for t in cache):
+        raise BitLinearError(f"cache must be on {device}")
+    return addresses, k.shape[0]
+
+
+def _table_args(block_table, lens, cu_seqlens, m: int, device, name: str = "lens"):
+    """(cu, lens, seqs, table, max_blocks) of a paged call; without cu_seqlens one row per sequence."""
+    cu, seqs = (None, m) if cu_seqlens is None else _starts(cu_seqlens, device)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise BitLinearError("block_table must be int32 [seqs][max_blocks]")
+    wide = block_table.shape[1]
+    return (cu, _ints(lens, name, (seqs,), device), seqs, _ints(block_table, "block_table", (seqs, wide), device), wide)
+
+
+def _own_workspace(nbytes: int, workspace, device):
+    if nbytes == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        _dev(workspace, "workspace")
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise BitLinearError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, {nbytes} needed")
+    # the caching allocator hands the memory on to later work of the same stream only
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def attention_workspace_size(dtype: torch.dtype, m: int, q_heads: int, kv_heads: int, head_dim: int, seqs: int) -> int:
+    code = _F32 if dtype == torch.float32 else _BF16 if dtype == torch.bfloat16 else -1
+    return int(load_library().bitlinear_attention_workspace_size(code, m, q_heads, kv_heads, head_dim, seqs))
+
+
+@_on_its_device
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
+              scale: float | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Causal attention over packed prompts. q [m][q_heads][head_dim], k and v [m][kv_heads][head_dim]
+    (fp32 or bf16, possibly slices of one projection's rows), cu_seqlens int32 [seqs + 1]
+    -> [m][q_heads * head_dim] of q's type. Rows outside the sequences are not written."""
+    lib = load_library()
+    qp, qs = _heads(q, "q")
+    dtype = _act_dtype(q)
+    kp, ks = _heads(k, "k", q)
+    vp, vs = _heads(v, "v", q)
+    m, hq, d = q.shape
+    hkv = k.shape[1]
+    if k.shape != (m, hkv, d) or v.shape != k.shape:
+        raise BitLinearError(f"k and v must be [{m}][kv_heads][{d}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    cu, seqs = _starts(cu_seqlens, q.device)
+    if out is None:
+        out = torch.empty((m, hq * d), dtype=q.dtype, device=q.device)
+    else:
+        _check_out(out, (m, hq * d), q.dtype, "out")
+    wp, wn = _own_workspace(lib.bitlinear_attention_workspace_size(dtype, m, hq, hkv, d, seqs), workspace, q.device)
+    _check(lib.bitlinear_attention(qp, qs, kp, ks, vp, vs, dtype, m, hq, hkv, d, cu, seqs,
+                                   d ** -0.5 if scale is None else scale, out.data_ptr(), wp, wn, _stream(q.device)),
+           "bitlinear_attention")
+    return out
+
+
+@_on_its_device
+def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
+                 cu_seqlens: torch.Tensor | None = None) -> None:
+    """Quantizes new tokens into the cache: row i of sequence s becomes token lens[s] + i. Without
+    cu_seqlens, one row per sequence. lens is left as it is (a negative entry: an unused slot)."""
+    lib = load_library()
+    kp, ks = _heads(k, "k")
+    dtype = _act_dtype(k)
+    vp, vs = _heads(v, "v", k)
+    m, heads, d = k.shape
+    if v.shape != k.shape:
+        raise BitLinearError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    (kc, vc, kscale, vscale), pages = _cache_args(cache, heads, d, k.device)
+    cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, k.device)
+    _check(lib.bitlinear_cache_append(kp, ks, vp, vs, dtype, m, heads, d, cu, lp, seqs, tp, wide, kc, vc, kscale, vscale,
+                                      pages, _stream(k.device)), "bitlinear_cache_append")
+
+
+@_on_its_device
+def cache_read(cache: KVCache, block_table: torch.Tensor, begin: torch.Tensor, cu_seqlens: torch.Tensor | None, m: int,
+               dtype: torch.dtype = torch.float32):
+    """The values of tokens begin[s] + i of every sequence, as many as cu_seqlens gives rows (m in all;
+    None: one each) -> (k, v) [m][kv_heads][head_dim]. Rows outside the sequences are not written."""
+    lib = load_library()
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise BitLinearError(f"dtype must be float32 or bfloat16, got {dtype}")
+    device = cache[0].device
+    d = cache[0].shape[2] // CACHE_BLOCK if cache[0].dim() == 3 else 0
+    (kc, vc, kscale, vscale), pages = _cache_args(cache, None, d, device)
+    cu, bp, seqs, tp, wide = _table_args(block_table, begin, cu_seqlens, m, device, "begin")
+    heads = cache[0].shape[1]
+    k = torch.empty((m, heads, d), dtype=dtype, device=device)
+    v = torch.empty((m, heads, d), dtype=dtype, device=device)
+    _check(lib.bitlinear_cache_read(kc, vc, kscale, vscale, pages, tp, wide, cu, bp, seqs,
+                                    _F32 if dtype == torch.float32 else _BF16, m, heads, d, k.data_ptr(), v.data_ptr(),
+                                    _stream(device)), "bitlinear_cache_read")
+    return k, v
+
+
+def attention_cached_workspace_size(m: int, q_heads: int, kv_heads: int, head_dim: int, seqs: int, max_blocks: int,
+                                    weights: bool = False) -> int:
+    return int(load_library().bitlinear_attention_cached_workspace_size(m, q_heads, kv_heads, head_dim, seqs, max_blocks,
+                                                                        int(weights)))
+
+
+@_on_its_device
+def attention_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lens: torch.Tensor,
+                     cu_seqlens: torch.Tensor | None = None, *, scale: float | None = None,
+                     weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None):
+    """Attention of new tokens, already appended, over the cache: row i of sequence s is token
+    lens[s] + i and sees the tokens up to itself. q [m][q_heads][head_dim] -> [m][q_heads * head_dim]
+    of q's type; weights fp32 [seqs][max_blocks] gets each block's attention weight added."""
+    lib = load_library()
+    qp, qs = _heads(q, "q")
+    dtype = _act_dtype(q)
+    m, hq, d = q.shape
+    (kc, vc, kscale, vscale), pages = _cache_args(cache, None, d, q.device)
+    hkv = cache[0].shape[1]
+    cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, q.device)
+    if weights is not None:
+        _check_out(weights, (seqs, wide), torch.float32, "weights")
+        if weights.device != q.device:
+            raise BitLinearError(f"weights must be on {q.device}")
+    if out is None:
+        out = torch.empty((m, hq * d), dtype=q.dtype, device=q.device)
+    else:
+        _check_out(out, (m, hq * d), q.dtype, "out")
+    need = lib.bitlinear_attention_cached_workspace_size(m, hq, hkv, d, seqs, wide, int(weights is not None))
+    wp, wn = _own_workspace(need, workspace, q.device)
+    _check(lib.bitlinear_attention_cached(qp, qs, dtype, m, hq, hkv, d, cu, lp, seqs, tp, wide, kc, vc, kscale, vscale,
+                                          pages, d ** -0.5 if scale is None else scale, out.data_ptr(),
+                                          weights.data_ptr() if weights is not None else None, wp, wn,
+                                          _stream(q.device)), "bitlinear_attention_cached")
+    return out
+
+
+@_on_its_device
+def cache_evict(block_table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, keep: int, *, first: int = 0,
+                recent: int = 1):
+    """Chooses the blocks every sequence keeps: its first `first`, its last `recent` and, up to `keep`
+    in all, those of the largest weight -> (block_table, lens, weights) of the kept blocks, and
+    (evicted, evicted_count): the pages that are free now, -1 behind them."""
+    lib = load_library()
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise BitLinearError("block_table must be int32 [seqs][max_blocks]")
+    seqs, wide = block_table.shape
+    device = block_table.device
+    tp = _ints(block_table, "block_table", (seqs, wide), device)
+    lp = _ints(lens, "lens", (seqs,), device)
+    wp = _dev(weights, "weights", torch.float32)
+    if tuple(weights.shape) != (seqs, wide) or weights.device != device:
+        raise BitLinearError(f"weights must have shape {(seqs, wide)} on {device}")
+    table_out, evicted = torch.empty((2, seqs, wide), dtype=torch.int32, device=device).unbind(0)
+    lens_out, count = torch.empty((2, seqs), dtype=torch.int32, device=device).unbind(0)
+    weights_out = torch.empty((seqs, wide), dtype=torch.float32, device=device)
+    _check(lib.bitlinear_cache_evict(tp, lp, wp, seqs, wide, keep, first, recent, table_out.data_ptr(),
+                                     lens_out.data_ptr(), weights_out.data_ptr(), evicted.data_ptr(), count.data_ptr(),
+                                     _stream(device)), "bitlinear_cache_evict")
+    return table_out, lens_out, weights_out, evicted, count

@@ -194,6 +194,49 @@ bl_status check_ws(void *ws, size_t ws_bytes, int64_t need)
     return BL_OK;
 }
 
+// ---- checks of the attention and cache calls
+bool heads_ok(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
+{
+    return tokens_ok(m) && kv_heads >= 1 && q_heads >= 1 && q_heads <= BL_MAX_HEADS && kv_heads <= q_heads &&
+           q_heads % kv_heads == 0 && (head_dim == 64 || head_dim == 128);
+}
+bool seqs_ok(int64_t seqs) { return seqs >= 1 && seqs <= BL_MAX_TOKENS; }
+bool cache_ok(int64_t max_blocks, int64_t pages)
+{
+    return max_blocks >= 1 && max_blocks <= BL_MAX_DIM && pages >= 1 && pages <= INT32_MAX;
+}
+bool finite(float v) { return v - v == 0.0f; }
+
+// rows of `width` adjacent elements, `stride` apart, read in 16-byte pieces
+bl_status rows_ok(const void *p, int64_t stride, int64_t width, bl_dtype dtype)
+{
+    const int64_t per16 = dtype == BL_BF16 ? 8 : 4;
+    if (stride < width || stride > INT32_MAX) return BL_ERR_SHAPE;
+    if (!aligned16(p) || stride % per16 != 0) return BL_ERR_ALIGN;
+    return BL_OK;
+}
+bool tables_aligned(const int32_t *cu, const int32_t *lens, const int32_t *table)
+{
+    return (!cu || aligned(cu, 4)) && aligned(lens, 4) && aligned(table, 4);
+}
+bool cache_aligned(const int8_t *k, const int8_t *v, const float *ks, const float *vs)
+{
+    return aligned16(k) && aligned16(v) && aligned(ks, 4) && aligned(vs, 4);
+}
+
+int64_t cached_workspace(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
+                         int64_t max_blocks, bool weights)
+{
+    CachedProblem p{};
+    p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads; p.head_dim = head_dim; p.seqs = seqs;
+    p.max_blocks = max_blocks; p.want_weights = weights; p.packed = true;
+    const int64_t packed = attention_cached_workspace(p);
+    if (m != seqs) return packed;
+    p.packed = false;  // one row per sequence may come without cu_seqlens
+    const int64_t single = attention_cached_workspace(p);
+    return packed > single ? packed : single;
+}
+
 }  // namespace
 
 extern "C" {
@@ -566,6 +609,134 @@ bl_status bitlinear_ffn(const void *x, bl_dtype dtype, int64_t m, int64_t hidden
     d.w0 = wd; d.w1 = nullptr; d.ldw = L.fp / 4; d.gamma0 = down_gamma; d.gamma1 = nullptr;
     d.out = y; d.acc_out = nullptr; d.epi = EPI_Y;
     return hip_status(launch_contraction(d, st));
+}
+
+// ---- attention and the 8-bit cache
+size_t bitlinear_attention_workspace_size(bl_dtype dtype, int64_t m, int64_t q_heads, int64_t kv_heads,
+                                          int64_t head_dim, int64_t seqs)
+{
+    if ((dtype != BL_F32 && dtype != BL_BF16) || !heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs)) return 0;
+    AttentionProblem p{};
+    p.bf16 = dtype == BL_BF16; p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads; p.head_dim = head_dim;
+    p.seqs = seqs;
+    return (size_t)attention_workspace(p);
+}
+
+bl_status bitlinear_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, bl_dtype dtype, int64_t m, int64_t q_heads, int64_t kv_heads,
+                              int64_t head_dim, const int32_t *cu_seqlens, int64_t seqs, float scale, void *out,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!q || !k || !v || !cu_seqlens || !out) return BL_ERR_NULL;
+    if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs)) return BL_ERR_SHAPE;
+    if (!finite(scale)) return BL_ERR_VALUE;
+    if (const bl_status s = rows_ok(q, q_stride, q_heads * head_dim, dtype)) return s;
+    if (const bl_status s = rows_ok(k, k_stride, kv_heads * head_dim, dtype)) return s;
+    if (const bl_status s = rows_ok(v, v_stride, kv_heads * head_dim, dtype)) return s;
+    if (!aligned16(out) || !aligned(cu_seqlens, 4)) return BL_ERR_ALIGN;
+    AttentionProblem p{};
+    p.q = q; p.k = k; p.v = v; p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.bf16 = dtype == BL_BF16; p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads; p.head_dim = head_dim;
+    p.cu = cu_seqlens; p.seqs = seqs; p.scale = scale; p.out = out;
+    if (const bl_status w = check_ws(workspace, workspace_bytes, attention_workspace(p))) return w;
+    return hip_status(launch_attention(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+bl_status bitlinear_cache_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, bl_dtype dtype,
+                                 int64_t m, int64_t kv_heads, int64_t head_dim, const int32_t *cu_seqlens,
+                                 const int32_t *lens, int64_t seqs, const int32_t *block_table, int64_t max_blocks,
+                                 int8_t *k_codes, int8_t *v_codes, float *k_scale, float *v_scale, int64_t pages,
+                                 void *stream)
+{
+    if (!k || !v || !lens || !block_table || !k_codes || !v_codes || !k_scale || !v_scale) return BL_ERR_NULL;
+    if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
+    if (!heads_ok(m, kv_heads, kv_heads, head_dim) || !seqs_ok(seqs) || !cache_ok(max_blocks, pages) ||
+        (!cu_seqlens && m != seqs))
+        return BL_ERR_SHAPE;
+    if (const bl_status s = rows_ok(k, k_stride, kv_heads * head_dim, dtype)) return s;
+    if (const bl_status s = rows_ok(v, v_stride, kv_heads * head_dim, dtype)) return s;
+    if (!tables_aligned(cu_seqlens, lens, block_table) || !cache_aligned(k_codes, v_codes, k_scale, v_scale))
+        return BL_ERR_ALIGN;
+    CacheAppend p{};
+    p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride; p.bf16 = dtype == BL_BF16;
+    p.m = m; p.kv_heads = kv_heads; p.head_dim = head_dim; p.cu = cu_seqlens; p.lens = lens; p.table = block_table;
+    p.seqs = seqs; p.max_blocks = max_blocks; p.k_codes = k_codes; p.v_codes = v_codes; p.k_scale = k_scale;
+    p.v_scale = v_scale; p.pages = pages;
+    return hip_status(launch_cache_append(p, static_cast<hipStream_t>(stream)));
+}
+
+bl_status bitlinear_cache_read(const int8_t *k_codes, const int8_t *v_codes, const float *k_scale, const float *v_scale,
+                               int64_t pages, const int32_t *block_table, int64_t max_blocks,
+                               const int32_t *cu_seqlens, const int32_t *begin, int64_t seqs, bl_dtype dtype, int64_t m,
+                               int64_t kv_heads, int64_t head_dim, void *k_out, void *v_out, void *stream)
+{
+    if (!k_codes || !v_codes || !k_scale || !v_scale || !block_table || !begin || !k_out || !v_out) return BL_ERR_NULL;
+    if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
+    if (!heads_ok(m, kv_heads, kv_heads, head_dim) || !seqs_ok(seqs) || !cache_ok(max_blocks, pages) ||
+        (!cu_seqlens && m != seqs))
+        return BL_ERR_SHAPE;
+    if (!tables_aligned(cu_seqlens, begin, block_table) || !cache_aligned(k_codes, v_codes, k_scale, v_scale) ||
+        !aligned16(k_out) || !aligned16(v_out))
+        return BL_ERR_ALIGN;
+    CacheRead p{};
+    p.k_codes = k_codes; p.v_codes = v_codes; p.k_scale = k_scale; p.v_scale = v_scale; p.pages = pages;
+    p.table = block_table; p.max_blocks = max_blocks; p.cu = cu_seqlens; p.begin = begin; p.seqs = seqs;
+    p.bf16 = dtype == BL_BF16; p.m = m; p.kv_heads = kv_heads; p.head_dim = head_dim; p.k_out = k_out; p.v_out = v_out;
+    return hip_status(launch_cache_read(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t bitlinear_attention_cached_workspace_size(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                                 int64_t seqs, int64_t max_blocks, int weights)
+{
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs) || !cache_ok(max_blocks, 1)) return 0;
+    return (size_t)cached_workspace(m, q_heads, kv_heads, head_dim, seqs, max_blocks, weights != 0);
+}
+
+bl_status bitlinear_attention_cached(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m, int64_t q_heads,
+                                     int64_t kv_heads, int64_t head_dim, const int32_t *cu_seqlens, const int32_t *lens,
+                                     int64_t seqs, const int32_t *block_table, int64_t max_blocks,
+                                     const int8_t *k_codes, const int8_t *v_codes, const float *k_scale,
+                                     const float *v_scale, int64_t pages, float scale, void *out, float *weights,
+                                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!q || !lens || !block_table || !k_codes || !v_codes || !k_scale || !v_scale || !out) return BL_ERR_NULL;
+    if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs) || !cache_ok(max_blocks, pages) ||
+        (!cu_seqlens && m != seqs))
+        return BL_ERR_SHAPE;
+    if (!finite(scale)) return BL_ERR_VALUE;
+    if (const bl_status s = rows_ok(q, q_stride, q_heads * head_dim, dtype)) return s;
+    if (!tables_aligned(cu_seqlens, lens, block_table) || !cache_aligned(k_codes, v_codes, k_scale, v_scale) ||
+        !aligned16(out) || (weights && !aligned(weights, 4)))
+        return BL_ERR_ALIGN;
+    const int64_t need = cached_workspace(m, q_heads, kv_heads, head_dim, seqs, max_blocks, weights != nullptr);
+    if (const bl_status w = check_ws(workspace, workspace_bytes, need)) return w;
+    CachedProblem p{};
+    p.q = q; p.q_stride = q_stride; p.bf16 = dtype == BL_BF16; p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads;
+    p.head_dim = head_dim; p.cu = cu_seqlens; p.lens = lens; p.table = block_table; p.seqs = seqs;
+    p.max_blocks = max_blocks; p.k_codes = k_codes; p.v_codes = v_codes; p.k_scale = k_scale; p.v_scale = v_scale;
+    p.pages = pages; p.scale = scale; p.out = out; p.weights = weights;
+    p.packed = cu_seqlens != nullptr; p.want_weights = weights != nullptr;
+    return hip_status(launch_attention_cached(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+bl_status bitlinear_cache_evict(const int32_t *block_table, const int32_t *lens, const float *weights, int64_t seqs,
+                                int64_t max_blocks, int64_t keep, int64_t first, int64_t recent, int32_t *table_out,
+                                int32_t *lens_out, float *weights_out, int32_t *evicted, int32_t *evicted_count,
+                                void *stream)
+{
+    if (!block_table || !lens || !weights || !table_out || !lens_out || !weights_out || !evicted || !evicted_count)
+        return BL_ERR_NULL;
+    if (!seqs_ok(seqs) || !cache_ok(max_blocks, 1)) return BL_ERR_SHAPE;
+    if (first < 0 || recent < 1 || first > BL_MAX_DIM || recent > BL_MAX_DIM || keep < first + recent)
+        return BL_ERR_VALUE;
+    if (!tables_aligned(nullptr, lens, block_table) || !aligned(weights, 4) || !aligned(table_out, 4) ||
+        !aligned(lens_out, 4) || !aligned(weights_out, 4) || !aligned(evicted, 4) || !aligned(evicted_count, 4))
+        return BL_ERR_ALIGN;
+    return hip_status(launch_cache_evict(block_table, lens, weights, seqs, max_blocks, keep, first, recent, table_out,
+                                         lens_out, weights_out, evicted, evicted_count,
+                                         static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -132,4 +132,74 @@ inline hipError_t launch_contraction(const GemmProblem &p, hipStream_t st)
     return skinny_supported(p.m) ? launch_skinny(p, st) : launch_gemm(p, st);
 }
 
+// ---- attention over packed prompts (attention.hip)
+template <int N>
+struct Width {
+    static constexpr int value = N;
+};
+struct AttentionProblem {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    bool bf16;
+    int64_t m, q_heads, kv_heads, head_dim;
+    const int32_t *cu;
+    int64_t seqs;
+    float scale;
+    void *out;  // [m][q_heads * head_dim]
+};
+int64_t attention_workspace(const AttentionProblem &p);
+hipError_t launch_attention(const AttentionProblem &p, void *ws, hipStream_t st);
+
+// ---- the 8-bit cache (cache.hip); cu == nullptr: one row per sequence
+struct CacheAppend {
+    const void *k, *v;
+    int64_t k_stride, v_stride;
+    bool bf16;
+    int64_t m, kv_heads, head_dim;
+    const int32_t *cu, *lens, *table;
+    int64_t seqs, max_blocks;
+    int8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int64_t pages;
+};
+hipError_t launch_cache_append(const CacheAppend &p, hipStream_t st);
+struct CacheRead {
+    const int8_t *k_codes, *v_codes;
+    const float *k_scale, *v_scale;
+    int64_t pages;
+    const int32_t *table;
+    int64_t max_blocks;
+    const int32_t *cu, *begin;
+    int64_t seqs;
+    bool bf16;
+    int64_t m, kv_heads, head_dim;
+    void *k_out, *v_out;
+};
+hipError_t launch_cache_read(const CacheRead &p, hipStream_t st);
+hipError_t launch_cache_evict(const int32_t *table, const int32_t *lens, const float *weights, int64_t seqs,
+                              int64_t max_blocks, int64_t keep, int64_t first, int64_t recent, int32_t *table_out,
+                              int32_t *lens_out, float *weights_out, int32_t *evicted, int32_t *evicted_count,
+                              hipStream_t st);
+
+// ---- attention of new tokens over the cache (attention_cached.hip)
+struct CachedProblem {
+    const void *q;
+    int64_t q_stride;
+    bool bf16;
+    int64_t m, q_heads, kv_heads, head_dim;
+    const int32_t *cu, *lens, *table;
+    int64_t seqs, max_blocks;
+    const int8_t *k_codes, *v_codes;
+    const float *k_scale, *v_scale;
+    int64_t pages;
+    float scale;
+    void *out;
+    float *weights;     // optional [seqs][max_blocks], added to
+    // what the layout of the workspace depends on beside the sizes
+    bool packed;        // cu given
+    bool want_weights;
+};
+int64_t attention_cached_workspace(const CachedProblem &p);
+hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t st);
+
 }  // namespace bl

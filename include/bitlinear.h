@@ -320,6 +320,137 @@ bl_status bitlinear_gemm_i32(const int8_t *q, int64_t m, int64_t k,
                              const uint8_t *packed, int64_t n, int32_t *acc,
                              void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Attention between the QKV and the output projection. The projections' fused
+ * output is read in place: q, k and v are [m][heads][head_dim] with the heads of
+ * a token adjacent and `*_stride` elements from one token to the next (a
+ * multiple of 16 bytes, at least heads * head_dim). head_dim is 64 or 128;
+ * q_heads is a multiple of kv_heads, and query head h reads kv head
+ * h / (q_heads / kv_heads).
+ *
+ * Packed sequences: `cu_seqlens` int32 [seqs + 1] on the device, sequence s is
+ * rows cu_seqlens[s] .. cu_seqlens[s+1]-1 (empty ones are allowed). Offsets are
+ * read by the kernels, so a call can be captured and replayed with others;
+ * values outside 0..m are taken as the nearest of the two, and a sequence that
+ * ends before it begins is empty. Rows before the first and behind the last
+ * sequence are neither read nor written.
+ */
+#define BL_MAX_HEADS ((int64_t)1 << 12)
+
+/* Bytes of workspace of bitlinear_attention (0 if none, or for invalid shapes) */
+size_t bitlinear_attention_workspace_size(bl_dtype dtype, int64_t m, int64_t q_heads, int64_t kv_heads,
+                                          int64_t head_dim, int64_t seqs);
+
+/*
+ * Causal attention over whole prompts: for row i of a sequence and query head h
+ *   p_ij = softmax over j <= i of scale * (q_i . k_j),   out_i = sum_j p_ij v_j
+ *   out       [m][q_heads * head_dim] of type `dtype` (output)
+ *   scale     finite (BL_ERR_VALUE otherwise); usually 1 / sqrt(head_dim)
+ * BL_BF16: products of the bf16 inputs summed in fp32, softmax in fp32, p
+ * rounded to bf16 for its product with v. BL_F32: as fp32 throughout.
+ * A row depends on rows 0..i of its own sequence only: infinities and NaN in
+ * later rows or in other sequences do not reach it.
+ *   workspace  >= bitlinear_attention_workspace_size() bytes
+ */
+bl_status bitlinear_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, bl_dtype dtype, int64_t m,
+                              int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                              const int32_t *cu_seqlens, int64_t seqs, float scale, void *out,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The 8-bit key/value cache. Pages hold BL_CACHE_BLOCK tokens; a sequence's
+ * block b of 64 tokens lies in page block_table[s][b] (int32 [seqs][max_blocks]).
+ * Per page and kv head there are 64 * head_dim int8 codes of K, as many of V, and
+ * one fp32 scale for each of the two; the code c stands for c * (scale / 127).
+ *   k_codes, v_codes  int8 [pages][kv_heads][64 * head_dim], 16-byte aligned
+ *   k_scale, v_scale  fp32 [pages][kv_heads]
+ * Inside a page and head the codes lie in 256-byte tiles of 16 rows x 16 bytes,
+ * the order in which the matrix instructions take them:
+ *   K code of (token, dim): ((token % 4) * (head_dim / 16) + dim / 16) * 256 + (token / 4) * 16 + dim % 16
+ *   V code of (token, dim): ((dim / 16) * 4 + token / 16) * 256 + (dim % 16) * 16 + token % 16
+ * Table entries outside 0..pages-1 name no page: such a block is not written and
+ * holds no tokens. Blocks from max_blocks on do not exist either.
+ * `lens` int32 [seqs] counts the tokens that a sequence holds before a call's new
+ * ones; a negative entry marks an unused slot, whose rows are skipped.
+ * `cu_seqlens` as above, or NULL for one row per sequence (m == seqs).
+ */
+#define BL_CACHE_BLOCK 64
+
+/*
+ * Appends new tokens: row i of sequence s becomes token lens[s] + i. Per block
+ * and kv head, for K and V each:
+ *   s' = max(s, max |x| over the block's new rows, 1e-30), where s is the stored
+ *        scale if the block holds earlier tokens and 0 otherwise
+ *   new codes      rint(x * (127 / s'))
+ *   earlier codes  rint(c * (s / s')) if the scale grew
+ * in fp32, ties to even. Codes of later slots stay as they are. NaN counts as 0
+ * and infinities as the largest finite number, so a token spoils its block's
+ * precision at most. `lens` is not changed: the caller adds the new tokens once
+ * every layer has appended. Two sequences may share pages that no call writes.
+ */
+bl_status bitlinear_cache_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                 bl_dtype dtype, int64_t m, int64_t kv_heads, int64_t head_dim,
+                                 const int32_t *cu_seqlens, const int32_t *lens, int64_t seqs,
+                                 const int32_t *block_table, int64_t max_blocks, int8_t *k_codes,
+                                 int8_t *v_codes, float *k_scale, float *v_scale, int64_t pages, void *stream);
+
+/*
+ * Reads tokens back: row i of sequence s is token begin[s] + i (begin as `lens`
+ * above), as fp32 c * (scale / 127), rounded once more for BL_BF16. Tokens
+ * without a page are written as 0.
+ *   k_out, v_out  [m][kv_heads][head_dim] of type `dtype` (output), dense
+ */
+bl_status bitlinear_cache_read(const int8_t *k_codes, const int8_t *v_codes, const float *k_scale,
+                               const float *v_scale, int64_t pages, const int32_t *block_table,
+                               int64_t max_blocks, const int32_t *cu_seqlens, const int32_t *begin,
+                               int64_t seqs, bl_dtype dtype, int64_t m, int64_t kv_heads, int64_t head_dim,
+                               void *k_out, void *v_out, void *stream);
+
+/* Bytes of workspace of bitlinear_attention_cached; `weights`: whether block
+ * weights are accumulated (0 if none, or for invalid shapes) */
+size_t bitlinear_attention_cached_workspace_size(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                                 int64_t seqs, int64_t max_blocks, int weights);
+
+/*
+ * Attention of new tokens over the cache (decode, and a few tokens at once).
+ * Row i of sequence s is the query of token lens[s] + i, already appended, and
+ * sees the tokens 0 .. lens[s] + i that have a page; a row that sees none gives 0.
+ *   q, out    as in bitlinear_attention
+ *   weights   optional fp32 [seqs][max_blocks] (input and output): the attention
+ *             weight that each block received, summed over the call's rows and
+ *             query heads, is added to it; blocks without one are left alone
+ * The codes enter exactly; q and the softmax weights are held to 2^-23 of their
+ * row's (and block's) largest, sums are exact int32 within a block and fp32
+ * across blocks, for either dtype. A row of q that is not finite gives NaN and
+ * adds nothing to the weights. Results do not depend on the order of execution.
+ *   workspace  >= bitlinear_attention_cached_workspace_size() bytes
+ */
+bl_status bitlinear_attention_cached(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m,
+                                     int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                     const int32_t *cu_seqlens, const int32_t *lens, int64_t seqs,
+                                     const int32_t *block_table, int64_t max_blocks, const int8_t *k_codes,
+                                     const int8_t *v_codes, const float *k_scale, const float *v_scale,
+                                     int64_t pages, float scale, void *out, float *weights, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/*
+ * Chooses the blocks that a sequence keeps, by accumulated attention weight. Of
+ * the ceil(lens[s] / 64) blocks (at most max_blocks) the first `first`, the last
+ * `recent` and, up to `keep` in all, the ones of the largest weight stay, in
+ * their order; of equal weights the lower block stays, and NaN counts as +inf.
+ *   keep >= first + recent, first >= 0, recent >= 1 (BL_ERR_VALUE otherwise)
+ *   table_out    int32 [seqs][max_blocks]: pages of the kept blocks, then -1
+ *   weights_out  fp32 [seqs][max_blocks]: their weights, then 0
+ *   lens_out     int32 [seqs]: lens minus 64 per evicted block (unused slots as is)
+ *   evicted      int32 [seqs][max_blocks]: pages of the evicted blocks, then -1
+ *   evicted_count  int32 [seqs]
+ */
+bl_status bitlinear_cache_evict(const int32_t *block_table, const int32_t *lens, const float *weights,
+                                int64_t seqs, int64_t max_blocks, int64_t keep, int64_t first, int64_t recent,
+                                int32_t *table_out, int32_t *lens_out, float *weights_out, int32_t *evicted,
+                                int32_t *evicted_count, void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *bitlinear_status_string(bl_status status);
 

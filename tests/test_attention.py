@@ -1,0 +1,529 @@
+"""Attention over packed prompts, the 8-bit cache, attention over it and the
+eviction of its blocks, on the GPU against the oracle's 64-bit definitions.
+
+Tolerances, per element. A rounding is off by at most u = eps / 2 of the type
+(fp32 2^-24, bf16 2^-8). An error r of every weight p_ij relative to itself moves
+out_i by at most r * sum_j p_ij |v_j| (`spread`), twice that with the division by
+their sum. The fp32 sum of d products is off by at most (d + 2) u sum |q||k|, and
+the logit's two scalings and the exponential's argument by a few u more of it, so
+r <= (d + 16) * 2^-24 * reach; the exponential and the sums over n keys add
+(n + 16) * 2^-24 (a running rescale rounds once per step). bf16 adds p's rounding
+to bf16 (2^-8 of spread) and the output's (2^-8 of the value)."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import attention as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def bl():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_ternary_weight_bitlinear_amd as m
+    m.load_library()
+    return m
+
+
+def _np(t):
+    return t.detach().float().cpu().numpy()
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def _starts(lens):
+    return _i32(np.concatenate([[0], np.cumsum(lens)]))
+
+
+def _rand(shape, seed, dtype, sd=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * sd).to(dtype).cuda()
+
+
+def _prompt_tolerance(want, spread, reach, n, d, dtype):
+    r = (d + 16) * 2.0**-24 * reach + (n + 16) * 2.0**-24
+    tol = 2 * r * spread + 2.0**-24 * np.abs(want)
+    if dtype == "bf16":
+        tol = tol + 2.0**-8 * np.abs(want) + 1.01 * 2.0**-8 * spread
+    return tol + 1e-30
+
+
+def _assert_within(got, want, tol, what=""):
+    off = np.abs(got - want)
+    bad = ~(off <= tol)
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} outside the tolerance; worst {np.nanmax(off / tol):.3g} of it, "
+                           f"first at {np.argwhere(bad)[0]}: {got[tuple(np.argwhere(bad)[0])]} for {want[tuple(np.argwhere(bad)[0])]}")
+
+
+# ---------------------------------------------------------------- prompts
+
+PROMPTS = [
+    ([1], 20, 5, 128), ([2, 1, 3], 4, 4, 64), ([63], 8, 2, 128), ([64, 65, 0, 127, 1], 8, 2, 64), ([128, 129], 7, 1, 128),
+    ([31, 32, 33], 6, 2, 128), ([0, 0, 5, 0], 3, 3, 64), ([257, 1, 190], 16, 2, 128), ([511], 5, 5, 64), ([700, 300], 4, 1, 128),
+    ([1] * 70 + [40], 4, 2, 64), ([1030], 12, 4, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,hq,hkv,d", PROMPTS)
+def test_prompt_against_the_definition(bl, lens, hq, hkv, d, dtype):
+    m = sum(lens)
+    qkv = _rand((m, (hq + 2 * hkv) * d), 1000 * m + hq, DTYPES[dtype], 1.3)
+    q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hkv * d, hkv * d], 1))  # slices of one projection's rows
+    out = bl.attention(q, k, v, _starts(lens))
+    want, spread, reach = ref.attention(_np(q), _np(k), _np(v), np.concatenate([[0], np.cumsum(lens)]), d ** -0.5)
+    assert out.dtype == DTYPES[dtype] and out.shape == (m, hq * d)
+    _assert_within(_np(out).reshape(m, hq, d), want, _prompt_tolerance(want, spread, reach, max(lens), d, dtype), f"{lens}")
+    again = bl.attention(q.contiguous(), k.contiguous(), v.contiguous(), _starts(lens))
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
+def test_prompt_scales(bl, dtype, scale):
+    """scale 0 is the running mean; a negative one turns the order of the logits; 3 is nearly one-hot."""
+    lens, hq, hkv, d = [150, 90], 8, 2, 64
+    q, k, v = (_rand((240, h, d), 7 + h + i, DTYPES[dtype]) for i, h in enumerate((hq, hkv, hkv)))
+    out = bl.attention(q, k, v, _starts(lens), scale=scale)
+    want, spread, reach = ref.attention(_np(q), _np(k), _np(v), [0, 150, 240], scale)
+    _assert_within(_np(out).reshape(240, hq, d), want, _prompt_tolerance(want, spread, reach, 150, d, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_growing_logits(bl, dtype):
+    """Keys that grow along the sequence (the running maximum rises with every tile) and ones that shrink."""
+    m, hq, hkv, d = 400, 4, 1, 128
+    q, k, v = _rand((m, hq, d), 3, DTYPES[dtype]), _rand((m, hkv, d), 4, DTYPES[dtype]), _rand((m, hkv, d), 5, DTYPES[dtype])
+    ramp = torch.linspace(0.05, 8, m, device="cuda")[:, None, None]
+    for r in (ramp, ramp.flip(0)):
+        kr = (k.float() * r).to(k.dtype)
+        out = bl.attention(q, kr, v, _starts([m]))
+        want, spread, reach = ref.attention(_np(q), _np(kr), _np(v), [0, m], d ** -0.5)
+        _assert_within(_np(out).reshape(m, hq, d), want, _prompt_tolerance(want, spread, reach, m, d, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_prompt_rows_do_not_see_later_or_foreign_values(bl, dtype, bad):
+    """NaN and infinities in a later row, or in another sequence, leave a row's bits as they are."""
+    lens, hq, hkv, d = [100, 37, 200], 8, 2, 128
+    m = sum(lens)
+    q, k, v = (_rand((m, h, d), 11 + i, DTYPES[dtype]) for i, h in enumerate((hq, hkv, hkv)))
+    clean = bl.attention(q, k, v, _starts(lens))
+    for row, col in ((60, 5), (99, 127), (100, 0), (137 + 130, 64), (137 + 131, 3), (336, 17)):
+        for which in (1, 2):
+            t = [q, k, v]
+            t[which] = t[which].clone()
+            t[which][row, :, col] = bad
+            out = bl.attention(*t, _starts(lens))
+            seq = 0 if row < 100 else 1 if row < 137 else 2
+            end = (100, 137, 337)[seq]
+            untouched = torch.ones(m, dtype=torch.bool, device="cuda")
+            untouched[row:end] = False
+            assert torch.equal(out[untouched], clean[untouched]), (row, which)
+            if which == 2:  # its own rows do see it
+                assert not torch.isfinite(out[row:end].view(-1, hq, d)[:, :, col]).any()
+
+
+def test_prompt_leaves_rows_outside_the_sequences(bl):
+    q, k, v = (_rand((90, h, 64), 21 + i, torch.bfloat16) for i, h in enumerate((4, 2, 2)))
+    out = torch.full((90, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    bl.attention(q, k, v, _i32([10, 30, 71]), out=out)
+    assert (out[:10] == 7).all() and (out[71:] == 7).all() and torch.isfinite(out).all()
+    alone = bl.attention(q[30:71], k[30:71], v[30:71], _starts([41]))
+    assert torch.equal(out[30:71], alone)
+
+
+@pytest.mark.parametrize("cu", [[-5, 40, 1000], [0, 50, 20, 90], [0, 2**31 - 1, 30], [95, 100]])
+def test_prompt_offsets_out_of_order_stay_in_bounds(bl, cu):
+    """Offsets that the rule for bad values covers: no access outside the rows."""
+    q, k, v = (_rand((90, h, 64), 31 + i, torch.bfloat16) for i, h in enumerate((4, 2, 2)))
+    guard = torch.full((92, 256), 3.0, dtype=torch.bfloat16, device="cuda")
+    bl.attention(q, k, v, _i32(cu), out=guard[1:91])
+    assert (guard[0] == 3).all() and (guard[91] == 3).all()
+    assert not torch.isnan(guard).any()
+
+
+# ---------------------------------------------------------------- the cache
+
+class _Paged:
+    """A cache and its natural-order copy, with pages dealt in no order."""
+
+    def __init__(self, bl, lens, new, hkv, d, seed, wide=None):
+        rng = np.random.default_rng(seed)
+        blocks = [max(0, -(-(max(a, 0) + b) // 64)) for a, b in zip(lens, new)]
+        self.wide = wide or max(1, max(blocks))
+        self.pages, self.hkv, self.d = sum(blocks) + 2, hkv, d
+        order = rng.permutation(self.pages)
+        self.table = np.full((len(lens), self.wide), -1, np.int64)
+        at = 0
+        for s, n in enumerate(blocks):
+            n = min(n, self.wide)
+            self.table[s, :n] = order[at:at + n]
+            at += n
+        self.place = ref.code_places(d)
+        shape = (self.pages, hkv, 64, d)
+        self.kc, self.vc = (np.clip(np.rint(rng.standard_normal(shape) * 40), -127, 127).astype(np.int8) for _ in range(2))
+        self.ks, self.vs = ((0.5 + 2 * rng.random((self.pages, hkv))).astype(np.float32) for _ in range(2))
+        self.cache = bl.KVCache(torch.tensor(ref.stored(self.kc, self.place[0])).cuda(),
+                                torch.tensor(ref.stored(self.vc, self.place[1])).cuda(),
+                                torch.tensor(self.ks).cuda(), torch.tensor(self.vs).cuda())
+
+    def same(self):
+        c = self.cache
+        np.testing.assert_array_equal(c.k_scale.cpu().numpy(), self.ks)
+        np.testing.assert_array_equal(c.v_scale.cpu().numpy(), self.vs)
+        np.testing.assert_array_equal(ref.natural(c.k.cpu().numpy(), self.place[0]), self.kc)
+        np.testing.assert_array_equal(ref.natural(c.v.cpu().numpy(), self.place[1]), self.vc)
+
+
+APPENDS = [  # tokens before, new tokens
+    ([0], [1]), ([63], [1]), ([64], [1]), ([5, 0, 130], [3, 64, 1]), ([17, 70, 128, 0], [1, 1, 1, 1]), ([0, 60], [200, 0]), ([1, 127], [63, 66]),
+    ([100, -1, 3], [20, 4, 7]), ([15, 16, 31, 48], [1, 16, 17, 15]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hkv,d", [(5, 128), (1, 64), (2, 128)])
+@pytest.mark.parametrize("lens,new", APPENDS)
+def test_append_bit_exact(bl, lens, new, hkv, d, dtype):
+    """Codes, scales and every byte that is not written, against the oracle; then read back."""
+    c = _Paged(bl, lens, new, hkv, d, 5)
+    m = sum(new)
+    # rows of very different sizes, so that some scales grow and some do not
+    x = _rand((m, 2 * hkv * d), 40 + m, DTYPES[dtype]) * (10.0 ** (torch.arange(m, device="cuda") % 4 - 2))[:, None].to(DTYPES[dtype])
+    k, v = (t.unflatten(1, (hkv, d)) for t in x.split(hkv * d, 1))
+    cu = None if new == [1] * len(new) and dtype == "bf16" else _starts(new)
+    bl.cache_append(c.cache, k, v, _i32(c.table), _i32(lens), cu)
+    host_cu = None if cu is None else cu.cpu().numpy()
+    ref.cache_append(c.kc, c.ks, _np(k), c.table, lens, host_cu)
+    ref.cache_append(c.vc, c.vs, _np(v), c.table, lens, host_cu)
+    c.same()
+    gk, gv = bl.cache_read(c.cache, _i32(c.table), _i32(lens), cu, m, DTYPES[dtype])
+    rows = [(s, s + 1) for s in range(m)] if cu is None else list(zip(host_cu[:-1], host_cu[1:]))
+    for s, (a, b) in enumerate(rows):
+        if lens[s] >= 0:
+            for got, codes, scales in ((gk, c.kc, c.ks), (gv, c.vc, c.vs)):
+                want = torch.tensor(ref.tokens(codes, scales, c.table[s], lens[s], lens[s] + b - a)[0]).to(DTYPES[dtype])
+                assert torch.equal(got[a:b].cpu(), want)
+
+
+def test_append_token_by_token_and_zero_rows(bl):
+    """A block filled by single tokens, each larger than the one before, with rows of zeros between."""
+    hkv, d = 2, 128
+    c = _Paged(bl, [60], [10], hkv, d, 9)
+    for i in range(10):
+        k = _rand((1, hkv, d), i, torch.float32, 0.0 if i % 3 == 1 else 2.0 ** i)
+        bl.cache_append(c.cache, k, -k, _i32(c.table), _i32([60 + i]))
+        ref.cache_append(c.kc, c.ks, _np(k), c.table, [60 + i], None)
+        ref.cache_append(c.vc, c.vs, _np(-k), c.table, [60 + i], None)
+        c.same()
+
+
+def test_append_values_that_are_not_finite(bl):
+    hkv, d = 1, 64
+    c = _Paged(bl, [3], [4], hkv, d, 10)
+    k = _rand((4, hkv, d), 3, torch.float32)
+    k[0, 0, 3], k[1, 0, 4], k[2, 0, 5] = float("nan"), float("inf"), -float("inf")
+    bl.cache_append(c.cache, k, k, _i32(c.table), _i32([3]), _starts([4]))
+    ref.cache_append(c.kc, c.ks, _np(k), c.table, [3], [0, 4])
+    ref.cache_append(c.vc, c.vs, _np(k), c.table, [3], [0, 4])
+    c.same()
+    assert torch.isfinite(c.cache.k_scale).all()
+
+
+@pytest.mark.parametrize("table,lens", [([[-1, 1]], [60]), ([[0, 99]], [60]), ([[0, -7]], [64]), ([[0, 1]], [126]), ([[0, 1]], [128]),
+                                        ([[0, 1]], [2**31 - 3])])
+def test_blocks_without_a_page(bl, table, lens):
+    """Entries that name no page, and tokens past the table: nothing is written there, nothing read."""
+    hkv, d = 2, 64
+    c = _Paged(bl, [0], [128], hkv, d, 12)
+    c.table = np.array(table)
+    k = _rand((5, hkv, d), 3, torch.float32)
+    bl.cache_append(c.cache, k, k, _i32(table), _i32(lens), _starts([5]))
+    ref.cache_append(c.kc, c.ks, _np(k), c.table, lens, [0, 5])
+    ref.cache_append(c.vc, c.vs, _np(k), c.table, lens, [0, 5])
+    c.same()
+    gk, gv = bl.cache_read(c.cache, _i32(table), _i32(lens), _starts([5]), 5)
+    assert torch.equal(gk.cpu(), torch.tensor(ref.tokens(c.kc, c.ks, c.table[0], lens[0], lens[0] + 5)[0]))
+    assert torch.equal(gv.cpu(), torch.tensor(ref.tokens(c.vc, c.vs, c.table[0], lens[0], lens[0] + 5)[0]))
+    if lens[0] < 1000:
+        _check_cached(bl, c, lens, [5], 4, "f32", True, 3)
+
+
+# ---------------------------------------------------------------- attention over the cache
+
+def _check_cached(bl, c, lens, new, hq, dtype, weighted, seed, packed=True, scale=None, workspace=None):
+    """attention_cached against the oracle. Besides the prompts' terms: q is held to 1 part in 8355711 of its
+    row's largest (`reach` counts that), p to 1 part of its block's largest (`grain`); the integer sums are exact,
+    their join rounds three times, and a block's result twice more."""
+    m, d = sum(new), c.d
+    q = _rand((m, hq, d), seed, DTYPES[dtype], 1.5)
+    cu = _starts(new) if packed else None
+    w0 = torch.rand((len(lens), c.wide), generator=torch.Generator().manual_seed(seed)).cuda()
+    w = w0.clone() if weighted else None
+    guard = torch.full((m, hq * d), 7.0, dtype=DTYPES[dtype], device="cuda")
+    out = bl.attention_cached(q, c.cache, _i32(c.table), _i32(lens), cu, weights=w, out=guard, scale=scale, workspace=workspace)
+    want, add, spread, reach, grain = ref.attention_cached(_np(q), c.kc, c.ks, c.vc, c.vs, c.table, lens,
+                                                           None if cu is None else cu.cpu().numpy(), d ** -0.5 if scale is None else scale)
+    for s, (a, b) in enumerate(ref._rows(None if cu is None else cu.cpu().numpy(), m, len(lens))):
+        if lens[s] < 0:
+            assert (out[a:b] == 7).all()
+            want[a:b] = 7
+    blocks = max(1, c.wide)
+    r = 32 * 2.0**-24 * reach + (blocks + 96) * 2.0**-24
+    tol = 2 * r * spread + 2.0**-22 * grain + 2.0**-24 * np.abs(want) + 1e-30
+    if dtype == "bf16":
+        tol = tol + 2.0**-8 * np.abs(want)
+    got = _np(out).reshape(m, hq, d)
+    _assert_within(got, want, tol, f"{lens} {new}")
+    if weighted:
+        add = add + w0.cpu().numpy()
+        rmax = float(r.max()) if r.size else 0.0
+        _assert_within(w.cpu().numpy(), add, 2 * rmax * add + (m * hq + 4) * 2.0**-24 * add + 1e-30, "weights")
+    return q, out
+
+
+CACHED = [
+    ([0], [1], 4, 1, 128), ([1022], [1], 20, 5, 128), ([63, 64, 65, 0], [1] * 4, 8, 8, 64), ([300, 5, 700], [1, 1, 1], 16, 2, 128),
+    ([100, 90], [1, 1], 7, 1, 64), ([64, 200, 10], [4, 1, 7], 20, 5, 128), ([130, 0, 77], [2, 30, 0], 6, 2, 64), ([0], [150], 4, 1, 128),
+    ([4000], [1], 4, 4, 128), ([10, -1, 500, -1], [1] * 4, 8, 2, 128), ([33, -3, 60], [3, 2, 1], 12, 4, 64), ([190], [5], 40, 2, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("lens,new,hq,hkv,d", CACHED)
+def test_cached_against_the_definition(bl, lens, new, hq, hkv, d, weighted, dtype):
+    c = _Paged(bl, lens, new, hkv, d, 77)
+    _check_cached(bl, c, lens, new, hq, dtype, weighted, 5)
+    if all(n == 1 for n in new):
+        _check_cached(bl, c, lens, new, hq, dtype, weighted, 5, packed=False)
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_cached_wide_table_of_short_sequences(bl, weighted):
+    """A table for long contexts, nearly empty: the split over blocks follows the lengths, not the table."""
+    lens, new = [70, 3, 0, 900], [1, 1, 1, 1]
+    c = _Paged(bl, lens, new, 2, 128, 3, wide=1500)
+    _check_cached(bl, c, lens, new, 8, "bf16", weighted, 9, packed=False)
+
+
+def test_cached_many_sequences(bl):
+    lens = [(37 * i) % 300 for i in range(150)]
+    new = [i % 3 for i in range(150)]
+    c = _Paged(bl, lens, new, 1, 64, 4)
+    _check_cached(bl, c, lens, new, 4, "f32", True, 2)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 4.0])
+def test_cached_scales(bl, scale):
+    c = _Paged(bl, [500], [2], 2, 64, 4)
+    _check_cached(bl, c, [500], [2], 8, "f32", True, 2, scale=scale)
+
+
+def test_cached_stale_codes_behind_the_last_token(bl):
+    """What stands in a page behind the last token does not enter."""
+    c = _Paged(bl, [70], [1], 1, 128, 4)
+    q = _rand((1, 4, 128), 1, torch.bfloat16)
+    before = bl.attention_cached(q, c.cache, _i32(c.table), _i32([70]))
+    page = int(c.table[0, 1])
+    tok = ref.code_places(128)
+    for codes, place in ((c.cache.k, tok[0]), (c.cache.v, tok[1])):
+        flat = codes[page, 0]
+        flat[torch.tensor(place[7:].ravel(), device="cuda")] = 127
+    after = bl.attention_cached(q, c.cache, _i32(c.table), _i32([70]))
+    assert torch.equal(before, after)
+
+
+def test_cached_rows_that_are_not_finite(bl):
+    c = _Paged(bl, [300], [3], 2, 64, 4)
+    q = _rand((3, 8, 64), 1, torch.float32)
+    w = torch.zeros((1, c.wide), device="cuda")
+    clean = bl.attention_cached(q, c.cache, _i32(c.table), _i32([300]), _starts([3]), weights=w).view(3, 8, 64)
+    q[1, 2, 5], q[2, 7, 63] = float("nan"), float("inf")
+    w2 = torch.zeros_like(w)
+    out = bl.attention_cached(q, c.cache, _i32(c.table), _i32([300]), _starts([3]), weights=w2).view(3, 8, 64)
+    bad = torch.zeros(3, 8, dtype=torch.bool, device="cuda")
+    bad[1, 2] = bad[2, 7] = True
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean[~bad])
+    assert abs(float(w.sum()) - 24) < 1e-3 and abs(float(w2.sum()) - 22) < 1e-3
+
+
+def test_cached_offsets_past_32_bits(bl):
+    """A page whose codes begin past 2^31 bytes and elements."""
+    hkv, d = 8, 128
+    pages = 2**31 // (hkv * 64 * d) + 40
+    cache = bl.cache_alloc(pages, hkv, d)
+    c = _Paged(bl, [100], [1], hkv, d, 6)
+    far = pages - 1 - np.arange(c.pages)
+    idx = torch.tensor(far, device="cuda")
+    for big, small in zip(cache, c.cache):
+        big[idx] = small
+    table = np.where(c.table >= 0, far[np.maximum(c.table, 0)], -1)
+    q = _rand((1, 16, d), 1, torch.float32)
+    near = bl.attention_cached(q, c.cache, _i32(c.table), _i32([100]))
+    assert torch.equal(near, bl.attention_cached(q, cache, _i32(table), _i32([100])))
+    k = _rand((1, hkv, d), 2, torch.float32)
+    bl.cache_append(cache, k, k, _i32(table), _i32([101]))
+    bl.cache_append(c.cache, k, k, _i32(c.table), _i32([101]))
+    for big, small in zip(cache, c.cache):
+        assert torch.equal(big[idx], small)
+
+
+# ---------------------------------------------------------------- eviction
+
+EVICTS = [(3, 6, 3, 0, 1), (5, 20, 7, 1, 2), (4, 20, 20, 0, 1), (2, 64, 3, 1, 2), (3, 1100, 400, 4, 8), (2, 2500, 2499, 0, 1), (1, 1, 1, 0, 1), (70, 33, 9, 2, 3)]
+
+
+@pytest.mark.parametrize("kind", ["spread", "equal", "signs"])
+@pytest.mark.parametrize("seqs,wide,keep,first,recent", EVICTS)
+def test_evict_against_the_definition(bl, seqs, wide, keep, first, recent, kind):
+    rng = np.random.default_rng(wide + keep)
+    table = rng.permutation(seqs * wide).reshape(seqs, wide).astype(np.int32)
+    lens = rng.integers(0, wide * 64 + 1, seqs).astype(np.int32)
+    lens[0] = wide * 64
+    if seqs > 2:
+        lens[1], lens[2] = 0, -1
+    w = (rng.random((seqs, wide)) ** 6 * 50).astype(np.float32)
+    if kind == "equal":
+        w = np.round(w * 0.05).astype(np.float32)
+    if kind == "signs":
+        w = (w - 3).astype(np.float32)
+        w.ravel()[::5] = 0.0
+        w.ravel()[2::5] = -0.0
+        w.ravel()[3::11], w.ravel()[4::13], w.ravel()[6::17] = np.nan, np.inf, -np.inf
+    got = bl.cache_evict(_i32(table), _i32(lens), torch.tensor(w).cuda(), keep, first=first, recent=recent)
+    want = ref.cache_evict(table, lens, w, keep, first, recent)
+    for g, x, name in zip(got, want, ("table", "lens", "weights", "evicted", "count")):
+        np.testing.assert_array_equal(g.cpu().numpy(), x, err_msg=name)
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_layer_from_prompt_to_eviction(bl, dtype):
+    """The QKV projection, the prompt's attention, its K and V appended, the output projection; then decode
+    steps over the cache, eviction, and a step over what is left."""
+    import synth
+    hidden, hq, hkv, d = 256, 8, 2, 64
+    wide = (hq + 2 * hkv) * d
+    qkv_w, qkv_g = bl.pack_weights(torch.from_numpy(synth.weights(31, "qkv", wide, hidden)).cuda())
+    o_w, o_g = bl.pack_weights(torch.from_numpy(synth.weights(31, "o", hidden, hq * d)).cuda())
+    lens = [150, 70]
+    cache = bl.cache_alloc(12, hkv, d)
+    table = _i32([[3, 1, 7, 5], [2, 9, 0, 11]])
+
+    def project(x):
+        y = bl.forward(x, qkv_w, qkv_g).to(DTYPES[dtype])
+        return (t.unflatten(1, (-1, d)) for t in y.split([hq * d, hkv * d, hkv * d], 1))
+
+    x = _rand((220, hidden), 3, torch.float32)
+    q, k, v = project(x)
+    out = bl.attention(q, k, v, _starts(lens))
+    want, spread, reach = ref.attention(_np(q), _np(k), _np(v), [0, 150, 220], d ** -0.5)
+    _assert_within(_np(out).reshape(220, hq, d), want, _prompt_tolerance(want, spread, reach, 150, d, dtype))
+    assert bl.forward(out, o_w, o_g).shape == (220, hidden)
+
+    have = torch.zeros(2, dtype=torch.int32, device="cuda")
+    bl.cache_append(cache, k, v, table, have, _starts(lens))
+    have += _i32(lens)
+    place = ref.code_places(d)
+    weights = torch.zeros((2, 4), device="cuda")
+    total = np.zeros((2, 4))
+    for step in range(3):
+        q, k, v = project(_rand((2, hidden), 50 + step, torch.float32))
+        bl.cache_append(cache, k, v, table, have)
+        out = bl.attention_cached(q, cache, table, have, weights=weights)
+        host = [ref.natural(c.cpu().numpy(), p) for c, p in ((cache.k, place[0]), (cache.v, place[1]))]
+        args = (host[0], cache.k_scale.cpu().numpy(), host[1], cache.v_scale.cpu().numpy())
+        want, add, spread, reach, grain = ref.attention_cached(_np(q), *args, table.cpu().numpy(), have.tolist(), None, d ** -0.5)
+        tol = 2 * (32 * 2.0**-24 * reach + 100 * 2.0**-24) * spread + 2.0**-22 * grain + (2.0**-8 if dtype == "bf16" else 2.0**-24) * np.abs(want)
+        _assert_within(_np(out).reshape(2, hq, d), want, tol)
+        total += add
+        have += 1
+    np.testing.assert_allclose(weights.cpu().numpy(), total, rtol=1e-4)
+    table2, have2, weights2, gone, count = bl.cache_evict(table, have, weights, 2, recent=1)
+    ref_evict = ref.cache_evict(table.cpu().numpy(), have.cpu().numpy(), weights.cpu().numpy(), 2, 0, 1)
+    assert torch.equal(table2.cpu(), torch.tensor(ref_evict[0])) and count.tolist() == [1, 0]
+    q, k, v = project(_rand((2, hidden), 70, torch.float32))
+    bl.cache_append(cache, k, v, table2, have2)
+    out = bl.attention_cached(q, cache, table2, have2, weights=weights2)
+    host = [ref.natural(c.cpu().numpy(), p) for c, p in ((cache.k, place[0]), (cache.v, place[1]))]
+    want, *_ = ref.attention_cached(_np(q), host[0], cache.k_scale.cpu().numpy(), host[1], cache.v_scale.cpu().numpy(),
+                                    table2.cpu().numpy(), have2.tolist(), None, d ** -0.5)
+    np.testing.assert_allclose(_np(out).reshape(2, hq, d), want, rtol=2.0**-7 if dtype == "bf16" else 1e-4, atol=1e-4)
+
+
+def test_captured_calls_follow_their_inputs(bl):
+    """Append, attention (split and joined) with weights, prompt attention and eviction in one graph; each replay, on
+    new inputs and with eager calls between, gives what eager calls give."""
+    hq, hkv, d, seqs = 8, 2, 128, 3
+    base = _Paged(bl, [500, 20, 130], [8] * 3, hkv, d, 8)
+    q, k, v = (torch.zeros((seqs, h, d), dtype=torch.bfloat16, device="cuda") for h in (hq, hkv, hkv))
+    lens, cu = _i32([500, 20, 130]), _i32([0, 1, 3])
+    table = _i32(base.table)
+
+    def fresh():
+        return type(base.cache)(*[t.clone() for t in base.cache]), torch.zeros((seqs, base.wide), device="cuda")
+
+    def step(cache, w):
+        bl.cache_append(cache, k, v, table, lens)
+        a = bl.attention_cached(q, cache, table, lens, weights=w)
+        b = bl.attention(q, k, v, cu)
+        return (a, b, *bl.cache_evict(table, lens, w, 3))
+
+    cache, w = fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(cache, w)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = step(cache, w)
+    for t, s in zip(cache, base.cache):
+        t.copy_(s)
+    w.zero_()
+    mirror, mw = fresh()
+    for i in range(4):
+        for t in (q, k, v):
+            t.copy_(_rand(t.shape, 100 + i, torch.bfloat16))
+        lens.copy_(_i32([500 + i, 20 + i, 130 - 40 * i]))
+        cu.copy_(_i32([0, i % 4, 3]))
+        g.replay()
+        torch.cuda.synchronize()
+        want = step(mirror, mw)
+        for n, (x, y) in enumerate(zip(captured, want)):
+            assert torch.equal(x, y), (i, n)
+        assert all(torch.equal(x, y) for x, y in zip(cache, mirror)) and torch.equal(w, mw)
+
+
+def test_another_stream(bl):
+    """Calls on a stream of their own, twice at once, give what they give alone."""
+    lens = [900, 333]
+    c = _Paged(bl, lens, [1, 1], 2, 128, 8)
+    q = [_rand((2, 8, 128), i, torch.bfloat16) for i in range(2)]
+    alone = [bl.attention_cached(x, c.cache, _i32(c.table), _i32(lens)) for x in q]
+    p = _rand((300, 12, 64), 5, torch.bfloat16)
+    prompt = bl.attention(p[:, :8], p[:, 8:10], p[:, 10:], _starts([300]))
+    table, have, cu = _i32(c.table), _i32(lens), _starts([300])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(5):
+        for s, x in zip(streams, q):
+            with torch.cuda.stream(s):
+                outs.append((bl.attention_cached(x, c.cache, table, have), bl.attention(p[:, :8], p[:, 8:10], p[:, 10:], cu)))
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(outs):
+        assert torch.equal(a, alone[i % 2]) and torch.equal(b, prompt)
