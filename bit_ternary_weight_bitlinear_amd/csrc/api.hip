@@ -200,6 +200,12 @@ bool heads_ok(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
     return tokens_ok(m) && kv_heads >= 1 && q_heads >= 1 && q_heads <= BL_MAX_HEADS && kv_heads <= q_heads &&
            q_heads % kv_heads == 0 && (head_dim == 64 || head_dim == 128);
 }
+// rows of a kv head and workgroups of a prompt call, counted in 32 bits on the device
+bool prompt_ok(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t seqs)
+{
+    const int64_t rows = m * (q_heads / kv_heads);
+    return rows <= INT32_MAX - 1024 && (rows / 64 + seqs) * kv_heads <= INT32_MAX;
+}
 bool seqs_ok(int64_t seqs) { return seqs >= 1 && seqs <= BL_MAX_TOKENS; }
 bool cache_ok(int64_t max_blocks, int64_t pages)
 {
@@ -211,7 +217,7 @@ bool finite(float v) { return v - v == 0.0f; }
 bl_status rows_ok(const void *p, int64_t stride, int64_t width, bl_dtype dtype)
 {
     const int64_t per16 = dtype == BL_BF16 ? 8 : 4;
-    if (stride < width || stride > INT32_MAX) return BL_ERR_SHAPE;
+    if (stride < width || stride > ((int64_t)1 << 24)) return BL_ERR_SHAPE;
     if (!aligned16(p) || stride % per16 != 0) return BL_ERR_ALIGN;
     return BL_OK;
 }
@@ -615,7 +621,9 @@ bl_status bitlinear_ffn(const void *x, bl_dtype dtype, int64_t m, int64_t hidden
 size_t bitlinear_attention_workspace_size(bl_dtype dtype, int64_t m, int64_t q_heads, int64_t kv_heads,
                                           int64_t head_dim, int64_t seqs)
 {
-    if ((dtype != BL_F32 && dtype != BL_BF16) || !heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs)) return 0;
+    if ((dtype != BL_F32 && dtype != BL_BF16) || !heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs) ||
+        !prompt_ok(m, q_heads, kv_heads, seqs))
+        return 0;
     AttentionProblem p{};
     p.bf16 = dtype == BL_BF16; p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads; p.head_dim = head_dim;
     p.seqs = seqs;
@@ -629,7 +637,8 @@ bl_status bitlinear_attention(const void *q, int64_t q_stride, const void *k, in
 {
     if (!q || !k || !v || !cu_seqlens || !out) return BL_ERR_NULL;
     if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
-    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs)) return BL_ERR_SHAPE;
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs) || !prompt_ok(m, q_heads, kv_heads, seqs))
+        return BL_ERR_SHAPE;
     if (!finite(scale)) return BL_ERR_VALUE;
     if (const bl_status s = rows_ok(q, q_stride, q_heads * head_dim, dtype)) return s;
     if (const bl_status s = rows_ok(k, k_stride, kv_heads * head_dim, dtype)) return s;

@@ -45,18 +45,304 @@ __global__ __launch_bounds__(64) void attention_kernel(AttentionProblem a)
     for (int e = 0; e < E; ++e) store_out(static_cast<T *>(a.out) + (row * a.q_heads + head) * D + e * 64 + lane, o[e] / l);
 }
 
+// ---------------------------------------------------------------- bf16 on the matrix cores
+//
+// A workgroup of 4 waves takes 128 * QT query rows of one kv head: row r of a
+// sequence is token r / group, query head r % group, so the heads that share K
+// and V share their tiles and short prompts fill a tile. Each wave has QT column
+// tiles of 32 rows and everything of a row in one lane pair:
+//   S^T = K Q^T      (v_mfma_f32_32x32x16_bf16, A = 32 keys, B = 32 query rows)
+//   O^T = V^T P^T    (A = 32 dims of V read transposed from LDS, B = P)
+// The result's column is lane % 32, so maximum, sum and rescaling are per lane,
+// joined with lane ^ 32 alone; and S^T's registers are P^T's operand as they lie
+// when V's keys are taken in the order 4h .. 4h+3, 8+4h .. 8+4h+3 (h = lane / 32)
+// of every 16: P never leaves the registers.
+// K and V tiles of 64 keys come by direct loads into two LDS buffers, one barrier
+// per tile. 16-byte chunks are permuted within a row by the global address, so
+// that the operand reads touch every bank once.
+constexpr int kKeys = 64;
+
+template <int D>
+__device__ inline int k_swizzle(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
+template <int D>
+__device__ inline int v_swizzle(int row) { return D == 128 ? (row & 3) << 2 : (row & 2) << 1; }
+
+// value of both halves of the wave: (lower, upper)
+__device__ inline void both_halves(float v, float &lower, float &upper)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    lower = __uint_as_float(r[0]);
+    upper = __uint_as_float(r[1]);
+}
+
+// Rescaling is put off until a maximum has grown by 2^kSlack: p stays below that,
+// which neither bf16 nor the fp32 sums notice.
+constexpr float kSlack = 8.0f;
+
+// Where a tile's mask leaves out keys, 0 * v must not bring a NaN or infinity of
+// theirs into the sum. Every such tile is looked through (128 of ~1500
+// instructions of one or two tiles per wave), and the rare one that holds a value
+// that is not finite takes part with zeros in such places. A second product then
+// counts, per dim and row, what stood there in the keys that the row sees: +inf as
+// 1, -inf as 2^7, NaN as 2^14 (at most 64 of each, so fp32 holds all three).
+template <int BYTES>
+__device__ inline bool holds_non_finite(const char *tile)
+{
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int i = 0; i < BYTES / 1024; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(tile + i * 1024 + (threadIdx.x & 63) * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t v = (&w.x)[j] & 0x7FFF7FFFu;
+            hi = v > hi ? v : hi;
+            lo = (v << 16) > lo ? v << 16 : lo;
+        }
+    }
+    return __any(hi >= 0x7F800000u || lo >= 0x7F800000u);
+}
+
+__device__ inline uint32_t finite_pair(uint32_t w)
+{
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    if ((w & 0x00007F80u) == 0x00007F80u) w &= 0xFFFF0000u;
+    return w;
+}
+__device__ inline uint32_t counted(uint32_t b)  // of bf16 bits, as bf16 bits
+{
+    return (b & 0x7F80u) != 0x7F80u ? 0u : b & 0x7Fu ? 0x4680u : b & 0x8000u ? 0x4300u : 0x3F80u;
+}
+__device__ inline uint32_t counted_pair(uint32_t w) { return counted(w & 0xFFFFu) | counted(w >> 16) << 16; }
+__device__ inline float counted_value(float n)
+{
+    const int c = (int)n, plus = c & 127, minus = (c >> 7) & 127;
+    return c >= 1 << 14 || (plus && minus) ? __builtin_nanf("") : plus ? __builtin_inff() : minus ? kNegInf : 0.0f;
+}
+
+template <int D, int QT>
+__global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(AttentionProblem a, int group)
+{
+    constexpr int ROWS = 128 * QT, C = D / 16, DT = D / 32;
+    constexpr int kTile = kKeys * D * 2;                  // bytes of a K or V tile
+    constexpr int kLoads = 2 * kTile / (1024 * 4);        // direct loads per wave and step
+    constexpr int kChunks = D / 8;                        // 16-byte chunks per row
+    __shared__ __align__(1024) char lds[2][2][kTile];
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
+    const int head = blockIdx.x % (int)a.kv_heads;
+    SeqTile t;
+    const int rows_per = ROWS;
+    if (!find_tile(a.cu, (int)a.seqs, a.m, blockIdx.x / (int)a.kv_heads,
+                   [=](int, int n) { return (int)(((int64_t)n * group + rows_per - 1) / rows_per); }, t))
+        return;
+    const int rows = t.n * group;
+    t.tile = (rows + ROWS - 1) / ROWS - 1 - t.tile;       // the longest rows first
+    const int r_wave = t.tile * ROWS + wave * 32 * QT;
+
+    // query rows (rows past the last one repeat it and are not stored)
+    const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    int tok[QT];
+    v8bf qf[QT][C];
+#pragma unroll
+    for (int u = 0; u < QT; ++u) {
+        int r = r_wave + 32 * u + col;
+        r = r < rows ? r : rows - 1;
+        tok[u] = r / group;
+        const bf16_t *src = static_cast<const bf16_t *>(a.q) + (t.begin + tok[u]) * a.q_stride +
+                            (int64_t)(head * group + r % group) * D + 8 * h;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            uint4 w = *reinterpret_cast<const uint4 *>(src + 16 * i);
+            w = make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
+            qf[u][i] = __builtin_bit_cast(v8bf, w);
+        }
+    }
+    const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
+    const int tiles = last_row / group / kKeys + 1;
+    int wave_last = r_wave + 32 * QT - 1;
+    wave_last = (wave_last < rows ? wave_last : rows - 1) / group;
+    const int wave_first = (r_wave < rows ? r_wave : rows - 1) / group;
+
+    // direct loads: load i of wave w brings rows of tile K (i < kLoads / 2) or V
+    const uint32_t base = lds_addr(&lds[0][0][0]);
+    auto request = [&](int tile, int buf) {
+        const int64_t first = t.begin + (int64_t)tile * kKeys;
+        const int left = t.n - 1 - tile * kKeys;
+        const bf16_t *kb = static_cast<const bf16_t *>(a.k) + first * a.k_stride + (int64_t)head * D;
+        const bf16_t *vb = static_cast<const bf16_t *>(a.v) + first * a.v_stride + (int64_t)head * D;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const bool is_v = i >= kLoads / 2;
+            const int piece = (is_v ? i - kLoads / 2 : i) * 4 + wave;      // 1 KB pieces of the tile
+            const int row = piece * (1024 / (D * 2)) + lane / kChunks;
+            const int chunk = (lane % kChunks) ^ (is_v ? v_swizzle<D>(row) : k_swizzle<D>(row));
+            const int64_t stride = is_v ? a.v_stride : a.k_stride;
+            const uint32_t off = (uint32_t)(row < left ? row : left) * (uint32_t)(stride * 2) + chunk * 16;
+            dma16(is_v ? vb : kb, off, base + (buf * 2 + is_v) * kTile + piece * 1024);
+        }
+    };
+
+    v16f o[QT][DT];
+    float mx[QT], sum[QT];
+#pragma unroll
+    for (int u = 0; u < QT; ++u) {
+        mx[u] = kNegInf;
+        sum[u] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) o[u][i] = v16f{};
+    }
+
+    request(0, 0);
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int buf = tile & 1;
+        ring_barrier<0>();
+        if (tile + 1 < tiles) request(tile + 1, buf ^ 1);
+        if (tile * kKeys > wave_last) continue;
+        const char *kt = lds[buf][0], *vt = lds[buf][1];
+
+        v16f s[QT][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int u = 0; u < QT; ++u) s[u][b] = v16f{};
+            const int row = 32 * b + col;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const v8bf kf = *reinterpret_cast<const v8bf *>(kt + row * (D * 2) + (((2 * i + h) ^ k_swizzle<D>(row)) << 4));
+#pragma unroll
+                for (int u = 0; u < QT; ++u) s[u][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[u][i], s[u][b], 0, 0, 0);
+            }
+        }
+        const bool masked = tile * kKeys + kKeys - 1 > wave_first;
+        if (masked) {
+#pragma unroll
+            for (int u = 0; u < QT; ++u)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int key = tile * kKeys + 32 * b + 8 * (i >> 2) + 4 * h + (i & 3);
+                        s[u][b][i] = key <= tok[u] ? s[u][b][i] : kNegInf;
+                    }
+        }
+        v8bf pf[QT][4];
+#pragma unroll
+        for (int u = 0; u < QT; ++u) {
+            float big = kNegInf;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) big = fmaxf(big, s[u][b][i]);
+            float lo, up;
+            both_halves(big, lo, up);
+            big = fmaxf(lo, up) * c;
+            if (__any(big > mx[u] + kSlack)) {
+                // only where it has grown: a row's result does not depend on its neighbours
+                const float now = big > mx[u] + kSlack ? big : mx[u];
+                const float keep = now == mx[u] ? 1.0f : __builtin_amdgcn_exp2f(mx[u] - now);
+                mx[u] = now;
+                sum[u] *= keep;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[u][d][i] *= keep;
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][b][i], c, -mx[u]));
+                    sum[u] += p;
+                    pf[u][2 * b + (i >> 3)][i & 7] = (__bf16)p;
+                }
+        }
+        // 16 lanes read 4 keys x 16 dims and get 4 keys of one dim each
+        auto v_fragment = [&](int kc, int d) {
+            v4s part[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int key = 16 * kc + 8 * e + 4 * h + ((lane & 15) >> 2);
+                const int chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+                const char *at = vt + key * (D * 2) + ((chunk ^ v_swizzle<D>(key)) << 4) + (lane & 1) * 8;
+                part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) v4s *)(uintptr_t)lds_addr(at));
+            }
+            return __builtin_bit_cast(uint4, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        if (!masked || !holds_non_finite<kTile>(vt)) {
+#pragma unroll
+            for (int kc = 0; kc < 4; ++kc)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const v8bf vf = __builtin_bit_cast(v8bf, v_fragment(kc, d));
+#pragma unroll
+                    for (int u = 0; u < QT; ++u)
+                        o[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u][kc], o[u][d], 0, 0, 0);
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < QT; ++u)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    v16f count = {};
+#pragma unroll
+                    for (int kc = 0; kc < 4; ++kc) {
+                        const uint4 w = v_fragment(kc, d);
+                        const v8bf vf = __builtin_bit_cast(
+                            v8bf, make_uint4(finite_pair(w.x), finite_pair(w.y), finite_pair(w.z), finite_pair(w.w)));
+                        o[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u][kc], o[u][d], 0, 0, 0);
+                        const v8bf nf = __builtin_bit_cast(
+                            v8bf, make_uint4(counted_pair(w.x), counted_pair(w.y), counted_pair(w.z), counted_pair(w.w)));
+                        v8bf seen;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            seen[i] = (__bf16)(tile * kKeys + 16 * kc + 8 * (i >> 2) + 4 * h + (i & 3) <= tok[u] ? 1.0f : 0.0f);
+                        count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(nf, seen, count, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[u][d][i] += counted_value(count[i]);
+                }
+        }
+    }
+
+#pragma unroll
+    for (int u = 0; u < QT; ++u) {
+        float lo, up;
+        both_halves(sum[u], lo, up);
+        const float inv = 1.0f / (lo + up);
+        const int r = r_wave + 32 * u + col;
+        if (r >= rows) continue;
+        bf16_t *dst = static_cast<bf16_t *>(a.out) + ((t.begin + tok[u]) * a.q_heads + head * group + r % group) * D + 4 * h;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                bf16_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) store_out(&w[i], o[u][d][4 * g + i] * inv);
+                *reinterpret_cast<uint2 *>(dst + 32 * d + 8 * g) = *reinterpret_cast<const uint2 *>(w);
+            }
+    }
+}
+
 int64_t attention_workspace(const AttentionProblem &) { return 0; }
 
 hipError_t launch_attention(const AttentionProblem &p, void *, hipStream_t st)
 {
+    const int group = (int)(p.q_heads / p.kv_heads);
+    if (p.bf16) {
+        auto go = [&](auto width, auto tiles) {
+            constexpr int D = decltype(width)::value, QT = decltype(tiles)::value;
+            const int64_t n = p.m * group / (128 * QT) + p.seqs;
+            hipLaunchKernelGGL((attention_bf16_kernel<D, QT>), dim3((unsigned)(n * p.kv_heads)), dim3(256), 0, st, p, group);
+        };
+        p.head_dim == 128 ? go(Width<128>{}, Width<1>{}) : go(Width<64>{}, Width<1>{});
+        return hipGetLastError();
+    }
     const dim3 grid((unsigned)p.m, (unsigned)p.q_heads);
-    auto go = [&](auto type, auto width) {
-        using T = decltype(type);
-        constexpr int D = decltype(width)::value;
-        hipLaunchKernelGGL((attention_kernel<T, D>), grid, dim3(64), 0, st, p);
-    };
-    if (p.bf16) p.head_dim == 128 ? go(bf16_t{}, Width<128>{}) : go(bf16_t{}, Width<64>{});
-    else p.head_dim == 128 ? go(float{}, Width<128>{}) : go(float{}, Width<64>{});
+    if (p.head_dim == 128) hipLaunchKernelGGL((attention_kernel<float, 128>), grid, dim3(64), 0, st, p);
+    else hipLaunchKernelGGL((attention_kernel<float, 64>), grid, dim3(64), 0, st, p);
     return hipGetLastError();
 }
 

@@ -106,7 +106,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArg
     const int chunk = pages_per_split(npages, a.splits);
     const int p0 = split * chunk, p1 = p0 + chunk < npages ? p0 + chunk : npages;
     if (p0 >= npages && split > 0) return;  // the join knows; split 0 writes rows that see nothing
-    const int rows = t.n * a.group;
+    const int64_t rows = (int64_t)t.n * a.group;
 
     // ---- query rows as digits. Lane (j, c) builds row c of the operand: digit
     // c % 4 of query row c / 4, dims 16*j .. 16*j+15 of every 64.
@@ -116,9 +116,9 @@ __global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArg
     bool poor[RT];         // query row j is not finite
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int r = t.tile * R + 4 * rt + (c >> 2);
+        const int64_t r = (int64_t)t.tile * R + 4 * rt + (c >> 2);
         const bool there = r < rows;
-        const int tok = there ? r / a.group : 0, hq = head * a.group + (there ? r % a.group : 0);
+        const int tok = there ? (int)(r / a.group) : 0, hq = head * a.group + (there ? (int)(r % a.group) : 0);
         const T *src = static_cast<const T *>(a.q) + (t.begin + tok) * a.q_stride + (int64_t)hq * D + 16 * j;
         float x[H][16];
         float big = 0.0f;
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArg
         // the result's lane (j, c) has query row j: that is operand row 4j of lane 4j
         const float big_j = __shfl(big, 4 * j);
         qs[rt] = (big_j / kDigitMax) * a.scale;
-        const int rj = t.tile * R + 4 * rt + j;
+        const int64_t rj = (int64_t)t.tile * R + 4 * rt + j;
         limit[rt] = rj < rows ? have + rj / a.group : -1;
         poor[rt] = (bad & (0x000F000F000F000Full << (4 * j))) != 0;
     }
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArg
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
             if (STAT && c == 0) {
-                const int rj = t.tile * R + 4 * rt + j;
+                const int64_t rj = (int64_t)t.tile * R + 4 * rt + j;
                 if (rj < rows) {
                     const int64_t row = (t.begin + rj / a.group) * a.q_heads + head * a.group + rj % a.group;
                     reinterpret_cast<float2 *>(a.stat)[row * a.max_blocks + p] = make_float2(big, poor[rt] ? 0.0f : total);
@@ -271,7 +271,8 @@ __global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArg
     __syncthreads();
     const int64_t total_rows = a.m * a.q_heads;
     for (int it = tid; it < R * D; it += 64 * kWaves) {
-        const int r = it / D, dim = it % D, rj = t.tile * R + r;
+        const int r = it / D, dim = it % D;
+        const int64_t rj = (int64_t)t.tile * R + r;
         if (rj >= rows) break;
         float top = kNegInf;
 #pragma unroll

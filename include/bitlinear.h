@@ -324,7 +324,7 @@ bl_status bitlinear_gemm_i32(const int8_t *q, int64_t m, int64_t k,
  * Attention between the QKV and the output projection. The projections' fused
  * output is read in place: q, k and v are [m][heads][head_dim] with the heads of
  * a token adjacent and `*_stride` elements from one token to the next (a
- * multiple of 16 bytes, at least heads * head_dim). head_dim is 64 or 128;
+ * multiple of 16 bytes, heads * head_dim to 2^24). head_dim is 64 or 128;
  * q_heads is a multiple of kv_heads, and query head h reads kv head
  * h / (q_heads / kv_heads).
  *
@@ -349,7 +349,9 @@ size_t bitlinear_attention_workspace_size(bl_dtype dtype, int64_t m, int64_t q_h
  * BL_BF16: products of the bf16 inputs summed in fp32, softmax in fp32, p
  * rounded to bf16 for its product with v. BL_F32: as fp32 throughout.
  * A row depends on rows 0..i of its own sequence only: infinities and NaN in
- * later rows or in other sequences do not reach it.
+ * later rows or in other sequences do not reach it. BL_ERR_SHAPE also where
+ * m * q_heads / kv_heads, or its 64th part (plus seqs) times kv_heads, passes
+ * 2^31 - 1024.
  *   workspace  >= bitlinear_attention_workspace_size() bytes
  */
 bl_status bitlinear_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
