@@ -80,28 +80,12 @@ __device__ inline void both_halves(float v, float &lower, float &upper)
 constexpr float kSlack = 8.0f;
 
 // Where a tile's mask leaves out keys, 0 * v must not bring a NaN or infinity of
-// theirs into the sum. Every such tile is looked through (128 of ~1500
-// instructions of one or two tiles per wave), and the rare one that holds a value
-// that is not finite takes part with zeros in such places. A second product then
-// counts, per dim and row, what stood there in the keys that the row sees: +inf as
-// 1, -inf as 2^7, NaN as 2^14 (at most 64 of each, so fp32 holds all three).
-template <int BYTES>
-__device__ inline bool holds_non_finite(const char *tile)
-{
-    uint32_t hi = 0, lo = 0;
-#pragma unroll
-    for (int i = 0; i < BYTES / 1024; ++i) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(tile + i * 1024 + (threadIdx.x & 63) * 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t v = (&w.x)[j] & 0x7FFF7FFFu;
-            hi = v > hi ? v : hi;
-            lo = (v << 16) > lo ? v << 16 : lo;
-        }
-    }
-    return __any(hi >= 0x7F800000u || lo >= 0x7F800000u);
-}
-
+// theirs into the sum. The workgroup looks through such a tile of V (the last one
+// or two) when it has arrived; what is not finite becomes 0 there, and a second
+// tile holds what it was: +inf as 1, -inf as 2^7, NaN as 2^14. A product of that
+// tile with the mask counts per dim and row what the row sees (at most 64 of each,
+// so fp32 holds all three counts).
+__device__ inline bool not_finite_pair(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u; }
 __device__ inline uint32_t finite_pair(uint32_t w)
 {
     if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
@@ -124,16 +108,18 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
 {
     constexpr int ROWS = 128 * QT, C = D / 16, DT = D / 32;
     constexpr int kTile = kKeys * D * 2;                  // bytes of a K or V tile
-    constexpr int kLoads = 2 * kTile / (1024 * 4);        // direct loads per wave and step
+    constexpr int kLoads = kTile / (1024 * 4);            // direct loads per wave and tile
     constexpr int kChunks = D / 8;                        // 16-byte chunks per row
-    __shared__ __align__(1024) char lds[2][2][kTile];
+    constexpr int kLoadRows = kKeys / kLoads;             // rows that one load of the four waves brings
+    // K, K, V, V, counts of what is not finite
+    __shared__ __align__(1024) char lds[5 * kTile];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = lane >> 5, col = lane & 31;
     const int head = blockIdx.x % (int)a.kv_heads;
     SeqTile t;
-    const int rows_per = ROWS;
     if (!find_tile(a.cu, (int)a.seqs, a.m, blockIdx.x / (int)a.kv_heads,
-                   [=](int, int n) { return (int)(((int64_t)n * group + rows_per - 1) / rows_per); }, t))
+                   [=](int, int n) { return (int)(((int64_t)n * group + ROWS - 1) / ROWS); }, t))
         return;
     const int rows = t.n * group;
     t.tile = (rows + ROWS - 1) / ROWS - 1 - t.tile;       // the longest rows first
@@ -160,27 +146,56 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
     }
     const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
     const int tiles = last_row / group / kKeys + 1;
-    int wave_last = r_wave + 32 * QT - 1;
-    wave_last = (wave_last < rows ? wave_last : rows - 1) / group;
-    const int wave_first = (r_wave < rows ? r_wave : rows - 1) / group;
+    // first tile that some row of the workgroup, of the wave, does not see whole
+    const int group_masked = (t.tile * ROWS / group + 1) / kKeys;
+    const int wave_masked = ((r_wave < rows ? r_wave : rows - 1) / group + 1) / kKeys;
 
-    // direct loads: load i of wave w brings rows of tile K (i < kLoads / 2) or V
-    const uint32_t base = lds_addr(&lds[0][0][0]);
-    auto request = [&](int tile, int buf) {
+    // direct loads: load i of wave w brings rows kLoadRows*i + (16 or 32 B per ...)
+    const uint32_t base = lds_addr(lds);
+    const int load_row = wave * (kLoadRows / 4) + lane / kChunks;
+    const int k_chunk = ((lane % kChunks) ^ k_swizzle<D>(load_row)) * 16, v_chunk = ((lane % kChunks) ^ v_swizzle<D>(load_row)) * 16;
+    const uint32_t k_off = (uint32_t)load_row * (uint32_t)(a.k_stride * 2) + k_chunk;
+    const uint32_t v_off = (uint32_t)load_row * (uint32_t)(a.v_stride * 2) + v_chunk;
+    auto bring = [&](const void *x, int64_t stride, uint32_t off, int chunk, int tile, uint32_t to) {
         const int64_t first = t.begin + (int64_t)tile * kKeys;
         const int left = t.n - 1 - tile * kKeys;
-        const bf16_t *kb = static_cast<const bf16_t *>(a.k) + first * a.k_stride + (int64_t)head * D;
-        const bf16_t *vb = static_cast<const bf16_t *>(a.v) + first * a.v_stride + (int64_t)head * D;
+        const bf16_t *from = static_cast<const bf16_t *>(x) + first * stride + (int64_t)head * D;
+        if (left >= kKeys - 1) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const bool is_v = i >= kLoads / 2;
-            const int piece = (is_v ? i - kLoads / 2 : i) * 4 + wave;      // 1 KB pieces of the tile
-            const int row = piece * (1024 / (D * 2)) + lane / kChunks;
-            const int chunk = (lane % kChunks) ^ (is_v ? v_swizzle<D>(row) : k_swizzle<D>(row));
-            const int64_t stride = is_v ? a.v_stride : a.k_stride;
-            const uint32_t off = (uint32_t)(row < left ? row : left) * (uint32_t)(stride * 2) + chunk * 16;
-            dma16(is_v ? vb : kb, off, base + (buf * 2 + is_v) * kTile + piece * 1024);
+            for (int i = 0; i < kLoads; ++i) dma16(from + i * kLoadRows * stride, off, to + (4 * i + wave) * 1024);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int row = i * kLoadRows + load_row;
+                dma16(from, (uint32_t)(row < left ? row : left) * (uint32_t)(stride * 2) + chunk, to + (4 * i + wave) * 1024);
+            }
         }
+    };
+    auto request = [&](int tile) {
+        bring(a.k, a.k_stride, k_off, k_chunk, tile, base + (tile & 1) * kTile);
+        bring(a.v, a.v_stride, v_off, v_chunk, tile, base + (2 + (tile & 1)) * kTile);
+    };
+
+    // operand addresses inside a tile; rows 32 keys further on, and 8 keys for V, are constant offsets
+    int k_at[C], v_at[DT];
+#pragma unroll
+    for (int i = 0; i < C; ++i) k_at[i] = col * (D * 2) + (((2 * i + h) ^ k_swizzle<D>(col)) << 4);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+        const int key = 4 * h + ((lane & 15) >> 2), chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        v_at[d] = key * (D * 2) + ((chunk ^ v_swizzle<D>(key)) << 4) + (lane & 1) * 8;
+    }
+    auto k_fragment = [&](int tile, int b, int i) {
+        return *reinterpret_cast<const v8bf *>(lds + (tile & 1) * kTile + k_at[i] + b * 32 * D * 2);
+    };
+    // 16 lanes read 4 keys x 16 dims and get 4 keys of one dim each
+    auto v_fragment = [&](int place, int kc, int d) {
+        v4s part[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(uintptr_t)(
+                base + place * kTile + v_at[d] + (16 * kc + 8 * e) * D * 2));
+        return __builtin_bit_cast(v8bf, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
 
     v16f o[QT][DT];
@@ -193,29 +208,62 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
         for (int i = 0; i < DT; ++i) o[u][i] = v16f{};
     }
 
-    request(0, 0);
+    // V of a masked tile, once it is there: keeps what is not finite from rows that do not see it
+    auto clean = [&](int tile) {
+        char *vt = lds + (2 + (tile & 1)) * kTile + wave * (kTile / 4) + lane * 16, *ct = lds + 4 * kTile + wave * (kTile / 4) + lane * 16;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kTile / 4096; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
+            bad = bad || not_finite_pair(w.x) || not_finite_pair(w.y) || not_finite_pair(w.z) || not_finite_pair(w.w);
+        }
+        int *flags = reinterpret_cast<int *>(lds + 4 * kTile);
+        bad = __any(bad);
+        if (lane == 0) flags[wave] = bad;
+        __syncthreads();
+        if (!(flags[0] | flags[1] | flags[2] | flags[3])) return;
+        __syncthreads();
+        for (int i = 0; i < kTile / 4096; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
+            *reinterpret_cast<uint4 *>(vt + i * 1024) = make_uint4(finite_pair(w.x), finite_pair(w.y), finite_pair(w.z), finite_pair(w.w));
+            *reinterpret_cast<uint4 *>(ct + i * 1024) = make_uint4(counted_pair(w.x), counted_pair(w.y), counted_pair(w.z), counted_pair(w.w));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < QT; ++u)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                v16f count = {};
+#pragma unroll
+                for (int kc = 0; kc < 4; ++kc) {
+                    v8bf seen;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        seen[i] = (__bf16)(tile * kKeys + 16 * kc + 8 * (i >> 2) + 4 * h + (i & 3) <= tok[u] ? 1.0f : 0.0f);
+                    count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_fragment(4, kc, d), seen, count, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[u][d][i] += counted_value(count[i]);
+            }
+    };
+
+    request(0);
     for (int tile = 0; tile < tiles; ++tile) {
-        const int buf = tile & 1;
         ring_barrier<0>();
-        if (tile + 1 < tiles) request(tile + 1, buf ^ 1);
-        if (tile * kKeys > wave_last) continue;
-        const char *kt = lds[buf][0], *vt = lds[buf][1];
+        if (tile + 1 < tiles) request(tile + 1);
+        if (tile >= group_masked) clean(tile);
 
         v16f s[QT][2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int i = 0; i < C; ++i)
 #pragma unroll
-            for (int u = 0; u < QT; ++u) s[u][b] = v16f{};
-            const int row = 32 * b + col;
+            for (int b = 0; b < 2; ++b) {
+                const v8bf kf = k_fragment(tile, b, i);
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const v8bf kf = *reinterpret_cast<const v8bf *>(kt + row * (D * 2) + (((2 * i + h) ^ k_swizzle<D>(row)) << 4));
-#pragma unroll
-                for (int u = 0; u < QT; ++u) s[u][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[u][i], s[u][b], 0, 0, 0);
+                for (int u = 0; u < QT; ++u)
+                    s[u][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[u][i], i ? s[u][b] : v16f{}, 0, 0, 0);
             }
-        }
-        const bool masked = tile * kKeys + kKeys - 1 > wave_first;
-        if (masked) {
+        if (tile >= wave_masked) {
 #pragma unroll
             for (int u = 0; u < QT; ++u)
 #pragma unroll
@@ -226,7 +274,7 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
                         s[u][b][i] = key <= tok[u] ? s[u][b][i] : kNegInf;
                     }
         }
-        v8bf pf[QT][4];
+        v8bf p[QT][4];
 #pragma unroll
         for (int u = 0; u < QT; ++u) {
             float big = kNegInf;
@@ -252,58 +300,20 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][b][i], c, -mx[u]));
-                    sum[u] += p;
-                    pf[u][2 * b + (i >> 3)][i & 7] = (__bf16)p;
+                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][b][i], c, -mx[u]));
+                    sum[u] += e;
+                    p[u][2 * b + (i >> 3)][i & 7] = (__bf16)e;
                 }
         }
-        // 16 lanes read 4 keys x 16 dims and get 4 keys of one dim each
-        auto v_fragment = [&](int kc, int d) {
-            v4s part[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int key = 16 * kc + 8 * e + 4 * h + ((lane & 15) >> 2);
-                const int chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-                const char *at = vt + key * (D * 2) + ((chunk ^ v_swizzle<D>(key)) << 4) + (lane & 1) * 8;
-                part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) v4s *)(uintptr_t)lds_addr(at));
+        for (int kc = 0; kc < 4; ++kc)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const v8bf vf = v_fragment(2 + (tile & 1), kc, d);
+#pragma unroll
+                for (int u = 0; u < QT; ++u)
+                    o[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[u][kc], o[u][d], 0, 0, 0);
             }
-            return __builtin_bit_cast(uint4, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        };
-        if (!masked || !holds_non_finite<kTile>(vt)) {
-#pragma unroll
-            for (int kc = 0; kc < 4; ++kc)
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const v8bf vf = __builtin_bit_cast(v8bf, v_fragment(kc, d));
-#pragma unroll
-                    for (int u = 0; u < QT; ++u)
-                        o[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u][kc], o[u][d], 0, 0, 0);
-                }
-        } else {
-#pragma unroll
-            for (int u = 0; u < QT; ++u)
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    v16f count = {};
-#pragma unroll
-                    for (int kc = 0; kc < 4; ++kc) {
-                        const uint4 w = v_fragment(kc, d);
-                        const v8bf vf = __builtin_bit_cast(
-                            v8bf, make_uint4(finite_pair(w.x), finite_pair(w.y), finite_pair(w.z), finite_pair(w.w)));
-                        o[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u][kc], o[u][d], 0, 0, 0);
-                        const v8bf nf = __builtin_bit_cast(
-                            v8bf, make_uint4(counted_pair(w.x), counted_pair(w.y), counted_pair(w.z), counted_pair(w.w)));
-                        v8bf seen;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            seen[i] = (__bf16)(tile * kKeys + 16 * kc + 8 * (i >> 2) + 4 * h + (i & 3) <= tok[u] ? 1.0f : 0.0f);
-                        count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(nf, seen, count, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[u][d][i] += counted_value(count[i]);
-                }
-        }
     }
 
 #pragma unroll
