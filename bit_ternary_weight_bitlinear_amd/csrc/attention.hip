@@ -47,10 +47,10 @@ __global__ __launch_bounds__(64) void attention_kernel(AttentionProblem a)
 
 // ---------------------------------------------------------------- bf16 on the matrix cores
 //
-// A workgroup of 4 waves takes 128 * QT query rows of one kv head: row r of a
-// sequence is token r / group, query head r % group, so the heads that share K
-// and V share their tiles and short prompts fill a tile. Each wave has QT column
-// tiles of 32 rows and everything of a row in one lane pair:
+// A workgroup of 4 waves takes 128 query rows of one kv head (64 with KS = 2): row
+// r of a sequence is token r / group, query head r % group, so the heads that
+// share K and V share their tiles and short prompts fill a tile. A wave has 32
+// rows, and everything of a row in one lane pair:
 //   S^T = K Q^T      (v_mfma_f32_32x32x16_bf16, A = 32 keys, B = 32 query rows)
 //   O^T = V^T P^T    (A = 32 dims of V read transposed from LDS, B = P)
 // The result's column is lane % 32, so maximum, sum and rescaling are per lane,
@@ -59,7 +59,15 @@ __global__ __launch_bounds__(64) void attention_kernel(AttentionProblem a)
 // of every 16: P never leaves the registers.
 // K and V tiles of 64 keys come by direct loads into two LDS buffers, one barrier
 // per tile. 16-byte chunks are permuted within a row by the global address, so
-// that the operand reads touch every bank once.
+// that the operand reads touch every bank once (conflicts: 1 % of the LDS time).
+// P is rounded to bf16 for its product with V, as the inputs are; sums and
+// statistics stay in fp32.
+// Bound by the matrix cores and the softmax's VALU work in about equal parts (55 %
+// and 50 % of the cycles at 8192 tokens), which two waves per SIMD overlap poorly.
+// Measured and not kept: eight waves per workgroup (536 against 543 us at 8192
+// tokens, 57.9 against 46.4 at 2048), raised wave priority around the products
+// (545 to 551), the row sum by dot products of pairs (551), 64 rows per wave with
+// the next tile's logits formed beside the softmax (registers spill: 1757 us).
 constexpr int kKeys = 64;
 
 template <int D>
@@ -78,6 +86,8 @@ __device__ inline void both_halves(float v, float &lower, float &upper)
 // Rescaling is put off until a maximum has grown by 2^kSlack: p stays below that,
 // which neither bf16 nor the fp32 sums notice.
 constexpr float kSlack = 8.0f;
+
+constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;
 
 // Where a tile's mask leaves out keys, 0 * v must not bring a NaN or infinity of
 // theirs into the sum. The workgroup looks through such a tile of V (the last one
@@ -103,10 +113,10 @@ __device__ inline float counted_value(float n)
     return c >= 1 << 14 || (plus && minus) ? __builtin_nanf("") : plus ? __builtin_inff() : minus ? kNegInf : 0.0f;
 }
 
-template <int D, int QT>
-__global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(AttentionProblem a, int group)
+template <int D, int KS>
+__global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem a, int group)
 {
-    constexpr int ROWS = 128 * QT, C = D / 16, DT = D / 32;
+    constexpr int ROWS = 128 / KS, C = D / 16, DT = D / 32, NB = 2 / KS;
     constexpr int kTile = kKeys * D * 2;                  // bytes of a K or V tile
     constexpr int kLoads = kTile / (1024 * 4);            // direct loads per wave and tile
     constexpr int kChunks = D / 8;                        // 16-byte chunks per row
@@ -123,25 +133,25 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
         return;
     const int rows = t.n * group;
     t.tile = (rows + ROWS - 1) / ROWS - 1 - t.tile;       // the longest rows first
-    const int r_wave = t.tile * ROWS + wave * 32 * QT;
+    const int r_wave = t.tile * ROWS + wave / KS * 32;
+    const int b0 = KS == 1 ? 0 : wave % KS;               // the wave's 32-key blocks of a tile: b0 .. b0+NB-1
 
     // query rows (rows past the last one repeat it and are not stored)
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-    int tok[QT];
-    v8bf qf[QT][C];
-#pragma unroll
-    for (int u = 0; u < QT; ++u) {
-        int r = r_wave + 32 * u + col;
+    int tok;
+    v8bf qf[C];
+    {
+        int r = r_wave + col;
         r = r < rows ? r : rows - 1;
-        tok[u] = r / group;
-        const bf16_t *src = static_cast<const bf16_t *>(a.q) + (t.begin + tok[u]) * a.q_stride +
+        tok = r / group;
+        const bf16_t *src = static_cast<const bf16_t *>(a.q) + (t.begin + tok) * a.q_stride +
                             (int64_t)(head * group + r % group) * D + 8 * h;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             uint4 w = *reinterpret_cast<const uint4 *>(src + 16 * i);
             w = make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
-            qf[u][i] = __builtin_bit_cast(v8bf, w);
+            qf[i] = __builtin_bit_cast(v8bf, w);
         }
     }
     const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
@@ -150,7 +160,7 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
     const int group_masked = (t.tile * ROWS / group + 1) / kKeys;
     const int wave_masked = ((r_wave < rows ? r_wave : rows - 1) / group + 1) / kKeys;
 
-    // direct loads: load i of wave w brings rows kLoadRows*i + (16 or 32 B per ...)
+    // direct loads: load i of the four waves brings rows kLoadRows*i .. kLoadRows*(i+1)-1 of a tile
     const uint32_t base = lds_addr(lds);
     const int load_row = wave * (kLoadRows / 4) + lane / kChunks;
     const int k_chunk = ((lane % kChunks) ^ k_swizzle<D>(load_row)) * 16, v_chunk = ((lane % kChunks) ^ v_swizzle<D>(load_row)) * 16;
@@ -179,11 +189,11 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
     // operand addresses inside a tile; rows 32 keys further on, and 8 keys for V, are constant offsets
     int k_at[C], v_at[DT];
 #pragma unroll
-    for (int i = 0; i < C; ++i) k_at[i] = col * (D * 2) + (((2 * i + h) ^ k_swizzle<D>(col)) << 4);
+    for (int i = 0; i < C; ++i) k_at[i] = (32 * b0 + col) * (D * 2) + (((2 * i + h) ^ k_swizzle<D>(col)) << 4);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
         const int key = 4 * h + ((lane & 15) >> 2), chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        v_at[d] = key * (D * 2) + ((chunk ^ v_swizzle<D>(key)) << 4) + (lane & 1) * 8;
+        v_at[d] = (32 * b0 + key) * (D * 2) + ((chunk ^ v_swizzle<D>(key)) << 4) + (lane & 1) * 8;
     }
     auto k_fragment = [&](int tile, int b, int i) {
         return *reinterpret_cast<const v8bf *>(lds + (tile & 1) * kTile + k_at[i] + b * 32 * D * 2);
@@ -198,15 +208,10 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
         return __builtin_bit_cast(v8bf, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
 
-    v16f o[QT][DT];
-    float mx[QT], sum[QT];
+    v16f o[DT];
+    float mx = kNegInf, sum = 0.0f;
 #pragma unroll
-    for (int u = 0; u < QT; ++u) {
-        mx[u] = kNegInf;
-        sum[u] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < DT; ++i) o[u][i] = v16f{};
-    }
+    for (int i = 0; i < DT; ++i) o[i] = v16f{};
 
     // V of a masked tile, once it is there: keeps what is not finite from rows that do not see it
     auto clean = [&](int tile) {
@@ -230,21 +235,20 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
         }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < QT; ++u)
+        for (int d = 0; d < DT; ++d) {
+            v16f count = {};
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                v16f count = {};
+            for (int n = 0; n < 2 * NB; ++n) {
+                const int kc = 2 * b0 + n;
+                v8bf seen;
 #pragma unroll
-                for (int kc = 0; kc < 4; ++kc) {
-                    v8bf seen;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        seen[i] = (__bf16)(tile * kKeys + 16 * kc + 8 * (i >> 2) + 4 * h + (i & 3) <= tok[u] ? 1.0f : 0.0f);
-                    count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_fragment(4, kc, d), seen, count, 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[u][d][i] += counted_value(count[i]);
+                for (int i = 0; i < 8; ++i)
+                    seen[i] = (__bf16)(tile * kKeys + 16 * kc + 8 * (i >> 2) + 4 * h + (i & 3) <= tok ? 1.0f : 0.0f);
+                count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_fragment(4, n, d), seen, count, 0, 0, 0);
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] += counted_value(count[i]);
+        }
     };
 
     request(0);
@@ -253,88 +257,117 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void attention_bf16_kernel(At
         if (tile + 1 < tiles) request(tile + 1);
         if (tile >= group_masked) clean(tile);
 
-        v16f s[QT][2];
+        v16f s[NB];
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const v8bf kf = k_fragment(tile, b, i);
+            for (int b = 0; b < NB; ++b)
+                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_fragment(tile, b, i), qf[i], i ? s[b] : v16f{}, 0, 0, 0);
+        // the operand reads run kAhead fragments ahead of the products
+        constexpr int kAhead = 6;
+        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, kAhead, 0);
 #pragma unroll
-                for (int u = 0; u < QT; ++u)
-                    s[u][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[u][i], i ? s[u][b] : v16f{}, 0, 0, 0);
-            }
+        for (int i = 0; i < NB * C - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kAhead, 0);
         if (tile >= wave_masked) {
 #pragma unroll
-            for (int u = 0; u < QT; ++u)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int key = tile * kKeys + 32 * b + 8 * (i >> 2) + 4 * h + (i & 3);
-                        s[u][b][i] = key <= tok[u] ? s[u][b][i] : kNegInf;
-                    }
-        }
-        v8bf p[QT][4];
-#pragma unroll
-        for (int u = 0; u < QT; ++u) {
-            float big = kNegInf;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) big = fmaxf(big, s[u][b][i]);
-            float lo, up;
-            both_halves(big, lo, up);
-            big = fmaxf(lo, up) * c;
-            if (__any(big > mx[u] + kSlack)) {
-                // only where it has grown: a row's result does not depend on its neighbours
-                const float now = big > mx[u] + kSlack ? big : mx[u];
-                const float keep = now == mx[u] ? 1.0f : __builtin_amdgcn_exp2f(mx[u] - now);
-                mx[u] = now;
-                sum[u] *= keep;
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[u][d][i] *= keep;
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][b][i], c, -mx[u]));
-                    sum[u] += e;
-                    p[u][2 * b + (i >> 3)][i & 7] = (__bf16)e;
+                    const int key = tile * kKeys + 32 * (b0 + b) + 8 * (i >> 2) + 4 * h + (i & 3);
+                    s[b][i] = key <= tok ? s[b][i] : kNegInf;
                 }
         }
+        float big = kNegInf, lo, up;
 #pragma unroll
-        for (int kc = 0; kc < 4; ++kc)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const v8bf vf = v_fragment(2 + (tile & 1), kc, d);
+            for (int i = 0; i < 16; ++i) big = fmaxf(big, s[b][i]);
+        both_halves(big, lo, up);
+        big = fmaxf(lo, up) * c;
+        if (__any(big > mx + kSlack)) {
+            // only where it has grown: a row's result does not depend on its neighbours
+            const float now = big > mx + kSlack ? big : mx;
+            const float keep = now == mx ? 1.0f : __builtin_amdgcn_exp2f(mx - now);
+            mx = now;
+            sum *= keep;
 #pragma unroll
-                for (int u = 0; u < QT; ++u)
-                    o[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[u][kc], o[u][d], 0, 0, 0);
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= keep;
+        }
+        const float ref = KS > 1 && mx == kNegInf ? 0.0f : mx;  // -inf: none of the wave's keys is seen yet
+        v8bf p[2 * NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -ref));
+                sum += e;
+                p[2 * b + (i >> 3)][i & 7] = (__bf16)e;
             }
+#pragma unroll
+        for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_fragment(2 + (tile & 1), n, d), p[n], o[d], 0, 0, 0);
     }
 
+    if constexpr (KS > 1) {
+        // the wave with the tiles' upper keys hands its part over, 4 lanes' values of 16 bytes at a time
+        __syncthreads();
+        float *part = reinterpret_cast<float *>(lds + wave / KS * (DT * 4096 + 512));
+        if (b0) {
 #pragma unroll
-    for (int u = 0; u < QT; ++u) {
-        float lo, up;
-        both_halves(sum[u], lo, up);
-        const float inv = 1.0f / (lo + up);
-        const int r = r_wave + 32 * u + col;
-        if (r >= rows) continue;
-        bf16_t *dst = static_cast<bf16_t *>(a.out) + ((t.begin + tok[u]) * a.q_heads + head * group + r % group) * D + 4 * h;
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    *reinterpret_cast<v4f *>(part + ((d * 4 + g) * 64 + lane) * 4) =
+                        v4f{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+            part[DT * 1024 + lane] = mx;
+            part[DT * 1024 + 64 + lane] = sum;
+        }
+        __syncthreads();
+        if (b0) return;
+        const float other = part[DT * 1024 + lane], top = fmaxf(mx, other);
+        const float f0 = __builtin_amdgcn_exp2f(mx - top), f1 = __builtin_amdgcn_exp2f(other - top);
+        sum = __builtin_fmaf(sum, f0, part[DT * 1024 + 64 + lane] * f1);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                bf16_t w[4];
+                const v4f w = *reinterpret_cast<const v4f *>(part + ((d * 4 + g) * 64 + lane) * 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) store_out(&w[i], o[u][d][4 * g + i] * inv);
-                *reinterpret_cast<uint2 *>(dst + 32 * d + 8 * g) = *reinterpret_cast<const uint2 *>(w);
+                for (int i = 0; i < 4; ++i) o[d][4 * g + i] = __builtin_fmaf(o[d][4 * g + i], f0, w[i] * f1);
             }
     }
+    float lo, up;
+    both_halves(sum, lo, up);
+    const float inv = 1.0f / (lo + up);
+    const int r = r_wave + col;
+    if (r >= rows) return;
+    bf16_t *dst = static_cast<bf16_t *>(a.out) + ((t.begin + tok) * a.q_heads + head * group + r % group) * D + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            bf16_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store_out(&w[i], o[d][4 * g + i] * inv);
+            *reinterpret_cast<uint2 *>(dst + 32 * d + 8 * g) = *reinterpret_cast<const uint2 *>(w);
+        }
 }
+
+// Few workgroups: a tile's keys are split over two waves (KS = 2), so that there
+// are twice as many and the longest takes half as long. It pays up to one and a
+// half workgroups per CU, three for 64-wide heads, whose LDS lets more of them
+// share a CU (20/5 heads of 128, one prompt, KS = 1 / 2: 1024 tokens 24.3 / 21.1
+// us, 2048 44.2 / 39.2, 3000 68.2 / 72.7, 4096 103 / 119; 16/4 heads of 64, 4096
+// tokens: 62.6 / 53.4).
+constexpr int64_t kFewGroups128 = 384, kFewGroups64 = 768;
 
 int64_t attention_workspace(const AttentionProblem &) { return 0; }
 
@@ -342,12 +375,14 @@ hipError_t launch_attention(const AttentionProblem &p, void *, hipStream_t st)
 {
     const int group = (int)(p.q_heads / p.kv_heads);
     if (p.bf16) {
-        auto go = [&](auto width, auto tiles) {
-            constexpr int D = decltype(width)::value, QT = decltype(tiles)::value;
-            const int64_t n = p.m * group / (128 * QT) + p.seqs;
-            hipLaunchKernelGGL((attention_bf16_kernel<D, QT>), dim3((unsigned)(n * p.kv_heads)), dim3(256), 0, st, p, group);
+        auto go = [&](auto width, auto splits) {
+            constexpr int D = decltype(width)::value, KS = decltype(splits)::value;
+            const int64_t n = p.m * group * KS / 128 + p.seqs;
+            hipLaunchKernelGGL((attention_bf16_kernel<D, KS>), dim3((unsigned)(n * p.kv_heads)), dim3(256), 0, st, p, group);
         };
-        p.head_dim == 128 ? go(Width<128>{}, Width<1>{}) : go(Width<64>{}, Width<1>{});
+        const int64_t groups = (p.m * group / 128 + p.seqs) * p.kv_heads;
+        if (p.head_dim == 128) groups > kFewGroups128 ? go(Width<128>{}, Width<1>{}) : go(Width<128>{}, Width<2>{});
+        else groups > kFewGroups64 ? go(Width<64>{}, Width<1>{}) : go(Width<64>{}, Width<2>{});
         return hipGetLastError();
     }
     const dim3 grid((unsigned)p.m, (unsigned)p.q_heads);
