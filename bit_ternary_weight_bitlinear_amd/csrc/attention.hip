@@ -7,44 +7,6 @@
 
 namespace bl {
 
-__device__ inline float wave_sum_f32(float v)
-{
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
-
-// One wave per row and query head, D / 64 dims per lane.
-template <typename T, int D>
-__global__ __launch_bounds__(64) void attention_kernel(AttentionProblem a)
-{
-    constexpr int E = D / 64;
-    const int lane = threadIdx.x, head = blockIdx.y;
-    const int first = a.cu[0] < 0 ? 0 : a.cu[0];
-    SeqTile t;
-    if (!find_tile(a.cu, (int)a.seqs, a.m, blockIdx.x - first, [](int, int n) { return n; }, t)) return;
-    const int64_t row = t.begin + t.tile;
-    const int64_t kv = head / (a.q_heads / a.kv_heads);
-    float q[E], o[E] = {}, mx = kNegInf, l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = to_f32(static_cast<const T *>(a.q)[row * a.q_stride + head * D + e * 64 + lane]);
-    for (int64_t j = t.begin; j <= row; ++j) {
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            s = __builtin_fmaf(q[e], to_f32(static_cast<const T *>(a.k)[j * a.k_stride + kv * D + e * 64 + lane]), s);
-        s = wave_sum_f32(s) * (a.scale * kLog2e);
-        const float now = fmaxf(mx, s), keep = __builtin_amdgcn_exp2f(mx - now), p = __builtin_amdgcn_exp2f(s - now);
-        mx = now;
-        l = __builtin_fmaf(l, keep, p);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = __builtin_fmaf(o[e], keep, p * to_f32(static_cast<const T *>(a.v)[j * a.v_stride + kv * D + e * 64 + lane]));
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) store_out(static_cast<T *>(a.out) + (row * a.q_heads + head) * D + e * 64 + lane, o[e] / l);
-}
-
 // ---------------------------------------------------------------- bf16 on the matrix cores
 //
 // A workgroup of 4 waves takes 128 query rows of one kv head (64 with KS = 2): row
@@ -95,22 +57,61 @@ constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;
 // tile holds what it was: +inf as 1, -inf as 2^7, NaN as 2^14. A product of that
 // tile with the mask counts per dim and row what the row sees (at most 64 of each,
 // so fp32 holds all three counts).
-__device__ inline bool not_finite_pair(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u; }
+struct Bf16Bits {
+    static constexpr uint32_t kExp = 0x7F80, kMan = 0x7F, kOne = 0x3F80, k128 = 0x4300, k16384 = 0x4680;
+};
+struct F16Bits {
+    static constexpr uint32_t kExp = 0x7C00, kMan = 0x3FF, kOne = 0x3C00, k128 = 0x5800, k16384 = 0x7400;
+};
+template <typename B>
+__device__ inline bool not_finite_pair(uint32_t w) { return (w & B::kExp) == B::kExp || (w >> 16 & B::kExp) == B::kExp; }
+template <typename B>
 __device__ inline uint32_t finite_pair(uint32_t w)
 {
-    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-    if ((w & 0x00007F80u) == 0x00007F80u) w &= 0xFFFF0000u;
+    if ((w >> 16 & B::kExp) == B::kExp) w &= 0x0000FFFFu;
+    if ((w & B::kExp) == B::kExp) w &= 0xFFFF0000u;
     return w;
 }
-__device__ inline uint32_t counted(uint32_t b)  // of bf16 bits, as bf16 bits
+template <typename B>
+__device__ inline uint32_t counted(uint32_t b)
 {
-    return (b & 0x7F80u) != 0x7F80u ? 0u : b & 0x7Fu ? 0x4680u : b & 0x8000u ? 0x4300u : 0x3F80u;
+    return (b & B::kExp) != B::kExp ? 0u : b & B::kMan ? B::k16384 : b & 0x8000u ? B::k128 : B::kOne;
 }
-__device__ inline uint32_t counted_pair(uint32_t w) { return counted(w & 0xFFFFu) | counted(w >> 16) << 16; }
+template <typename B>
+__device__ inline uint32_t counted_pair(uint32_t w) { return counted<B>(w & 0xFFFFu) | counted<B>(w >> 16) << 16; }
 __device__ inline float counted_value(float n)
 {
     const int c = (int)n, plus = c & 127, minus = (c >> 7) & 127;
     return c >= 1 << 14 || (plus && minus) ? __builtin_nanf("") : plus ? __builtin_inff() : minus ? kNegInf : 0.0f;
+}
+
+// The first half of it, by a workgroup of four waves: whether the tile held any
+template <typename B, int BYTES>
+__device__ inline bool set_aside(char *tile, char *counts)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    char *vt = tile + wave * (BYTES / 4) + lane * 16, *ct = counts + wave * (BYTES / 4) + lane * 16;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < BYTES / 4096; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
+        bad = bad || not_finite_pair<B>(w.x) || not_finite_pair<B>(w.y) || not_finite_pair<B>(w.z) || not_finite_pair<B>(w.w);
+    }
+    int *flags = reinterpret_cast<int *>(counts);
+    bad = __any(bad);
+    if (lane == 0) flags[wave] = bad;
+    __syncthreads();
+    if (!(flags[0] | flags[1] | flags[2] | flags[3])) return false;
+    __syncthreads();
+    for (int i = 0; i < BYTES / 4096; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
+        *reinterpret_cast<uint4 *>(vt + i * 1024) =
+            make_uint4(finite_pair<B>(w.x), finite_pair<B>(w.y), finite_pair<B>(w.z), finite_pair<B>(w.w));
+        *reinterpret_cast<uint4 *>(ct + i * 1024) =
+            make_uint4(counted_pair<B>(w.x), counted_pair<B>(w.y), counted_pair<B>(w.z), counted_pair<B>(w.w));
+    }
+    __syncthreads();
+    return true;
 }
 
 template <int D, int KS>
@@ -215,25 +216,7 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 
     // V of a masked tile, once it is there: keeps what is not finite from rows that do not see it
     auto clean = [&](int tile) {
-        char *vt = lds + (2 + (tile & 1)) * kTile + wave * (kTile / 4) + lane * 16, *ct = lds + 4 * kTile + wave * (kTile / 4) + lane * 16;
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < kTile / 4096; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
-            bad = bad || not_finite_pair(w.x) || not_finite_pair(w.y) || not_finite_pair(w.z) || not_finite_pair(w.w);
-        }
-        int *flags = reinterpret_cast<int *>(lds + 4 * kTile);
-        bad = __any(bad);
-        if (lane == 0) flags[wave] = bad;
-        __syncthreads();
-        if (!(flags[0] | flags[1] | flags[2] | flags[3])) return;
-        __syncthreads();
-        for (int i = 0; i < kTile / 4096; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
-            *reinterpret_cast<uint4 *>(vt + i * 1024) = make_uint4(finite_pair(w.x), finite_pair(w.y), finite_pair(w.z), finite_pair(w.w));
-            *reinterpret_cast<uint4 *>(ct + i * 1024) = make_uint4(counted_pair(w.x), counted_pair(w.y), counted_pair(w.z), counted_pair(w.w));
-        }
-        __syncthreads();
+        if (!set_aside<Bf16Bits, kTile>(lds + (2 + (tile & 1)) * kTile, lds + 4 * kTile)) return;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             v16f count = {};
@@ -361,6 +344,323 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
         }
 }
 
+// ---------------------------------------------------------------- fp32 on the matrix cores
+//
+// fp32 products from fp16 ones: x = 2^a (hi + lo) with hi the nearest fp16 of
+// x / 2^a and lo that of the rest (22 bits and a sign), a such that the row's
+// largest magnitude lies in 2^14 .. 2^15; then xy ~ hi hi' + hi lo' + lo hi', off
+// by 2^-22 of |x||y| at most, with fp32 sums. Rows' elements below 2^-16 of the
+// largest keep 2^-40 of it. Three matrix products instead of one on the fp32
+// matrix cores, whose rate is a sixteenth.
+// A first kernel writes K and V in this form, once per row (the rows that read
+// them split nothing): [head][token][hi, lo][D], and 2^a per row.
+// The scale of K's rows multiplies the logits. That of V's rows goes into the
+// weights: w_j = p_j 2^(a_j - r) with r the running maximum of a_j over the keys
+// that the row sees, so that hi and lo of w keep 22 bits of the largest products.
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+constexpr float kSlackF32 = 3.0f;      // as kSlack: p stays below 2^3 ...
+constexpr float kWeightOne = 2048.0f;  // ... and w times this below 2^14
+
+// 2^a of a row whose largest finite magnitude is big, and its reciprocal
+__device__ inline void row_scale(float big, float &scale, float &inv)
+{
+    int a = (int)(__float_as_uint(big) >> 23) - 127 - 14;
+    a = a < -100 ? -100 : a;
+    scale = __uint_as_float((uint32_t)(a + 127) << 23);
+    inv = __uint_as_float((uint32_t)(127 - a) << 23);
+}
+__device__ inline float finite_abs(float v) { return fabsf(v) <= 3.402823466e38f ? fabsf(v) : 0.0f; }
+__device__ inline void split_f16(float v, _Float16 &hi, _Float16 &lo)
+{
+    hi = (_Float16)v;
+    const float rest = v - (float)hi;
+    lo = (_Float16)(rest - rest == 0.0f ? rest : 0.0f);
+}
+
+// D / 4 lanes per row of K or V (blockIdx.y: 0, 1)
+template <int D>
+__global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a, char *__restrict__ planes,
+                                                              float *__restrict__ scales)
+{
+    constexpr int L = D / 4;
+    const int64_t rows = a.m * a.kv_heads, n = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    if (n >= rows) return;
+    const int64_t tok = n / a.kv_heads, head = n % a.kv_heads, at = head * a.m + tok;
+    const int is_v = blockIdx.y, lane = threadIdx.x % L;
+    const float *src = static_cast<const float *>(is_v ? a.v : a.k) + tok * (is_v ? a.v_stride : a.k_stride) + head * D + 4 * lane;
+    const float4 x = *reinterpret_cast<const float4 *>(src);
+    float big = fmaxf(fmaxf(finite_abs(x.x), finite_abs(x.y)), fmaxf(finite_abs(x.z), finite_abs(x.w)));
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) big = fmaxf(big, __shfl_xor(big, d));
+    float scale, inv;
+    row_scale(big, scale, inv);
+    _Float16 hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_f16((&x.x)[i] * inv, hi[i], lo[i]);
+    char *dst = planes + (is_v * rows + at) * (D * 4) + lane * 8;
+    *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(hi);
+    *reinterpret_cast<uint2 *>(dst + D * 2) = *reinterpret_cast<const uint2 *>(lo);
+    if (lane == 0) scales[is_v * rows + at] = scale;
+}
+
+// The loop of attention_bf16_kernel with the four 16-bit planes of a tile of
+// 32 * KS keys, 32 keys per wave.
+template <int D, int KS>
+__global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(AttentionProblem a, int group,
+                                                                            const char *__restrict__ planes,
+                                                                            const float *__restrict__ scales)
+{
+    constexpr int ROWS = 128 / KS, C = D / 16, DT = D / 32, KEYS = 32 * KS;
+    constexpr int kPlane = KEYS * D * 2;
+    constexpr int kLoads = kPlane / (1024 * 4);           // direct loads per wave and plane
+    constexpr int kChunks = D / 8, kLoadRows = KEYS / kLoads;
+    constexpr int kStage = 4 * kPlane + 512;              // K hi, lo, V hi, lo, scales of K and V
+    __shared__ __align__(1024) char lds[2 * kStage + kPlane];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = lane >> 5, col = lane & 31;
+    const int head = blockIdx.x % (int)a.kv_heads;
+    SeqTile t;
+    if (!find_tile(a.cu, (int)a.seqs, a.m, blockIdx.x / (int)a.kv_heads,
+                   [=](int, int n) { return (int)(((int64_t)n * group + ROWS - 1) / ROWS); }, t))
+        return;
+    const int rows = t.n * group;
+    t.tile = (rows + ROWS - 1) / ROWS - 1 - t.tile;
+    const int r_wave = t.tile * ROWS + wave / KS * 32;
+    const int b0 = KS == 1 ? 0 : wave % KS;               // the wave's 32 keys of a tile
+
+    int tok;
+    float c;
+    v8h qh[C], ql[C];
+    {
+        int r = r_wave + col;
+        r = r < rows ? r : rows - 1;
+        tok = r / group;
+        const float *src = static_cast<const float *>(a.q) + (t.begin + tok) * a.q_stride + (int64_t)(head * group + r % group) * D + 8 * h;
+        float x[C][8];
+        float big = 0.0f, lo, up;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            *reinterpret_cast<float4 *>(&x[i][0]) = *reinterpret_cast<const float4 *>(src + 16 * i);
+            *reinterpret_cast<float4 *>(&x[i][4]) = *reinterpret_cast<const float4 *>(src + 16 * i + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = fmaxf(big, finite_abs(x[i][e]));
+        }
+        both_halves(big, lo, up);
+        float scale, inv;
+        row_scale(fmaxf(lo, up), scale, inv);
+        c = fmaxf(fabsf(a.scale) * kLog2e * scale, 1e-37f);
+        if (a.scale < 0.0f) inv = -inv;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                _Float16 hi, lo16;
+                split_f16(x[i][e] * inv, hi, lo16);
+                qh[i][e] = hi;
+                ql[i][e] = lo16;
+            }
+    }
+    const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
+    const int tiles = last_row / group / KEYS + 1;
+    const int group_masked = (t.tile * ROWS / group + 1) / KEYS;
+    const int wave_masked = ((r_wave < rows ? r_wave : rows - 1) / group + 1) / KEYS;
+
+    const uint32_t base = lds_addr(lds);
+    const int load_row = wave * (kLoadRows / 4) + lane / kChunks;
+    const int k_chunk = ((lane % kChunks) ^ k_swizzle<D>(load_row)) * 16, v_chunk = ((lane % kChunks) ^ v_swizzle<D>(load_row)) * 16;
+    const int64_t plane_rows = a.m * a.kv_heads, first_row = (int64_t)head * a.m + t.begin;
+    auto request = [&](int tile) {
+        const uint32_t to = base + (tile & 1) * kStage;
+        const int left = t.n - 1 - tile * KEYS;
+#pragma unroll
+        for (int is_v = 0; is_v < 2; ++is_v) {
+            const char *from = planes + (is_v * plane_rows + first_row + (int64_t)tile * KEYS) * (D * 4);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int row = i * kLoadRows + load_row;
+                const uint32_t off = (uint32_t)(row < left ? row : left) * (D * 4) + (is_v ? v_chunk : k_chunk);
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo) dma16(from + lo * D * 2, off, to + (2 * is_v + lo) * kPlane + (4 * i + wave) * 1024);
+            }
+        }
+        if (wave < 2) {  // scales of K, V: 64 keys (32 of them twice where a tile has no more)
+            const int key = lane % KEYS;
+            dma4(scales + wave * plane_rows + first_row + (int64_t)tile * KEYS, (uint32_t)(key < left ? key : left) * 4,
+                 to + 4 * kPlane + wave * 256);
+        }
+    };
+
+    int k_at[C], v_at[DT];
+#pragma unroll
+    for (int i = 0; i < C; ++i) k_at[i] = (32 * b0 + col) * (D * 2) + (((2 * i + h) ^ k_swizzle<D>(col)) << 4);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+        const int key = 4 * h + ((lane & 15) >> 2), chunk = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        v_at[d] = (32 * b0 + key) * (D * 2) + ((chunk ^ v_swizzle<D>(key)) << 4) + (lane & 1) * 8;
+    }
+    auto v_fragment = [&](uint32_t plane, int n, int d) {
+        v4s part[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(uintptr_t)(
+                plane + v_at[d] + (16 * n + 8 * e) * D * 2));
+        return __builtin_bit_cast(v8h, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+
+    v16f o[DT];
+    float mx = kNegInf, sum = 0.0f, ref_v = 0.0f;  // ref_v: largest scale of V seen, o is relative to it
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] = v16f{};
+
+    auto clean = [&](int tile) {
+        const uint32_t counts = base + 2 * kStage;
+        if (!set_aside<F16Bits, kPlane>(lds + (tile & 1) * kStage + 2 * kPlane, lds + 2 * kStage)) return;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            v16f count = {};
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                v8h seen;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    seen[i] = (_Float16)(tile * KEYS + 32 * b0 + 16 * n + 8 * (i >> 2) + 4 * h + (i & 3) <= tok ? 1.0f : 0.0f);
+                count = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_fragment(counts, n, d), seen, count, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] += counted_value(count[i]);
+        }
+    };
+
+    request(0);
+    for (int tile = 0; tile < tiles; ++tile) {
+        ring_barrier<0>();
+        if (tile + 1 < tiles) request(tile + 1);
+        if (tile >= group_masked) clean(tile);
+        const char *stage = lds + (tile & 1) * kStage;
+        const uint32_t vt = base + (tile & 1) * kStage + 2 * kPlane;
+
+        v16f s = {};
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const v8h kh = *reinterpret_cast<const v8h *>(stage + k_at[i]), kl = *reinterpret_cast<const v8h *>(stage + kPlane + k_at[i]);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl, qh[i], s, 0, 0, 0);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kh, ql[i], s, 0, 0, 0);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kh, qh[i], s, 0, 0, 0);
+        }
+        // scales of keys 8g + 4h .. +3
+        const float *sc = reinterpret_cast<const float *>(stage + 4 * kPlane) + 32 * b0 + 4 * h;
+        float gv[16];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(sc + 8 * g), v4 = *reinterpret_cast<const float4 *>(sc + 64 + 8 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[4 * g + i] *= (&k4.x)[i];
+                gv[4 * g + i] = (&v4.x)[i];
+            }
+        }
+        if (tile >= wave_masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const bool seen = tile * KEYS + 32 * b0 + 8 * (i >> 2) + 4 * h + (i & 3) <= tok;
+                s[i] = seen ? s[i] : kNegInf;
+                gv[i] = seen ? gv[i] : 0.0f;
+            }
+        }
+        float big = kNegInf, top_v = 0.0f, lo, up;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            big = fmaxf(big, s[i]);
+            top_v = fmaxf(top_v, gv[i]);
+        }
+        both_halves(big, lo, up);
+        big = fmaxf(lo, up) * c;
+        both_halves(top_v, lo, up);
+        top_v = fmaxf(lo, up);
+        if (__any(big > mx + kSlackF32 || top_v > ref_v)) {
+            // only where it has grown: a row's result does not depend on its neighbours
+            const float now = big > mx + kSlackF32 ? big : mx;
+            const float keep = now == mx ? 1.0f : __builtin_amdgcn_exp2f(mx - now);
+            const float now_v = fmaxf(ref_v, top_v), keep_v = now_v == ref_v ? 1.0f : ref_v / now_v;
+            mx = now;
+            ref_v = now_v;
+            sum *= keep;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= keep * keep_v;
+        }
+        const float ref = KS > 1 && mx == kNegInf ? 0.0f : mx;
+        const float to_w = KS > 1 && ref_v == 0.0f ? 0.0f : kWeightOne / ref_v;
+        v8h ph[2], pl[2];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ref));
+            sum += e;
+            _Float16 hi, lo16;
+            const float w = e * (gv[i] * to_w);
+            hi = (_Float16)w;
+            lo16 = (_Float16)(w - (float)hi);
+            ph[i >> 3][i & 7] = hi;
+            pl[i >> 3][i & 7] = lo16;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const v8h vh = v_fragment(vt, n, d), vl = v_fragment(vt + kPlane, n, d);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl, ph[n], o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vh, pl[n], o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vh, ph[n], o[d], 0, 0, 0);
+            }
+    }
+
+    if constexpr (KS > 1) {
+        __syncthreads();
+        float *part = reinterpret_cast<float *>(lds + wave / KS * (DT * 4096 + 768));
+        if (b0) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    *reinterpret_cast<v4f *>(part + ((d * 4 + g) * 64 + lane) * 4) =
+                        v4f{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+            part[DT * 1024 + lane] = mx;
+            part[DT * 1024 + 64 + lane] = sum;
+            part[DT * 1024 + 128 + lane] = ref_v;
+        }
+        __syncthreads();
+        if (b0) return;
+        const float other = part[DT * 1024 + lane], top = fmaxf(mx, other);
+        const float other_v = part[DT * 1024 + 128 + lane], top_v = fmaxf(ref_v, other_v);
+        const float f0 = __builtin_amdgcn_exp2f(mx - top), f1 = __builtin_amdgcn_exp2f(other - top);
+        const float g0 = f0 * (ref_v / top_v), g1 = f1 * (other_v / top_v);
+        sum = __builtin_fmaf(sum, f0, part[DT * 1024 + 64 + lane] * f1);
+        ref_v = top_v;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const v4f w = *reinterpret_cast<const v4f *>(part + ((d * 4 + g) * 64 + lane) * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[d][4 * g + i] = __builtin_fmaf(o[d][4 * g + i], g0, w[i] * g1);
+            }
+    }
+    float lo, up;
+    both_halves(sum, lo, up);
+    const float inv = (ref_v / kWeightOne) / (lo + up);
+    const int r = r_wave + col;
+    if (r >= rows) return;
+    float *dst = static_cast<float *>(a.out) + ((t.begin + tok) * a.q_heads + head * group + r % group) * D + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<float4 *>(dst + 32 * d + 8 * g) =
+                make_float4(o[d][4 * g] * inv, o[d][4 * g + 1] * inv, o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv);
+}
+
 // Few workgroups: a tile's keys are split over two waves (KS = 2), so that there
 // are twice as many and the longest takes half as long. It pays up to one and a
 // half workgroups per CU, three for 64-wide heads, whose LDS lets more of them
@@ -369,25 +669,33 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 // tokens: 62.6 / 53.4).
 constexpr int64_t kFewGroups128 = 384, kFewGroups64 = 768;
 
-int64_t attention_workspace(const AttentionProblem &) { return 0; }
+int64_t attention_workspace(const AttentionProblem &p)
+{
+    const int64_t rows = p.m * p.kv_heads;
+    return p.bf16 ? 0 : round_up(2 * rows * p.head_dim * 4, 256) + round_up(2 * rows * 4, 256);
+}
 
-hipError_t launch_attention(const AttentionProblem &p, void *, hipStream_t st)
+hipError_t launch_attention(const AttentionProblem &p, void *ws, hipStream_t st)
 {
     const int group = (int)(p.q_heads / p.kv_heads);
-    if (p.bf16) {
-        auto go = [&](auto width, auto splits) {
-            constexpr int D = decltype(width)::value, KS = decltype(splits)::value;
-            const int64_t n = p.m * group * KS / 128 + p.seqs;
-            hipLaunchKernelGGL((attention_bf16_kernel<D, KS>), dim3((unsigned)(n * p.kv_heads)), dim3(256), 0, st, p, group);
-        };
-        const int64_t groups = (p.m * group / 128 + p.seqs) * p.kv_heads;
-        if (p.head_dim == 128) groups > kFewGroups128 ? go(Width<128>{}, Width<1>{}) : go(Width<128>{}, Width<2>{});
-        else groups > kFewGroups64 ? go(Width<64>{}, Width<1>{}) : go(Width<64>{}, Width<2>{});
-        return hipGetLastError();
-    }
-    const dim3 grid((unsigned)p.m, (unsigned)p.q_heads);
-    if (p.head_dim == 128) hipLaunchKernelGGL((attention_kernel<float, 128>), grid, dim3(64), 0, st, p);
-    else hipLaunchKernelGGL((attention_kernel<float, 64>), grid, dim3(64), 0, st, p);
+    const int64_t rows = p.m * p.kv_heads;
+    char *planes = static_cast<char *>(ws);
+    float *scales = p.bf16 ? nullptr : reinterpret_cast<float *>(planes + round_up(2 * rows * p.head_dim * 4, 256));
+    auto go = [&](auto width, auto splits) {
+        constexpr int D = decltype(width)::value, KS = decltype(splits)::value;
+        const dim3 grid((unsigned)((p.m * group * KS / 128 + p.seqs) * p.kv_heads));
+        if (p.bf16) {
+            hipLaunchKernelGGL((attention_bf16_kernel<D, KS>), grid, dim3(256), 0, st, p, group);
+        } else {
+            hipLaunchKernelGGL((attention_split_kernel<D>), dim3((unsigned)ceil_div(rows * (D / 4), 256), 2), dim3(256), 0, st, p,
+                               planes, scales);
+            hipLaunchKernelGGL((attention_f32_kernel<D, KS>), grid, dim3(256), 0, st, p, group, (const char *)planes,
+                               (const float *)scales);
+        }
+    };
+    const int64_t groups = (p.m * group / 128 + p.seqs) * p.kv_heads;
+    if (p.head_dim == 128) groups > kFewGroups128 ? go(Width<128>{}, Width<1>{}) : go(Width<128>{}, Width<2>{});
+    else groups > kFewGroups64 ? go(Width<64>{}, Width<1>{}) : go(Width<64>{}, Width<2>{});
     return hipGetLastError();
 }
 
