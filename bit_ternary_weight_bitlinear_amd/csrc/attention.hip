@@ -548,6 +548,15 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
             s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kh, ql[i], s, 0, 0, 0);
             s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kh, qh[i], s, 0, 0, 0);
         }
+        // the operand reads run kAhead pairs ahead of the products
+        constexpr int kAhead = 4;
+        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 2 * kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < C - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 3, 0);
+            __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 3 * kAhead, 0);
         // scales of keys 8g + 4h .. +3
         const float *sc = reinterpret_cast<const float *>(stage + 4 * kPlane) + 32 * b0 + 4 * h;
         float gv[16];
@@ -663,11 +672,15 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 
 // Few workgroups: a tile's keys are split over two waves (KS = 2), so that there
 // are twice as many and the longest takes half as long. It pays up to one and a
-// half workgroups per CU, three for 64-wide heads, whose LDS lets more of them
-// share a CU (20/5 heads of 128, one prompt, KS = 1 / 2: 1024 tokens 24.3 / 21.1
-// us, 2048 44.2 / 39.2, 3000 68.2 / 72.7, 4096 103 / 119; 16/4 heads of 64, 4096
-// tokens: 62.6 / 53.4).
-constexpr int64_t kFewGroups128 = 384, kFewGroups64 = 768;
+// half workgroups per CU in bf16, one in fp32 (whose KS = 2 fills a CU's LDS), and
+// twice as many of 64-wide heads, whose tiles are half as large. 20/5 heads of 128,
+// one prompt, KS = 1 / 2: bf16 1024 tokens 24.3 / 21.1 us, 2048 44.2 / 39.2, 3000
+// 68.2 / 72.7, 4096 103 / 119; fp32 1024 tokens 70.8 / 53.5, 2048 130 / 137. 16/4
+// heads of 64: bf16 4096 tokens 62.6 / 53.4, fp32 2048 tokens 82.5 / 60.7.
+static bool few_groups(const AttentionProblem &p, int64_t groups)
+{
+    return groups <= (p.bf16 ? 384 : 256) * (128 / p.head_dim);
+}
 
 int64_t attention_workspace(const AttentionProblem &p)
 {
@@ -694,8 +707,9 @@ hipError_t launch_attention(const AttentionProblem &p, void *ws, hipStream_t st)
         }
     };
     const int64_t groups = (p.m * group / 128 + p.seqs) * p.kv_heads;
-    if (p.head_dim == 128) groups > kFewGroups128 ? go(Width<128>{}, Width<1>{}) : go(Width<128>{}, Width<2>{});
-    else groups > kFewGroups64 ? go(Width<64>{}, Width<1>{}) : go(Width<64>{}, Width<2>{});
+    const bool few = few_groups(p, groups);
+    if (p.head_dim == 128) few ? go(Width<128>{}, Width<2>{}) : go(Width<128>{}, Width<1>{});
+    else few ? go(Width<64>{}, Width<2>{}) : go(Width<64>{}, Width<1>{});
     return hipGetLastError();
 }
 
