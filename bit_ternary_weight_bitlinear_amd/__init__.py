@@ -423,159 +423,182 @@ def cache_alloc(pages: int, kv_heads: int, head_dim: int, device="cuda") -> KVCa
     return KVCache(*codes, *scales)
 
 
-def _on_its_device(fn):
-    """Runs a call with its first tensor's device as the current one: a kernel is launched on the
-    current device, and the stream taken for it has to be that device's."""
-    @functools.wraps(fn)
-    def call(*args, **kwargs):
-        t = args[0] if args else None
-        t = t[0] if isinstance(t, tuple) and t else t
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index == torch.cuda.current_device():
-            return fn(*args, **kwargs)
-        with torch.cuda.device(t.device):
-            return fn(*args, **kwargs)
-    return call
+# One token's calls take a few microseconds on the device, so what stands before the launch counts:
+# every tensor is looked at once, and a check that fails says what it expected.
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the address alone; the public call builds a Stream object (1.5 us)
+_I32, _I8, _U8, _F32T = torch.int32, torch.int8, torch.uint8, torch.float32
+_ACT = {torch.float32: _F32, torch.bfloat16: _BF16}
 
 
-def _heads(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
-    """(address, elements between tokens) of q, k or v [m][heads][head_dim]: heads of a token adjacent."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _elsewhere(t, name: str) -> int | None:
+    """The device index of a call's first tensor if it is not the current one: a kernel is launched on
+    the current device, and the stream taken for it has to be that device's."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise BitLinearError(f"{name} must be a device (HIP) tensor")
-    if t.dim() != 3 or t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] != 1):
+    device = t.get_device()
+    return None if device == torch.cuda.current_device() else device
+
+
+def _heads(t: torch.Tensor, name: str, dtype, device: int):
+    """(address, elements between tokens) of q, k or v [m][heads][head_dim]: heads of a token adjacent."""
+    if not isinstance(t, torch.Tensor):
+        raise BitLinearError(f"{name} must be a device (HIP) tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] != 1):
         raise BitLinearError(f"{name} must be [m][heads][head_dim] with a token's heads adjacent")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise BitLinearError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if t.dtype != dtype or t.get_device() != device:
+        raise BitLinearError(f"{name} must be {dtype} on device {device}, got {t.dtype} on {t.device}")
     # the stride of a single token means nothing; torch may report any
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _ints(t: torch.Tensor, name: str, shape, device) -> int:
-    p = _dev(t, name, torch.int32)
-    if tuple(t.shape) != shape or t.device != device:
-        raise BitLinearError(f"{name} must have shape {shape} on {device}, got {tuple(t.shape)} on {t.device}")
-    return p
+def _dense(t: torch.Tensor, name: str, dtype, shape: tuple, device: int) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise BitLinearError(f"{name} must be a device (HIP) tensor")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise BitLinearError(f"{name} must be {dtype}, contiguous, of shape {shape} on device {device}; got {t.dtype}, "
+                             f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _starts(cu: torch.Tensor, device):
+def _starts(cu, device: int):
     if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 2:
         raise BitLinearError("cu_seqlens must be int32 [seqs + 1]")
-    return _ints(cu, "cu_seqlens", (cu.shape[0],), device), cu.shape[0] - 1
+    n = cu.shape[0]
+    return _dense(cu, "cu_seqlens", _I32, (n,), device), n - 1
 
 
-def _cache_args(cache, kv_heads: int | None, head_dim: int, device):
+def _cache_args(cache, kv_heads: int | None, head_dim: int, device: int):
+    """(K codes, V codes, K scales, V scales, pages, kv_heads)"""
     if len(cache) != 4:
         raise BitLinearError("cache must be a KVCache")
     k, v, ks, vs = cache
-    addresses = (_dev(k, "cache.k", torch.int8), _dev(v, "cache.v", torch.int8),
-                 _dev(ks, "cache.k_scale", torch.float32), _dev(vs, "cache.v_scale", torch.float32))
-    if k.dim() != 3 or v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != ks.shape or \
-            k.shape[2] != CACHE_BLOCK * head_dim or (kv_heads is not None and k.shape[1] != kv_heads):
-        raise BitLinearError(f"cache does not hold heads of {head_dim} (and {kv_heads} of them)")
-    if any(t.device != device for t in cache):
-        raise BitLinearError(f"cache must be on {device}")
-    return addresses, k.shape[0]
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise BitLinearError(f"cache.k must be int8 [pages][kv_heads][{CACHE_BLOCK} * head_dim]")
+    shape = k.shape
+    pages, heads, width = shape
+    if width != CACHE_BLOCK * head_dim or (kv_heads is not None and heads != kv_heads):
+        raise BitLinearError(f"cache holds {heads} heads of {width // CACHE_BLOCK}, not {kv_heads or heads} of {head_dim}")
+    per = (pages, heads)
+    return (_dense(k, "cache.k", _I8, shape, device), _dense(v, "cache.v", _I8, shape, device),
+            _dense(ks, "cache.k_scale", _F32T, per, device), _dense(vs, "cache.v_scale", _F32T, per, device), pages, heads)
 
 
-def _table_args(block_table, lens, cu_seqlens, m: int, device, name: str = "lens"):
+def _table_args(block_table, lens, cu_seqlens, m: int, device: int, name: str = "lens"):
     """(cu, lens, seqs, table, max_blocks) of a paged call; without cu_seqlens one row per sequence."""
     cu, seqs = (None, m) if cu_seqlens is None else _starts(cu_seqlens, device)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise BitLinearError("block_table must be int32 [seqs][max_blocks]")
     wide = block_table.shape[1]
-    return (cu, _ints(lens, name, (seqs,), device), seqs, _ints(block_table, "block_table", (seqs, wide), device), wide)
+    return cu, _dense(lens, name, _I32, (seqs,), device), seqs, _dense(block_table, "block_table", _I32, (seqs, wide), device), wide
 
 
-def _own_workspace(nbytes: int, workspace, device):
+def _scratch(nbytes: int, workspace, device: torch.device):
+    """(tensor, address, bytes) of a call's workspace. The tensor is held until the launch: the caching
+    allocator hands its memory on to later work of the same stream only."""
     if nbytes == 0:
-        return None, 0
+        return None, None, 0
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    else:
-        _dev(workspace, "workspace")
-        if workspace.numel() * workspace.element_size() < nbytes:
-            raise BitLinearError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, {nbytes} needed")
-    # the caching allocator hands the memory on to later work of the same stream only
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        workspace = torch.empty(nbytes, dtype=_U8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
+    _dev(workspace, "workspace")
+    have = workspace.numel() * workspace.element_size()
+    if have < nbytes or workspace.device != device:
+        raise BitLinearError(f"workspace holds {have} bytes on {workspace.device}, {nbytes} needed on {device}")
+    return workspace, workspace.data_ptr(), have
 
 
+@functools.lru_cache(maxsize=4096)
 def attention_workspace_size(dtype: torch.dtype, m: int, q_heads: int, kv_heads: int, head_dim: int, seqs: int) -> int:
-    code = _F32 if dtype == torch.float32 else _BF16 if dtype == torch.bfloat16 else -1
-    return int(load_library().bitlinear_attention_workspace_size(code, m, q_heads, kv_heads, head_dim, seqs))
+    return int(load_library().bitlinear_attention_workspace_size(_ACT.get(dtype, -1), m, q_heads, kv_heads, head_dim, seqs))
 
 
-@_on_its_device
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
               scale: float | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Causal attention over packed prompts. q [m][q_heads][head_dim], k and v [m][kv_heads][head_dim]
     (fp32 or bf16, possibly slices of one projection's rows), cu_seqlens int32 [seqs + 1]
     -> [m][q_heads * head_dim] of q's type. Rows outside the sequences are not written."""
+    if (other := _elsewhere(q, "q")) is not None:
+        with torch.cuda.device(other):
+            return attention(q, k, v, cu_seqlens, scale=scale, out=out, workspace=workspace)
     lib = load_library()
-    qp, qs = _heads(q, "q")
-    dtype = _act_dtype(q)
-    kp, ks = _heads(k, "k", q)
-    vp, vs = _heads(v, "v", q)
+    dtype, device = q.dtype, q.get_device()
+    qp, qs = _heads(q, "q", dtype, device)
+    kp, ks = _heads(k, "k", dtype, device)
+    vp, vs = _heads(v, "v", dtype, device)
     m, hq, d = q.shape
-    hkv = k.shape[1]
-    if k.shape != (m, hkv, d) or v.shape != k.shape:
+    mk, hkv, dk = k.shape
+    if mk != m or dk != d or v.shape != k.shape:
         raise BitLinearError(f"k and v must be [{m}][kv_heads][{d}], got {tuple(k.shape)} and {tuple(v.shape)}")
-    cu, seqs = _starts(cu_seqlens, q.device)
+    cu, seqs = _starts(cu_seqlens, device)
+    code = _act_dtype(q)
     if out is None:
-        out = torch.empty((m, hq * d), dtype=q.dtype, device=q.device)
+        out = torch.empty((m, hq * d), dtype=dtype, device=q.device)
+        op = out.data_ptr()
     else:
-        _check_out(out, (m, hq * d), q.dtype, "out")
-    wp, wn = _own_workspace(lib.bitlinear_attention_workspace_size(dtype, m, hq, hkv, d, seqs), workspace, q.device)
-    _check(lib.bitlinear_attention(qp, qs, kp, ks, vp, vs, dtype, m, hq, hkv, d, cu, seqs,
-                                   d ** -0.5 if scale is None else scale, out.data_ptr(), wp, wn, _stream(q.device)),
-           "bitlinear_attention")
+        op = _dense(out, "out", dtype, (m, hq * d), device)
+    need = attention_workspace_size(dtype, m, hq, hkv, d, seqs)
+    ws, wp, wn = _scratch(need, workspace, q.device)
+    status = lib.bitlinear_attention(qp, qs, kp, ks, vp, vs, code, m, hq, hkv, d, cu, seqs,
+                                     d ** -0.5 if scale is None else scale, op, wp, wn, _raw_stream(device))
+    if status:
+        _check(status, "bitlinear_attention")
     return out
 
 
-@_on_its_device
 def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
                  cu_seqlens: torch.Tensor | None = None) -> None:
     """Quantizes new tokens into the cache: row i of sequence s becomes token lens[s] + i. Without
     cu_seqlens, one row per sequence. lens is left as it is (a negative entry: an unused slot)."""
+    if (other := _elsewhere(k, "k")) is not None:
+        with torch.cuda.device(other):
+            return cache_append(cache, k, v, block_table, lens, cu_seqlens)
     lib = load_library()
-    kp, ks = _heads(k, "k")
-    dtype = _act_dtype(k)
-    vp, vs = _heads(v, "v", k)
+    dtype, device = k.dtype, k.get_device()
+    kp, ks = _heads(k, "k", dtype, device)
+    vp, vs = _heads(v, "v", dtype, device)
     m, heads, d = k.shape
     if v.shape != k.shape:
         raise BitLinearError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
-    (kc, vc, kscale, vscale), pages = _cache_args(cache, heads, d, k.device)
-    cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, k.device)
-    _check(lib.bitlinear_cache_append(kp, ks, vp, vs, dtype, m, heads, d, cu, lp, seqs, tp, wide, kc, vc, kscale, vscale,
-                                      pages, _stream(k.device)), "bitlinear_cache_append")
+    code = _act_dtype(k)
+    kc, vc, kscale, vscale, pages, _ = _cache_args(cache, heads, d, device)
+    cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, device)
+    status = lib.bitlinear_cache_append(kp, ks, vp, vs, code, m, heads, d, cu, lp, seqs, tp, wide, kc, vc, kscale, vscale,
+                                        pages, _raw_stream(device))
+    if status:
+        _check(status, "bitlinear_cache_append")
 
 
-@_on_its_device
 def cache_read(cache: KVCache, block_table: torch.Tensor, begin: torch.Tensor, cu_seqlens: torch.Tensor | None, m: int,
                dtype: torch.dtype = torch.float32):
     """The values of tokens begin[s] + i of every sequence, as many as cu_seqlens gives rows (m in all;
     None: one each) -> (k, v) [m][kv_heads][head_dim]. Rows outside the sequences are not written."""
+    if (other := _elsewhere(cache[0], "cache.k")) is not None:
+        with torch.cuda.device(other):
+            return cache_read(cache, block_table, begin, cu_seqlens, m, dtype)
     lib = load_library()
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype not in _ACT:
         raise BitLinearError(f"dtype must be float32 or bfloat16, got {dtype}")
-    device = cache[0].device
-    d = cache[0].shape[2] // CACHE_BLOCK if cache[0].dim() == 3 else 0
-    (kc, vc, kscale, vscale), pages = _cache_args(cache, None, d, device)
+    device = cache[0].get_device()
+    d = cache[0].shape[-1] // CACHE_BLOCK
+    kc, vc, kscale, vscale, pages, heads = _cache_args(cache, None, d, device)
     cu, bp, seqs, tp, wide = _table_args(block_table, begin, cu_seqlens, m, device, "begin")
-    heads = cache[0].shape[1]
-    k = torch.empty((m, heads, d), dtype=dtype, device=device)
-    v = torch.empty((m, heads, d), dtype=dtype, device=device)
-    _check(lib.bitlinear_cache_read(kc, vc, kscale, vscale, pages, tp, wide, cu, bp, seqs,
-                                    _F32 if dtype == torch.float32 else _BF16, m, heads, d, k.data_ptr(), v.data_ptr(),
-                                    _stream(device)), "bitlinear_cache_read")
+    k = torch.empty((m, heads, d), dtype=dtype, device=cache[0].device)
+    v = torch.empty_like(k)
+    status = lib.bitlinear_cache_read(kc, vc, kscale, vscale, pages, tp, wide, cu, bp, seqs, _ACT[dtype], m, heads, d,
+                                      k.data_ptr(), v.data_ptr(), _raw_stream(device))
+    if status:
+        _check(status, "bitlinear_cache_read")
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
 def attention_cached_workspace_size(m: int, q_heads: int, kv_heads: int, head_dim: int, seqs: int, max_blocks: int,
                                     weights: bool = False) -> int:
     return int(load_library().bitlinear_attention_cached_workspace_size(m, q_heads, kv_heads, head_dim, seqs, max_blocks,
                                                                         int(weights)))
 
 
-@_on_its_device
 def attention_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lens: torch.Tensor,
                      cu_seqlens: torch.Tensor | None = None, *, scale: float | None = None,
                      weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -583,50 +606,53 @@ def attention_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     """Attention of new tokens, already appended, over the cache: row i of sequence s is token
     lens[s] + i and sees the tokens up to itself. q [m][q_heads][head_dim] -> [m][q_heads * head_dim]
     of q's type; weights fp32 [seqs][max_blocks] gets each block's attention weight added."""
+    if (other := _elsewhere(q, "q")) is not None:
+        with torch.cuda.device(other):
+            return attention_cached(q, cache, block_table, lens, cu_seqlens, scale=scale, weights=weights, out=out,
+                                    workspace=workspace)
     lib = load_library()
-    qp, qs = _heads(q, "q")
-    dtype = _act_dtype(q)
+    dtype, device = q.dtype, q.get_device()
+    qp, qs = _heads(q, "q", dtype, device)
+    code = _act_dtype(q)
     m, hq, d = q.shape
-    (kc, vc, kscale, vscale), pages = _cache_args(cache, None, d, q.device)
-    hkv = cache[0].shape[1]
-    cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, q.device)
-    if weights is not None:
-        _check_out(weights, (seqs, wide), torch.float32, "weights")
-        if weights.device != q.device:
-            raise BitLinearError(f"weights must be on {q.device}")
+    kc, vc, kscale, vscale, pages, hkv = _cache_args(cache, None, d, device)
+    cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, device)
+    weighted = weights is not None
+    gp = _dense(weights, "weights", _F32T, (seqs, wide), device) if weighted else None
     if out is None:
-        out = torch.empty((m, hq * d), dtype=q.dtype, device=q.device)
+        out = torch.empty((m, hq * d), dtype=dtype, device=q.device)
+        op = out.data_ptr()
     else:
-        _check_out(out, (m, hq * d), q.dtype, "out")
-    need = lib.bitlinear_attention_cached_workspace_size(m, hq, hkv, d, seqs, wide, int(weights is not None))
-    wp, wn = _own_workspace(need, workspace, q.device)
-    _check(lib.bitlinear_attention_cached(qp, qs, dtype, m, hq, hkv, d, cu, lp, seqs, tp, wide, kc, vc, kscale, vscale,
-                                          pages, d ** -0.5 if scale is None else scale, out.data_ptr(),
-                                          weights.data_ptr() if weights is not None else None, wp, wn,
-                                          _stream(q.device)), "bitlinear_attention_cached")
+        op = _dense(out, "out", dtype, (m, hq * d), device)
+    need = attention_cached_workspace_size(m, hq, hkv, d, seqs, wide, weighted)
+    ws, wp, wn = _scratch(need, workspace, q.device)
+    status = lib.bitlinear_attention_cached(qp, qs, code, m, hq, hkv, d, cu, lp, seqs, tp, wide, kc, vc, kscale, vscale, pages,
+                                            d ** -0.5 if scale is None else scale, op, gp, wp, wn, _raw_stream(device))
+    if status:
+        _check(status, "bitlinear_attention_cached")
     return out
 
 
-@_on_its_device
 def cache_evict(block_table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, keep: int, *, first: int = 0,
                 recent: int = 1):
     """Chooses the blocks every sequence keeps: its first `first`, its last `recent` and, up to `keep`
     in all, those of the largest weight -> (block_table, lens, weights) of the kept blocks, and
     (evicted, evicted_count): the pages that are free now, -1 behind them."""
+    if (other := _elsewhere(block_table, "block_table")) is not None:
+        with torch.cuda.device(other):
+            return cache_evict(block_table, lens, weights, keep, first=first, recent=recent)
     lib = load_library()
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+    if block_table.dim() != 2:
         raise BitLinearError("block_table must be int32 [seqs][max_blocks]")
-    seqs, wide = block_table.shape
-    device = block_table.device
-    tp = _ints(block_table, "block_table", (seqs, wide), device)
-    lp = _ints(lens, "lens", (seqs,), device)
-    wp = _dev(weights, "weights", torch.float32)
-    if tuple(weights.shape) != (seqs, wide) or weights.device != device:
-        raise BitLinearError(f"weights must have shape {(seqs, wide)} on {device}")
-    table_out, evicted = torch.empty((2, seqs, wide), dtype=torch.int32, device=device).unbind(0)
-    lens_out, count = torch.empty((2, seqs), dtype=torch.int32, device=device).unbind(0)
-    weights_out = torch.empty((seqs, wide), dtype=torch.float32, device=device)
-    _check(lib.bitlinear_cache_evict(tp, lp, wp, seqs, wide, keep, first, recent, table_out.data_ptr(),
-                                     lens_out.data_ptr(), weights_out.data_ptr(), evicted.data_ptr(), count.data_ptr(),
-                                     _stream(device)), "bitlinear_cache_evict")
+    shape, device = block_table.shape, block_table.get_device()
+    seqs, wide = shape
+    tp = _dense(block_table, "block_table", _I32, shape, device)
+    lp = _dense(lens, "lens", _I32, (seqs,), device)
+    wp = _dense(weights, "weights", _F32T, shape, device)
+    table_out, evicted, lens_out, count, weights_out = (torch.empty_like(t) for t in (block_table, block_table, lens, lens, weights))
+    status = lib.bitlinear_cache_evict(tp, lp, wp, seqs, wide, keep, first, recent, table_out.data_ptr(),
+                                       lens_out.data_ptr(), weights_out.data_ptr(), evicted.data_ptr(), count.data_ptr(),
+                                       _raw_stream(device))
+    if status:
+        _check(status, "bitlinear_cache_evict")
     return table_out, lens_out, weights_out, evicted, count
