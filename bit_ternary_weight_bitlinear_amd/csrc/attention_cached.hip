@@ -21,7 +21,6 @@
 
 namespace bl {
 
-constexpr int kWaves = 4;
 constexpr float kDigitMax = 8355711.0f;  // 0x7F7F7F: every digit within -128..127
 
 // signed base-256 digits of an integer of at most kDigitMax: digit i in byte 0 of d[i]
@@ -41,10 +40,10 @@ __device__ inline float join_digits(v4i c)
 
 // How the pages of a sequence are split: in pages per workgroup. At least one for
 // each of its waves, and at most `splits` workgroups.
-__device__ inline int pages_per_split(int npages, int splits)
+__device__ inline int pages_per_split(int npages, int splits, int waves)
 {
     const int c = (npages + splits - 1) / splits;
-    return c < kWaves ? kWaves : c;
+    return c < waves ? waves : c;
 }
 
 __device__ inline int pages_of(int64_t have, int n, int64_t max_blocks)
@@ -57,7 +56,7 @@ struct CachedArgs {
     const void *q;
     int64_t q_stride, m;
     const int32_t *cu, *lens, *table;
-    int seqs, q_heads, kv_heads, group, splits, tiles_per_seq;
+    int seqs, q_heads, kv_heads, group, splits, waves, tiles_per_seq;
     int64_t max_blocks, pages;
     const int8_t *k_codes, *v_codes;
     const float *k_scale, *v_scale;
@@ -66,6 +65,7 @@ struct CachedArgs {
     float *part_o;    // [splits][m * q_heads][D]
     float *part_ml;   // [splits][m * q_heads][2]: reference exponent, sum
     float *stat;      // [m * q_heads][max_blocks][2]: a page's largest exponent, sum
+    float *final_ml;  // [m * q_heads][2]: a row's reference exponent, 1 / sum (0: adds no weight)
 };
 
 // tiles of 4*RT query rows: row r of a sequence is token r / group, head r % group
@@ -86,91 +86,101 @@ __device__ inline bool find_rows(const CachedArgs &a, int idx, SeqTile &t)
     }, t);
 }
 
-template <typename T, int D, int RT, bool STAT>
-__global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArgs a)
+// what a row adds to the blocks' weights: nothing if it sees nothing or is not finite
+__device__ inline float2 final_of(float top, float l) { return make_float2(top, l > 0.0f ? 1.0f / l : 0.0f); }
+
+template <typename T, int D, int RT, int W, bool STAT>
+__global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kernel(CachedArgs a)
 {
     constexpr int H = D / 64;   // matrix steps over the head width
     constexpr int N = D / 16;   // 16-dim tiles of the output
     constexpr int R = 4 * RT;   // query rows
-    // per wave: digits of p, [16 rows][16 dwords of 4 tokens]; the join at the end
-    constexpr int kDigitWords = kWaves * RT * 256, kJoinWords = kWaves * R * (D + 2);
-    __shared__ __align__(16) uint32_t lds[kDigitWords > kJoinWords ? kDigitWords : kJoinWords];
+    constexpr int E = D / 16;   // elements of a query row per thread
+    // digits of q in operand order, [row tile][step][lane][16 bytes]; per wave the
+    // digits of p, [16 rows][16 dwords of 4 tokens]; at the end the waves' results
+    constexpr int kQueryWords = RT * H * 256, kDigitWords = W * 256, kJoinWords = W * R * (D + 2);
+    constexpr int kWords = kQueryWords + kDigitWords;
+    __shared__ __align__(16) uint32_t lds[kWords > kJoinWords ? kWords : kJoinWords];
+    __shared__ float row_scale[R];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane >> 4, c = lane & 15;
     SeqTile t;
     if (!find_rows<RT>(a, blockIdx.x, t)) return;
     const int head = blockIdx.y, split = blockIdx.z;
+    const int32_t *table = a.table + (int64_t)t.seq * a.max_blocks;
+    // one split: the wave's pages do not depend on the length, which is on its way
+    int ids = -1;
+    if (a.splits == 1 && wave + W * lane < a.max_blocks) ids = table[wave + W * lane];
     const int64_t have = a.lens[t.seq];
     const int npages = pages_of(have, t.n, a.max_blocks);
-    const int chunk = pages_per_split(npages, a.splits);
+    const int chunk = pages_per_split(npages, a.splits, W);
     const int p0 = split * chunk, p1 = p0 + chunk < npages ? p0 + chunk : npages;
     if (p0 >= npages && split > 0) return;  // the join knows; split 0 writes rows that see nothing
     const int64_t rows = (int64_t)t.n * a.group;
 
-    // ---- query rows as digits. Lane (j, c) builds row c of the operand: digit
-    // c % 4 of query row c / 4, dims 16*j .. 16*j+15 of every 64.
+    // ---- query rows as digits, 16 lanes per row
+    for (int r = tid >> 4; r < R; r += 4 * W) {
+        const int64_t rj = (int64_t)t.tile * R + r;
+        const bool there = rj < rows;
+        const int tok = there ? (int)(rj / a.group) : 0, hq = head * a.group + (there ? (int)(rj % a.group) : 0);
+        const T *src = static_cast<const T *>(a.q) + (t.begin + tok) * a.q_stride + (int64_t)hq * D + E * c;
+        T raw[E];
+        if constexpr (E * sizeof(T) == 8) *reinterpret_cast<uint2 *>(raw) = *reinterpret_cast<const uint2 *>(src);
+        else
+#pragma unroll
+            for (int i = 0; i < (int)(E * sizeof(T) / 16); ++i)
+                reinterpret_cast<uint4 *>(raw)[i] = reinterpret_cast<const uint4 *>(src)[i];
+        float x[E], big = 0.0f, bad = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            x[i] = there ? to_f32(raw[i]) : 0.0f;
+            if (!(fabsf(x[i]) <= 3.402823466e38f)) {
+                bad = 1.0f;
+                x[i] = 0.0f;
+            }
+            big = fmaxf(big, fabsf(x[i]));
+        }
+        big = fmaxf(row16_max(big), 1e-30f);
+        bad = row16_max(bad);
+        const float inv = kDigitMax / big;
+        uint32_t w[3][E / 4];
+#pragma unroll
+        for (int g = 0; g < E / 4; ++g) {
+            int d[4][3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) digits3((int)rintf(fminf(fmaxf(x[4 * g + i] * inv, -kDigitMax), kDigitMax)), d[i]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) w[k][g] = pack_low_bytes(d[0][k], d[1][k], d[2][k], d[3][k]);
+        }
+        // operand lane of (row, digit k, dim): 16 * (dim % 64 / 16) + 4 * (r % 4) + k of step dim / 64
+        const int dim = E * c;
+        uint32_t *dst = lds + (((r >> 2) * H + dim / 64) * 64 + (dim % 64 / 16) * 16 + (r & 3) * 4) * 4 + dim % 16 / 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int g = 0; g < E / 4; ++g) dst[k * 4 + g] = k < 3 ? w[k < 3 ? k : 0][g] : 0u;
+        if (c == 0) row_scale[r] = bad > 0.0f ? __builtin_nanf("") : (big / kDigitMax) * a.scale;
+    }
+    uint32_t *dig = lds + kQueryWords + wave * 256;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dig[i * 64 + lane] = 0;  // rows 4j+3 stay 0
+    __syncthreads();
+    float qs[RT];          // scale of query row j of each tile
+    int64_t limit[RT];     // last token that it sees (-1: none)
+    bool poor[RT];         // it is not finite
     v4i qd[RT][H];
-    float qs[RT];          // per lane of the result: scale of query row j
-    int64_t limit[RT];     // last token that query row j sees (-1: none)
-    bool poor[RT];         // query row j is not finite
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int64_t r = (int64_t)t.tile * R + 4 * rt + (c >> 2);
-        const bool there = r < rows;
-        const int tok = there ? (int)(r / a.group) : 0, hq = head * a.group + (there ? (int)(r % a.group) : 0);
-        const T *src = static_cast<const T *>(a.q) + (t.begin + tok) * a.q_stride + (int64_t)hq * D + 16 * j;
-        float x[H][16];
-        float big = 0.0f;
-        bool ok = true;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            T raw[16];
-            constexpr int V = 16 * sizeof(T) / 16;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                reinterpret_cast<uint4 *>(raw)[i] = reinterpret_cast<const uint4 *>(src + 64 * h)[i];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[h][i] = there ? to_f32(raw[i]) : 0.0f;
-                ok = ok && fabsf(x[h][i]) <= 3.402823466e38f;
-                big = fmaxf(big, fabsf(x[h][i]));
-            }
-        }
-        big = fmaxf(big, __shfl_xor(big, 16));
-        big = fmaxf(big, __shfl_xor(big, 32));
-        const uint64_t bad = __ballot(!ok);
-        big = fmaxf(big, 1e-30f);
-        const float inv = kDigitMax / fminf(big, 3.402823466e38f);
-        const int digit = c & 3;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            uint32_t w[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                uint32_t b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float f = x[h][4 * g + i];
-                    int d[3];
-                    digits3(ok ? (int)rintf(fminf(fmaxf(f * inv, -kDigitMax), kDigitMax)) : 0, d);
-                    b[i] = digit == 0 ? d[0] : digit == 1 ? d[1] : digit == 2 ? d[2] : 0;
-                }
-                w[g] = pack_low_bytes(b[0], b[1], b[2], b[3]);
-            }
-            qd[rt][h] = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-        }
-        // the result's lane (j, c) has query row j: that is operand row 4j of lane 4j
-        const float big_j = __shfl(big, 4 * j);
-        qs[rt] = (big_j / kDigitMax) * a.scale;
         const int64_t rj = (int64_t)t.tile * R + 4 * rt + j;
         limit[rt] = rj < rows ? have + rj / a.group : -1;
-        poor[rt] = (bad & (0x000F000F000F000Full << (4 * j))) != 0;
-    }
-
-    uint32_t *dig = lds + wave * RT * 256;
+        qs[rt] = row_scale[4 * rt + j];
+        poor[rt] = !(qs[rt] == qs[rt]);
+        if (poor[rt]) qs[rt] = 0.0f;
+        if constexpr (RT == 1)
 #pragma unroll
-    for (int i = 0; i < RT * 4; ++i) dig[i * 64 + lane] = 0;  // row 4j+3 of every tile stays 0
+            for (int h = 0; h < H; ++h) qd[rt][h] = *reinterpret_cast<const v4i *>(lds + (h * 64 + lane) * 4);
+    }
 
     float mx[RT], sum[RT], acc[RT][N];
 #pragma unroll
@@ -181,75 +191,87 @@ __global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArg
         for (int n = 0; n < N; ++n) acc[rt][n] = 0.0f;
     }
 
-    const int32_t *table = a.table + (int64_t)t.seq * a.max_blocks;
-    for (int p = p0 + wave; p < p1; p += kWaves) {
-        const int64_t id = table[p];
-        const bool there = id >= 0 && id < a.pages;
-        const int64_t at = (there ? id : 0) * a.kv_heads + head;
-        const uint4 *kp = reinterpret_cast<const uint4 *>(a.k_codes + at * (kBlock * D)) + lane;
-        const uint4 *vp = reinterpret_cast<const uint4 *>(a.v_codes + at * (kBlock * D)) + lane;
-        v4i kf[4][H], vf[N];
+    for (int base = p0 + wave; base < p1; base += 64 * W) {
+        // ids and scales of the wave's next 64 pages, one per lane
+        const int mine = base + W * lane;
+        if (a.splits > 1 || base != wave) ids = mine < p1 ? table[mine] : -1;
+        const bool ok = mine < p1 && ids >= 0 && ids < a.pages;
+        const int64_t my_at = ok ? (int64_t)ids * a.kv_heads + head : 0;
+        const float my_ks = a.k_scale[my_at], my_vs = a.v_scale[my_at];
+        for (int p = base, i = 0; p < p1 && i < 64; p += W, ++i) {
+            const int id = __builtin_amdgcn_readlane(ids, i);
+            const bool there = id >= 0 && id < a.pages;
+            const int64_t at = (int64_t)(there ? id : 0) * a.kv_heads + head;
+            const uint4 *kp = reinterpret_cast<const uint4 *>(a.k_codes + at * (kBlock * D)) + lane;
+            const uint4 *vp = reinterpret_cast<const uint4 *>(a.v_codes + at * (kBlock * D)) + lane;
+            v4i kf[4][H], vf[N];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
+            for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-            for (int h = 0; h < H; ++h) kf[tt][h] = *reinterpret_cast<const v4i *>(kp + (tt * H + h) * 64);
+                for (int h = 0; h < H; ++h) kf[tt][h] = *reinterpret_cast<const v4i *>(kp + (tt * H + h) * 64);
 #pragma unroll
-        for (int n = 0; n < N; ++n) vf[n] = *reinterpret_cast<const v4i *>(vp + n * 64);
-        const float ks = a.k_scale[at] / 127.0f, vs = a.v_scale[at] / 127.0f;
+            for (int n = 0; n < N; ++n) vf[n] = *reinterpret_cast<const v4i *>(vp + n * 64);
+            const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_ks), i)) / 127.0f;
+            const float vs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_vs), i)) / 127.0f;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float x[4];
-            float big = kNegInf;
-            const float f = qs[rt] * ks;
+            for (int rt = 0; rt < RT; ++rt) {
+                if constexpr (RT > 1)
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                v4i s = {0, 0, 0, 0};
+                    for (int h = 0; h < H; ++h) qd[rt][h] = *reinterpret_cast<const v4i *>(lds + ((rt * H + h) * 64 + lane) * 4);
+                float x[4];
+                float big = kNegInf;
+                const float f = qs[rt] * ks;
 #pragma unroll
-                for (int h = 0; h < H; ++h) s = __builtin_amdgcn_mfma_i32_16x16x64_i8(qd[rt][h], kf[tt][h], s, 0, 0, 0);
-                const bool seen = there && (int64_t)p * kBlock + 4 * c + tt <= limit[rt];
-                x[tt] = seen ? join_digits(s) * f : kNegInf;
-                big = fmaxf(big, x[tt]);
-            }
-            big = row16_max(big);
-            const float ref = big == kNegInf ? 0.0f : big;
-            float total = 0.0f;
-            uint32_t b[4][3];
+                for (int tt = 0; tt < 4; ++tt) {
+                    v4i s = {0, 0, 0, 0};
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                const float e = __builtin_amdgcn_exp2f(x[tt] - ref);
-                total += e;
-                int d[3];
-                digits3((int)rintf(e * kDigitMax), d);
-                b[tt][0] = d[0];
-                b[tt][1] = d[1];
-                b[tt][2] = d[2];
-            }
-            total = row16_sum(total);
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                dig[rt * 256 + (4 * j + i) * 16 + c] = pack_low_bytes(b[0][i], b[1][i], b[2][i], b[3][i]);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            const v4i pd = *reinterpret_cast<const v4i *>(&dig[rt * 256 + c * 16 + 4 * j]);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            if (STAT && c == 0) {
-                const int64_t rj = (int64_t)t.tile * R + 4 * rt + j;
-                if (rj < rows) {
-                    const int64_t row = (t.begin + rj / a.group) * a.q_heads + head * a.group + rj % a.group;
-                    reinterpret_cast<float2 *>(a.stat)[row * a.max_blocks + p] = make_float2(big, poor[rt] ? 0.0f : total);
+                    for (int h = 0; h < H; ++h) s = __builtin_amdgcn_mfma_i32_16x16x64_i8(qd[rt][h], kf[tt][h], s, 0, 0, 0);
+                    const bool seen = there && (int64_t)p * kBlock + 4 * c + tt <= limit[rt];
+                    x[tt] = seen ? join_digits(s) * f : kNegInf;
+                    big = fmaxf(big, x[tt]);
                 }
-            }
-            const float now = fmaxf(mx[rt], big);
-            const float base = now == kNegInf ? 0.0f : now;
-            const float keep = __builtin_amdgcn_exp2f(mx[rt] - base), add = __builtin_amdgcn_exp2f(big - base);
-            mx[rt] = now;
-            sum[rt] = __builtin_fmaf(sum[rt], keep, total * add);
-            const float g = add * vs * (1.0f / kDigitMax);
+                big = row16_max(big);
+                const float ref = big == kNegInf ? 0.0f : big;
+                float total = 0.0f;
+                uint32_t b[4][3];
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const v4i o = __builtin_amdgcn_mfma_i32_16x16x64_i8(pd, vf[n], v4i{0, 0, 0, 0}, 0, 0, 0);
-                acc[rt][n] = __builtin_fmaf(acc[rt][n], keep, join_digits(o) * g);
+                for (int tt = 0; tt < 4; ++tt) {
+                    const float e = __builtin_amdgcn_exp2f(x[tt] - ref);
+                    total += e;
+                    int d[3];
+                    digits3((int)rintf(e * kDigitMax), d);
+                    b[tt][0] = d[0];
+                    b[tt][1] = d[1];
+                    b[tt][2] = d[2];
+                }
+                total = row16_sum(total);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    dig[(4 * j + k) * 16 + c] = pack_low_bytes(b[0][k], b[1][k], b[2][k], b[3][k]);
+                // the lanes of a wave exchange through LDS, which serves them in order
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                const v4i pd = *reinterpret_cast<const v4i *>(&dig[c * 16 + 4 * j]);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                if (STAT && c == 0) {
+                    const int64_t rj = (int64_t)t.tile * R + 4 * rt + j;
+                    if (rj < rows) {
+                        const int64_t row = (t.begin + rj / a.group) * a.q_heads + head * a.group + rj % a.group;
+                        reinterpret_cast<float2 *>(a.stat)[row * a.max_blocks + p] = make_float2(big, total);
+                    }
+                }
+                const float now = fmaxf(mx[rt], big);
+                const float to = now == kNegInf ? 0.0f : now;
+                const float keep = __builtin_amdgcn_exp2f(mx[rt] - to), add = __builtin_amdgcn_exp2f(big - to);
+                mx[rt] = now;
+                sum[rt] = __builtin_fmaf(sum[rt], keep, total * add);
+                const float g = add * vs * (1.0f / kDigitMax);
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const v4i o = __builtin_amdgcn_mfma_i32_16x16x64_i8(pd, vf[n], v4i{0, 0, 0, 0}, 0, 0, 0);
+                    acc[rt][n] = __builtin_fmaf(acc[rt][n], keep, join_digits(o) * g);
+                }
             }
         }
     }
@@ -257,7 +279,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArg
     // ---- join the waves, in wave order
     __syncthreads();
     float *jo = reinterpret_cast<float *>(lds);              // [wave][row][D]
-    float *jm = jo + kWaves * R * D;                         // [wave][row][2]
+    float *jm = jo + W * R * D;                              // [wave][row][2]
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int r = wave * R + 4 * rt + j;
@@ -270,45 +292,44 @@ __global__ __launch_bounds__(64 * kWaves) void attention_cached_kernel(CachedArg
     }
     __syncthreads();
     const int64_t total_rows = a.m * a.q_heads;
-    for (int it = tid; it < R * D; it += 64 * kWaves) {
+    for (int it = tid; it < R * D; it += 64 * W) {
         const int r = it / D, dim = it % D;
         const int64_t rj = (int64_t)t.tile * R + r;
         if (rj >= rows) break;
         float top = kNegInf;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, jm[2 * (w * R + r)]);
-        const float base = top == kNegInf ? 0.0f : top;
+        for (int w = 0; w < W; ++w) top = fmaxf(top, jm[2 * (w * R + r)]);
+        const float to = top == kNegInf ? 0.0f : top;
         float o = 0.0f, l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float f = __builtin_amdgcn_exp2f(jm[2 * (w * R + r)] - base);
+        for (int w = 0; w < W; ++w) {
+            const float f = __builtin_amdgcn_exp2f(jm[2 * (w * R + r)] - to);
             o = __builtin_fmaf(f, jo[(w * R + r) * D + dim], o);
             l = __builtin_fmaf(f, jm[2 * (w * R + r) + 1], l);
         }
         const int64_t row = (t.begin + rj / a.group) * a.q_heads + head * a.group + rj % a.group;
         if (a.splits > 1) {
             a.part_o[((int64_t)split * total_rows + row) * D + dim] = o;
+            if (dim == 0) reinterpret_cast<float2 *>(a.part_ml)[(int64_t)split * total_rows + row] = make_float2(top, l);
         } else {
             store_out(static_cast<T *>(a.out) + row * D + dim, l == 0.0f ? 0.0f : o / l);
-        }
-        if (dim == 0 && a.part_ml) {
-            a.part_ml[2 * ((int64_t)split * total_rows + row)] = top;
-            a.part_ml[2 * ((int64_t)split * total_rows + row) + 1] = l;
+            if (STAT && dim == 0) reinterpret_cast<float2 *>(a.final_ml)[row] = final_of(top, l);
         }
     }
 }
 
-// Joins the splits: one workgroup per query row, its waves take the splits in
-// turn and meet in LDS.
+// Joins the splits: one workgroup per query row. The splits' sums become factors in
+// LDS; then every thread adds one dim of every other split (or fourth, of 64 dims),
+// all loads independent.
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kWaves) void attention_join_kernel(CachedArgs a)
+__global__ __launch_bounds__(256) void attention_join_kernel(CachedArgs a)
 {
-    constexpr int E = D / 64;
-    __shared__ float jo[kWaves][D];
-    __shared__ float jm[kWaves][2];
+    constexpr int G = 256 / D;
+    __shared__ float factor[256];
+    __shared__ float red[8], jo[256];
     SeqTile t;
     const int64_t row = blockIdx.x;
-    const int tok = (int)(row / a.q_heads), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int tok = (int)(row / a.q_heads), tid = threadIdx.x, wave = tid >> 6;
     if (!a.cu) {
         t.seq = tok;
         t.n = 1;
@@ -319,97 +340,68 @@ __global__ __launch_bounds__(64 * kWaves) void attention_join_kernel(CachedArgs 
     }
     const int64_t have = a.lens[t.seq];
     if (have < 0) return;
-    const int npages = pages_of(have, t.n, a.max_blocks), chunk = pages_per_split(npages, a.splits);
+    const int npages = pages_of(have, t.n, a.max_blocks), chunk = pages_per_split(npages, a.splits, a.waves);
     const int parts = npages <= chunk ? 1 : (npages + chunk - 1) / chunk;
     const int64_t total_rows = a.m * a.q_heads;
-    float mx = kNegInf, l = 0.0f, o[E] = {};
-    for (int s = wave; s < parts; s += kWaves) {
-        const int64_t at = s * total_rows + row;
-        const float pm = a.part_ml[2 * at], pl = a.part_ml[2 * at + 1];
-        float po[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) po[e] = a.part_o[at * D + e * 64 + lane];
-        const float now = fmaxf(mx, pm), base = now == kNegInf ? 0.0f : now;
-        const float keep = __builtin_amdgcn_exp2f(mx - base), add = __builtin_amdgcn_exp2f(pm - base);
-        mx = now;
-        l = __builtin_fmaf(l, keep, pl * add);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(o[e], keep, po[e] * add);
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) jo[wave][e * 64 + lane] = o[e];
-    if (lane == 0) {
-        jm[wave][0] = mx;
-        jm[wave][1] = l;
-    }
+    float2 ml = make_float2(kNegInf, 0.0f);
+    if (tid < parts) ml = reinterpret_cast<const float2 *>(a.part_ml)[tid * total_rows + row];
+    const float wave_top = wave_max(ml.x);
+    if ((tid & 63) == 0) red[wave] = wave_top;
     __syncthreads();
-    if ((int)threadIdx.x >= D) return;
-    float top = kNegInf;
+    const float top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float f = tid < parts ? __builtin_amdgcn_exp2f(ml.x - (top == kNegInf ? 0.0f : top)) : 0.0f;
+    factor[tid] = f;
+    float l = f * ml.y;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, jm[w][0]);
-    const float base = top == kNegInf ? 0.0f : top;
-    float out = 0.0f, all = 0.0f;
+    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+    if ((tid & 63) == 0) red[4 + wave] = l;
+    __syncthreads();
+    l = (red[4] + red[5]) + (red[6] + red[7]);
+    const int dim = tid % D;
+    const float *src = a.part_o + row * D + dim;
+    float o = 0.0f;
+#pragma unroll 8
+    for (int s = tid / D; s < parts; s += G) o = __builtin_fmaf(factor[s], src[s * total_rows * D], o);
+    jo[tid] = o;
+    __syncthreads();
+    if (tid >= D) return;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(jm[w][0] - base);
-        out = __builtin_fmaf(f, jo[w][threadIdx.x], out);
-        all = __builtin_fmaf(f, jm[w][1], all);
-    }
-    store_out(static_cast<T *>(a.out) + row * D + threadIdx.x, all == 0.0f ? 0.0f : out / all);
+    for (int g = 1; g < G; ++g) o += jo[g * D + tid];
+    store_out(static_cast<T *>(a.out) + row * D + tid, l == 0.0f ? 0.0f : o / l);
+    if (a.stat && tid == 0) reinterpret_cast<float2 *>(a.final_ml)[row] = final_of(top, l);
 }
 
-// Adds each block's attention weight: one workgroup per sequence and 256 blocks.
-// The rows' final exponents and sums are joined from the splits again (a few
-// hundred values) rather than in a launch of their own.
-__global__ __launch_bounds__(256) void attention_weights_kernel(CachedArgs a, float *__restrict__ weights)
+// Adds each block's attention weight: 64 blocks of a sequence per workgroup, the
+// rows split over its waves and their sums met in LDS, in a fixed order.
+constexpr int kWeightWaves = 8;
+__global__ __launch_bounds__(64 * kWeightWaves) void attention_weights_kernel(CachedArgs a, float *__restrict__ weights)
 {
-    __shared__ float2 fin[64];
-    const int s = blockIdx.x, tid = threadIdx.x;
+    __shared__ float part[kWeightWaves][64];
+    const int s = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int64_t begin;
     int n;
     seq_rows(a.cu, s, a.m, begin, n);
     const int64_t have = a.lens[s];
     if (have < 0 || n == 0) return;
-    const int npages = pages_of(have, n, a.max_blocks), chunk = pages_per_split(npages, a.splits);
-    const int parts = npages <= chunk ? 1 : (npages + chunk - 1) / chunk;
-    const int p = blockIdx.y * 256 + tid;
-    if ((int)blockIdx.y * 256 >= npages) return;
-    const int64_t total_rows = a.m * a.q_heads, row0 = begin * a.q_heads, rows = (int64_t)n * a.q_heads;
+    const int npages = pages_of(have, n, a.max_blocks), p = blockIdx.y * 64 + lane;
+    if ((int)blockIdx.y * 64 >= npages) return;
+    const int64_t row0 = begin * a.q_heads, rows = (int64_t)n * a.q_heads;
     float w = 0.0f;
-    for (int64_t r0 = 0; r0 < rows; r0 += 64) {
-        __syncthreads();
-        // four threads of a quad share a row's splits
-        const int64_t r = r0 + (tid >> 2);
-        float mx = kNegInf, l = 0.0f;
-        if (r < rows) {
-            for (int i = tid & 3; i < parts; i += 4) {
-                const int64_t at = i * total_rows + row0 + r;
-                const float pm = a.part_ml[2 * at], pl = a.part_ml[2 * at + 1];
-                const float now = fmaxf(mx, pm), base = now == kNegInf ? 0.0f : now;
-                l = __builtin_fmaf(l, __builtin_amdgcn_exp2f(mx - base), pl * __builtin_amdgcn_exp2f(pm - base));
-                mx = now;
-            }
-        }
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-            const float om = __shfl_xor(mx, d), ol = __shfl_xor(l, d);
-            const float now = fmaxf(mx, om), base = now == kNegInf ? 0.0f : now;
-            l = l * __builtin_amdgcn_exp2f(mx - base) + ol * __builtin_amdgcn_exp2f(om - base);
-            mx = now;
-        }
-        // a row that is not finite, or sees nothing, adds nothing
-        if ((tid & 3) == 0) fin[tid >> 2] = make_float2(mx, l > 0.0f ? 1.0f / l : 0.0f);
-        __syncthreads();
-        const int here = rows - r0 < 64 ? (int)(rows - r0) : 64;
-        if (p < npages) {
-            for (int i = 0; i < here; ++i) {
-                const float2 st = reinterpret_cast<const float2 *>(a.stat)[(row0 + r0 + i) * a.max_blocks + p];
-                const float2 f = fin[i];
-                if (f.y > 0.0f && st.y > 0.0f) w = __builtin_fmaf(st.y * f.y, __builtin_amdgcn_exp2f(st.x - f.x), w);
-            }
+    if (p < npages) {
+#pragma unroll 4
+        for (int64_t r = wave; r < rows; r += kWeightWaves) {
+            const float2 fin = reinterpret_cast<const float2 *>(a.final_ml)[row0 + r];
+            const float2 st = reinterpret_cast<const float2 *>(a.stat)[(row0 + r) * a.max_blocks + p];
+            const float add = st.y * fin.y * __builtin_amdgcn_exp2f(st.x - fin.x);
+            w += fin.y > 0.0f && st.y > 0.0f ? add : 0.0f;
         }
     }
-    if (p < npages) weights[(int64_t)s * a.max_blocks + p] += w;
+    part[wave][lane] = w;
+    __syncthreads();
+    if (wave || p >= npages) return;
+#pragma unroll
+    for (int i = 1; i < kWeightWaves; ++i) w += part[i][lane];
+    weights[(int64_t)s * a.max_blocks + p] += w;
 }
 
 // ---------------------------------------------------------------- launcher
@@ -424,32 +416,50 @@ static int64_t query_tiles(const CachedProblem &p, int rt)
     return p.packed ? p.m * group / r + p.seqs : p.seqs * ceil_div(group, r);
 }
 
-// Workgroups wanted: four per CU, so that 16 waves of a CU keep their pages in
-// flight. Splits beyond one page per wave would stay empty.
-constexpr int64_t kWantedGroups = 1024;
-static int64_t split_count(const CachedProblem &p, int rt)
+// Waves per workgroup, and workgroups per sequence, head and tile of query rows
+// (a unit). 16 waves per workgroup (as many as their results fit LDS for: 16 / RT)
+// are a CU's share for 4 query rows, and need few or no launches to join:
+//  - no more blocks than four per wave: one workgroup per unit, no joining launch
+//    (one sequence of 1023 tokens, 20/5 heads: 6.8 us; split over 4: 10.0);
+//  - up to one unit per CU: as many workgroups as give every CU 16 waves, but at
+//    least a page per wave;
+//  - between one and one and a half, where whole workgroups would leave the second
+//    round half empty: four waves, split for a thousand workgroups (35 sequences of
+//    7800 tokens, 32/8 heads: 107 against 122 us);
+//  - two and more: one workgroup per unit, of four waves, which even out unequal
+//    lengths (200 sequences of 2000: 118 against 124 us; 64 of 7800: 168 and 167).
+struct Shape {
+    int waves;
+    int64_t splits;
+};
+static Shape launch_shape(const CachedProblem &p, int rt)
 {
-    const int64_t units = query_tiles(p, rt) * p.kv_heads;
-    const int64_t most = ceil_div(p.max_blocks, kWaves);
-    int64_t s = kWantedGroups / units;
-    if (s > most) s = most;
-    if (s > 256) s = 256;
-    return s < 1 ? 1 : s;
+    const int64_t units = query_tiles(p, rt) * p.kv_heads, cus = 256;
+    const bool wide = units <= cus || (2 * units >= 3 * cus && units < 2 * cus);
+    const int waves = wide ? 16 / rt : 4;
+    if (p.max_blocks <= 4 * waves) return {waves, 1};
+    int64_t s = 16 * cus / (waves * units);
+    const int64_t most = ceil_div(p.max_blocks, waves);
+    s = s > most ? most : s;
+    if (units >= 2 * cus || s < 1) s = 1;
+    return {waves, s > 256 ? 256 : s};
 }
 
 struct CachedLayout {
-    int64_t part_o, part_ml, stat, bytes;
+    int64_t part_ml, stat, final_ml, bytes;
 };
 static CachedLayout cached_layout(const CachedProblem &p)
 {
-    const int64_t splits = split_count(p, row_tiles(!p.packed, p.q_heads / p.kv_heads)), rows = p.m * p.q_heads;
+    const int64_t splits = launch_shape(p, row_tiles(!p.packed, p.q_heads / p.kv_heads)).splits, rows = p.m * p.q_heads;
     CachedLayout L{};
     int64_t off = 0;
     if (splits > 1) off += round_up(splits * rows * p.head_dim * 4, 256);
     L.part_ml = off;
-    if (splits > 1 || p.want_weights) off += round_up(splits * rows * 8, 256);
+    if (splits > 1) off += round_up(splits * rows * 8, 256);
     L.stat = off;
     if (p.want_weights) off += round_up(rows * p.max_blocks * 8, 256);
+    L.final_ml = off;
+    if (p.want_weights) off += round_up(rows * 8, 256);
     L.bytes = off;
     return L;
 }
@@ -460,29 +470,41 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
 {
     const int64_t group = p.q_heads / p.kv_heads;
     const int rt = row_tiles(!p.packed, group);
+    const Shape shape = launch_shape(p, rt);
     const CachedLayout L = cached_layout(p);
     char *base = static_cast<char *>(ws);
     CachedArgs a{};
     a.q = p.q; a.q_stride = p.q_stride; a.m = p.m;
     a.cu = p.cu; a.lens = p.lens; a.table = p.table;
     a.seqs = (int)p.seqs; a.q_heads = (int)p.q_heads; a.kv_heads = (int)p.kv_heads; a.group = (int)group;
-    a.splits = (int)split_count(p, rt);
+    a.splits = (int)shape.splits;
+    a.waves = shape.waves;
     a.tiles_per_seq = (int)ceil_div(group, 4 * rt);
     a.max_blocks = p.max_blocks; a.pages = p.pages;
     a.k_codes = p.k_codes; a.v_codes = p.v_codes; a.k_scale = p.k_scale; a.v_scale = p.v_scale;
     a.scale = p.scale * kLog2e; a.out = p.out;
-    a.part_o = a.splits > 1 ? reinterpret_cast<float *>(base) : nullptr;
-    a.part_ml = a.splits > 1 || p.weights ? reinterpret_cast<float *>(base + L.part_ml) : nullptr;
-    a.stat = p.weights ? reinterpret_cast<float *>(base + L.stat) : nullptr;
+    if (a.splits > 1) {
+        a.part_o = reinterpret_cast<float *>(base);
+        a.part_ml = reinterpret_cast<float *>(base + L.part_ml);
+    }
+    if (p.weights) {
+        a.stat = reinterpret_cast<float *>(base + L.stat);
+        a.final_ml = reinterpret_cast<float *>(base + L.final_ml);
+    }
 
     const dim3 grid((unsigned)query_tiles(p, rt), (unsigned)p.kv_heads, (unsigned)a.splits);
-    auto go = [&](auto type, auto width, auto tiles) {
+    auto go_waves = [&](auto type, auto width, auto tiles, auto waves) {
         using T = decltype(type);
-        constexpr int D = decltype(width)::value, RT = decltype(tiles)::value;
-        if (p.weights) hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, true>), grid, dim3(64 * kWaves), 0, st, a);
-        else hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, false>), grid, dim3(64 * kWaves), 0, st, a);
+        constexpr int D = decltype(width)::value, RT = decltype(tiles)::value, W = decltype(waves)::value;
+        if (p.weights) hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, true>), grid, dim3(64 * W), 0, st, a);
+        else hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, false>), grid, dim3(64 * W), 0, st, a);
         if (a.splits > 1)
-            hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(p.m * p.q_heads)), dim3(64 * kWaves), 0, st, a);
+            hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(p.m * p.q_heads)), dim3(256), 0, st, a);
+    };
+    auto go = [&](auto type, auto width, auto tiles) {
+        constexpr int RT = decltype(tiles)::value;
+        if (shape.waves == 4) go_waves(type, width, tiles, Width<4>{});
+        else if constexpr (RT < 4) go_waves(type, width, tiles, Width<16 / RT>{});
     };
     auto go_rt = [&](auto type, auto width) {
         if (rt == 1) go(type, width, Width<1>{});
@@ -492,8 +514,8 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
     if (p.bf16) p.head_dim == 128 ? go_rt(bf16_t{}, Width<128>{}) : go_rt(bf16_t{}, Width<64>{});
     else p.head_dim == 128 ? go_rt(float{}, Width<128>{}) : go_rt(float{}, Width<64>{});
     if (p.weights)
-        hipLaunchKernelGGL(attention_weights_kernel, dim3((unsigned)p.seqs, (unsigned)ceil_div(p.max_blocks, 256)),
-                           dim3(256), 0, st, a, p.weights);
+        hipLaunchKernelGGL(attention_weights_kernel, dim3((unsigned)p.seqs, (unsigned)ceil_div(p.max_blocks, 64)),
+                           dim3(64 * kWeightWaves), 0, st, a, p.weights);
     return hipGetLastError();
 }
 
