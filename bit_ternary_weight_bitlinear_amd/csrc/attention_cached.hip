@@ -23,19 +23,27 @@ namespace bl {
 
 constexpr float kDigitMax = 8355711.0f;  // 0x7F7F7F: every digit within -128..127
 
-// signed base-256 digits of an integer of at most kDigitMax: digit i in byte 0 of d[i]
-__device__ inline void digits3(int n, int d[3])
+// Signed base-256 digits: with 0x80 added to each, the bytes of n + 0x808080. For
+// |x| <= kDigitMax the fp32 sum x * scale + 0x808080 is at least 2^23 but for
+// x * scale < -32896, so its rounding is the one to an integer (or, there, to half
+// of one, and the conversion's): one fma and one conversion per value.
+__device__ inline uint32_t biased_digits(float x, float scale)
 {
-    d[0] = n;
-    const int n1 = (n - (int)(int8_t)n) >> 8;
-    d[1] = n1;
-    d[2] = (n1 - (int)(int8_t)n1) >> 8;
+    return (uint32_t)__builtin_fmaf(x, scale, 8421504.0f);
+}
+// digit k of four values, one per byte
+template <int K>
+__device__ inline uint32_t digit_bytes(const uint32_t n[4])
+{
+    const uint32_t lo = __builtin_amdgcn_perm(n[1], n[0], 0x0C0C0400u + 0x0101u * K);
+    const uint32_t hi = __builtin_amdgcn_perm(n[3], n[2], 0x04000C0Cu + 0x01010000u * K);
+    return (lo | hi) ^ 0x80808080u;
 }
 
-// digits' sums to one fp32 value
+// digits' sums to one fp32 value; the lower two meet exactly (|c1| <= 2^21)
 __device__ inline float join_digits(v4i c)
 {
-    return __builtin_fmaf((float)c[2], 65536.0f, __builtin_fmaf((float)c[1], 256.0f, (float)c[0]));
+    return __builtin_fmaf((float)c[2], 65536.0f, (float)(c[0] + (c[1] << 8)));
 }
 
 // How the pages of a sequence are split: in pages per workgroup. At least one for
@@ -147,11 +155,12 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
         uint32_t w[3][E / 4];
 #pragma unroll
         for (int g = 0; g < E / 4; ++g) {
-            int d[4][3];
+            uint32_t n[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) digits3((int)rintf(fminf(fmaxf(x[4 * g + i] * inv, -kDigitMax), kDigitMax)), d[i]);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) w[k][g] = pack_low_bytes(d[0][k], d[1][k], d[2][k], d[3][k]);
+            for (int i = 0; i < 4; ++i) n[i] = biased_digits(fminf(fmaxf(x[4 * g + i] * inv, -kDigitMax), kDigitMax), 1.0f);
+            w[0][g] = digit_bytes<0>(n);
+            w[1][g] = digit_bytes<1>(n);
+            w[2][g] = digit_bytes<2>(n);
         }
         // operand lane of (row, digit k, dim): 16 * (dim % 64 / 16) + 4 * (r % 4) + k of step dim / 64
         const int dim = E * c;
@@ -167,13 +176,14 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
     for (int i = 0; i < 4; ++i) dig[i * 64 + lane] = 0;  // rows 4j+3 stay 0
     __syncthreads();
     float qs[RT];          // scale of query row j of each tile
-    int64_t limit[RT];     // last token that it sees (-1: none)
+    int limit[RT];         // last token that it sees (-1: none; tokens past the table are in no page)
     bool poor[RT];         // it is not finite
     v4i qd[RT][H];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int64_t rj = (int64_t)t.tile * R + 4 * rt + j;
-        limit[rt] = rj < rows ? have + rj / a.group : -1;
+        const int64_t last = have + rj / a.group;
+        limit[rt] = rj >= rows ? -1 : last < 0x7FFFFFFF ? (int)last : 0x7FFFFFFF;
         qs[rt] = row_scale[4 * rt + j];
         poor[rt] = !(qs[rt] == qs[rt]);
         if (poor[rt]) qs[rt] = 0.0f;
@@ -221,33 +231,30 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
                 float x[4];
                 float big = kNegInf;
                 const float f = qs[rt] * ks;
+                const int last = there ? limit[rt] - p * kBlock : -1;
 #pragma unroll
                 for (int tt = 0; tt < 4; ++tt) {
                     v4i s = {0, 0, 0, 0};
 #pragma unroll
                     for (int h = 0; h < H; ++h) s = __builtin_amdgcn_mfma_i32_16x16x64_i8(qd[rt][h], kf[tt][h], s, 0, 0, 0);
-                    const bool seen = there && (int64_t)p * kBlock + 4 * c + tt <= limit[rt];
+                    const bool seen = 4 * c + tt <= last;
                     x[tt] = seen ? join_digits(s) * f : kNegInf;
                     big = fmaxf(big, x[tt]);
                 }
                 big = row16_max(big);
                 const float ref = big == kNegInf ? 0.0f : big;
                 float total = 0.0f;
-                uint32_t b[4][3];
+                uint32_t n4[4];
 #pragma unroll
                 for (int tt = 0; tt < 4; ++tt) {
                     const float e = __builtin_amdgcn_exp2f(x[tt] - ref);
                     total += e;
-                    int d[3];
-                    digits3((int)rintf(e * kDigitMax), d);
-                    b[tt][0] = d[0];
-                    b[tt][1] = d[1];
-                    b[tt][2] = d[2];
+                    n4[tt] = biased_digits(e, kDigitMax);
                 }
                 total = row16_sum(total);
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    dig[(4 * j + k) * 16 + c] = pack_low_bytes(b[0][k], b[1][k], b[2][k], b[3][k]);
+                dig[4 * j * 16 + c] = digit_bytes<0>(n4);
+                dig[(4 * j + 1) * 16 + c] = digit_bytes<1>(n4);
+                dig[(4 * j + 2) * 16 + c] = digit_bytes<2>(n4);
                 // the lanes of a wave exchange through LDS, which serves them in order
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
@@ -421,8 +428,9 @@ static int64_t query_tiles(const CachedProblem &p, int rt)
 // are a CU's share for 4 query rows, and need few or no launches to join:
 //  - no more blocks than four per wave: one workgroup per unit, no joining launch
 //    (one sequence of 1023 tokens, 20/5 heads: 6.8 us; split over 4: 10.0);
-//  - up to one unit per CU: as many workgroups as give every CU 16 waves, but at
-//    least a page per wave;
+//  - up to one unit per CU: as many workgroups as give every CU 16 waves (8 with 8
+//    query rows, whose registers allow no more; of 16 rows' workgroups about half
+//    turn out empty), but at least a page per wave;
 //  - between one and one and a half, where whole workgroups would leave the second
 //    round half empty: four waves, split for a thousand workgroups (35 sequences of
 //    7800 tokens, 32/8 heads: 107 against 122 us);
@@ -438,7 +446,7 @@ static Shape launch_shape(const CachedProblem &p, int rt)
     const bool wide = units <= cus || (2 * units >= 3 * cus && units < 2 * cus);
     const int waves = wide ? 16 / rt : 4;
     if (p.max_blocks <= 4 * waves) return {waves, 1};
-    int64_t s = 16 * cus / (waves * units);
+    int64_t s = (rt == 2 ? 8 : 16) * cus / (waves * units);
     const int64_t most = ceil_div(p.max_blocks, waves);
     s = s > most ? most : s;
     if (units >= 2 * cus || s < 1) s = 1;
