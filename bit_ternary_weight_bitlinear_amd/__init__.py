@@ -426,46 +426,44 @@ def cache_alloc(pages: int, kv_heads: int, head_dim: int, device="cuda") -> KVCa
 # One token's calls take a few microseconds on the device, so what stands before the launch counts:
 # every tensor is looked at once, and a check that fails says what it expected.
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the address alone; the public call builds a Stream object (1.5 us)
+_current_device = torch._C._cuda_getDevice
 _I32, _I8, _U8, _F32T = torch.int32, torch.int8, torch.uint8, torch.float32
 _ACT = {torch.float32: _F32, torch.bfloat16: _BF16}
+_Tensor = torch.Tensor
 
 
-def _elsewhere(t, name: str) -> int | None:
-    """The device index of a call's first tensor if it is not the current one: a kernel is launched on
-    the current device, and the stream taken for it has to be that device's."""
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, _Tensor) or (device := t.get_device()) < 0:
         raise BitLinearError(f"{name} must be a device (HIP) tensor")
-    device = t.get_device()
-    return None if device == torch.cuda.current_device() else device
+    return device
 
 
 def _heads(t: torch.Tensor, name: str, dtype, device: int):
-    """(address, elements between tokens) of q, k or v [m][heads][head_dim]: heads of a token adjacent."""
-    if not isinstance(t, torch.Tensor):
+    """(address, elements between tokens, shape) of q, k or v [m][heads][head_dim]: heads of a token adjacent."""
+    if not isinstance(t, _Tensor):
         raise BitLinearError(f"{name} must be a device (HIP) tensor")
+    if t.dtype != dtype or t.get_device() != device:
+        raise BitLinearError(f"{name} must be {dtype} on device {device}, got {t.dtype} on {t.device}")
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] != 1):
         raise BitLinearError(f"{name} must be [m][heads][head_dim] with a token's heads adjacent")
-    if t.dtype != dtype or t.get_device() != device:
-        raise BitLinearError(f"{name} must be {dtype} on device {device}, got {t.dtype} on {t.device}")
     # the stride of a single token means nothing; torch may report any
-    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2]
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2], shape
 
 
 def _dense(t: torch.Tensor, name: str, dtype, shape: tuple, device: int) -> int:
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise BitLinearError(f"{name} must be a device (HIP) tensor")
     if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        raise BitLinearError(f"{name} must be {dtype}, contiguous, of shape {shape} on device {device}; got {t.dtype}, "
+        raise BitLinearError(f"{name} must be {dtype}, contiguous, of shape {tuple(shape)} on device {device}; got {t.dtype}, "
                              f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _starts(cu, device: int):
-    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 2:
+    if not isinstance(cu, _Tensor) or len(shape := cu.shape) != 1 or shape[0] < 2:
         raise BitLinearError("cu_seqlens must be int32 [seqs + 1]")
-    n = cu.shape[0]
-    return _dense(cu, "cu_seqlens", _I32, (n,), device), n - 1
+    return _dense(cu, "cu_seqlens", _I32, shape, device), shape[0] - 1
 
 
 def _cache_args(cache, kv_heads: int | None, head_dim: int, device: int):
@@ -473,9 +471,8 @@ def _cache_args(cache, kv_heads: int | None, head_dim: int, device: int):
     if len(cache) != 4:
         raise BitLinearError("cache must be a KVCache")
     k, v, ks, vs = cache
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+    if not isinstance(k, _Tensor) or len(shape := k.shape) != 3:
         raise BitLinearError(f"cache.k must be int8 [pages][kv_heads][{CACHE_BLOCK} * head_dim]")
-    shape = k.shape
     pages, heads, width = shape
     if width != CACHE_BLOCK * head_dim or (kv_heads is not None and heads != kv_heads):
         raise BitLinearError(f"cache holds {heads} heads of {width // CACHE_BLOCK}, not {kv_heads or heads} of {head_dim}")
@@ -487,9 +484,9 @@ def _cache_args(cache, kv_heads: int | None, head_dim: int, device: int):
 def _table_args(block_table, lens, cu_seqlens, m: int, device: int, name: str = "lens"):
     """(cu, lens, seqs, table, max_blocks) of a paged call; without cu_seqlens one row per sequence."""
     cu, seqs = (None, m) if cu_seqlens is None else _starts(cu_seqlens, device)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+    if not isinstance(block_table, _Tensor) or len(shape := block_table.shape) != 2:
         raise BitLinearError("block_table must be int32 [seqs][max_blocks]")
-    wide = block_table.shape[1]
+    wide = shape[1]
     return cu, _dense(lens, name, _I32, (seqs,), device), seqs, _dense(block_table, "block_table", _I32, (seqs, wide), device), wide
 
 
@@ -518,18 +515,17 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: tor
     """Causal attention over packed prompts. q [m][q_heads][head_dim], k and v [m][kv_heads][head_dim]
     (fp32 or bf16, possibly slices of one projection's rows), cu_seqlens int32 [seqs + 1]
     -> [m][q_heads * head_dim] of q's type. Rows outside the sequences are not written."""
-    if (other := _elsewhere(q, "q")) is not None:
-        with torch.cuda.device(other):
+    device, dtype = _device_of(q, "q"), q.dtype
+    if device != _current_device():
+        with torch.cuda.device(device):
             return attention(q, k, v, cu_seqlens, scale=scale, out=out, workspace=workspace)
-    lib = load_library()
-    dtype, device = q.dtype, q.get_device()
-    qp, qs = _heads(q, "q", dtype, device)
-    kp, ks = _heads(k, "k", dtype, device)
-    vp, vs = _heads(v, "v", dtype, device)
-    m, hq, d = q.shape
-    mk, hkv, dk = k.shape
-    if mk != m or dk != d or v.shape != k.shape:
-        raise BitLinearError(f"k and v must be [{m}][kv_heads][{d}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    lib = _lib or load_library()
+    qp, qs, (m, hq, d) = _heads(q, "q", dtype, device)
+    kp, ks, shape = _heads(k, "k", dtype, device)
+    vp, vs, vshape = _heads(v, "v", dtype, device)
+    mk, hkv, dk = shape
+    if mk != m or dk != d or vshape != shape:
+        raise BitLinearError(f"k and v must be [{m}][kv_heads][{d}], got {tuple(shape)} and {tuple(vshape)}")
     cu, seqs = _starts(cu_seqlens, device)
     code = _act_dtype(q)
     if out is None:
@@ -550,16 +546,16 @@ def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: 
                  cu_seqlens: torch.Tensor | None = None) -> None:
     """Quantizes new tokens into the cache: row i of sequence s becomes token lens[s] + i. Without
     cu_seqlens, one row per sequence. lens is left as it is (a negative entry: an unused slot)."""
-    if (other := _elsewhere(k, "k")) is not None:
-        with torch.cuda.device(other):
+    device, dtype = _device_of(k, "k"), k.dtype
+    if device != _current_device():
+        with torch.cuda.device(device):
             return cache_append(cache, k, v, block_table, lens, cu_seqlens)
-    lib = load_library()
-    dtype, device = k.dtype, k.get_device()
-    kp, ks = _heads(k, "k", dtype, device)
-    vp, vs = _heads(v, "v", dtype, device)
-    m, heads, d = k.shape
-    if v.shape != k.shape:
-        raise BitLinearError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    lib = _lib or load_library()
+    kp, ks, shape = _heads(k, "k", dtype, device)
+    vp, vs, vshape = _heads(v, "v", dtype, device)
+    m, heads, d = shape
+    if vshape != shape:
+        raise BitLinearError(f"v must have shape {tuple(shape)}, got {tuple(vshape)}")
     code = _act_dtype(k)
     kc, vc, kscale, vscale, pages, _ = _cache_args(cache, heads, d, device)
     cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, device)
@@ -573,13 +569,13 @@ def cache_read(cache: KVCache, block_table: torch.Tensor, begin: torch.Tensor, c
                dtype: torch.dtype = torch.float32):
     """The values of tokens begin[s] + i of every sequence, as many as cu_seqlens gives rows (m in all;
     None: one each) -> (k, v) [m][kv_heads][head_dim]. Rows outside the sequences are not written."""
-    if (other := _elsewhere(cache[0], "cache.k")) is not None:
-        with torch.cuda.device(other):
+    device = _device_of(cache[0], "cache.k")
+    if device != _current_device():
+        with torch.cuda.device(device):
             return cache_read(cache, block_table, begin, cu_seqlens, m, dtype)
-    lib = load_library()
+    lib = _lib or load_library()
     if dtype not in _ACT:
         raise BitLinearError(f"dtype must be float32 or bfloat16, got {dtype}")
-    device = cache[0].get_device()
     d = cache[0].shape[-1] // CACHE_BLOCK
     kc, vc, kscale, vscale, pages, heads = _cache_args(cache, None, d, device)
     cu, bp, seqs, tp, wide = _table_args(block_table, begin, cu_seqlens, m, device, "begin")
@@ -606,15 +602,14 @@ def attention_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     """Attention of new tokens, already appended, over the cache: row i of sequence s is token
     lens[s] + i and sees the tokens up to itself. q [m][q_heads][head_dim] -> [m][q_heads * head_dim]
     of q's type; weights fp32 [seqs][max_blocks] gets each block's attention weight added."""
-    if (other := _elsewhere(q, "q")) is not None:
-        with torch.cuda.device(other):
+    device, dtype = _device_of(q, "q"), q.dtype
+    if device != _current_device():
+        with torch.cuda.device(device):
             return attention_cached(q, cache, block_table, lens, cu_seqlens, scale=scale, weights=weights, out=out,
                                     workspace=workspace)
-    lib = load_library()
-    dtype, device = q.dtype, q.get_device()
-    qp, qs = _heads(q, "q", dtype, device)
+    lib = _lib or load_library()
+    qp, qs, (m, hq, d) = _heads(q, "q", dtype, device)
     code = _act_dtype(q)
-    m, hq, d = q.shape
     kc, vc, kscale, vscale, pages, hkv = _cache_args(cache, None, d, device)
     cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, device)
     weighted = weights is not None
@@ -638,13 +633,13 @@ def cache_evict(block_table: torch.Tensor, lens: torch.Tensor, weights: torch.Te
     """Chooses the blocks every sequence keeps: its first `first`, its last `recent` and, up to `keep`
     in all, those of the largest weight -> (block_table, lens, weights) of the kept blocks, and
     (evicted, evicted_count): the pages that are free now, -1 behind them."""
-    if (other := _elsewhere(block_table, "block_table")) is not None:
-        with torch.cuda.device(other):
+    device, shape = _device_of(block_table, "block_table"), block_table.shape
+    if device != _current_device():
+        with torch.cuda.device(device):
             return cache_evict(block_table, lens, weights, keep, first=first, recent=recent)
-    lib = load_library()
-    if block_table.dim() != 2:
+    lib = _lib or load_library()
+    if len(shape) != 2:
         raise BitLinearError("block_table must be int32 [seqs][max_blocks]")
-    shape, device = block_table.shape, block_table.get_device()
     seqs, wide = shape
     tp = _dense(block_table, "block_table", _I32, shape, device)
     lp = _dense(lens, "lens", _I32, (seqs,), device)
