@@ -61,48 +61,70 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const T *__restrict__
                                                            int64_t pages)
 {
     constexpr int Q = D / 4;                       // 4-element pieces of a row
-    constexpr int ITER = 2 * kBlock * Q / 256;     // pieces a thread may hold
+    constexpr int ITER = kBlock * Q / 256;         // pieces of K, and of V, that a thread may hold
     __shared__ __align__(16) uint32_t codes[2][kBlock][Q];
     __shared__ float red[2][4];
     SeqTile t;
     int64_t block;
     if (!find_block(cu, lens, seqs, m, max_blocks, blockIdx.x, t, block)) return;
     const int head = blockIdx.y, heads = gridDim.y, tid = threadIdx.x;
-    const int64_t page = table[(int64_t)t.seq * max_blocks + block];
-    if (page < 0 || page >= pages) return;
+    const int64_t page = table[(int64_t)t.seq * max_blocks + block];  // waited for after the rows
     const int64_t have = lens[t.seq], t0 = block * kBlock;
     const int64_t lo = have > t0 ? have : t0, hi = have + t.n < t0 + kBlock ? have + t.n : t0 + kBlock;
     const int used = (int)(lo - t0), cnt = (int)(hi - lo), end = used + cnt;
-    const int64_t row0 = t.begin + (lo - have), at = page * heads + head;
-    const float old_k = used ? k_scale[at] : 0.0f, old_v = used ? v_scale[at] : 0.0f;
+    const int64_t row0 = t.begin + (lo - have);
 
-    // items 0 .. cnt*Q-1 are K, then as many of V
-    float x[ITER][4];
-    float mk = 0.0f, mv = 0.0f;
+    // x[0] is K, x[1] V: item i * 256 + tid is 4 elements of a row
     const int items = cnt * Q;
+    T raw[2][ITER][4];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int it = i * 256 + tid;
-        if (it >= 2 * items) continue;
-        const bool is_v = it >= items;
-        const int e = is_v ? it - items : it, tok = e / Q, piece = e % Q;
-        const T *src = (is_v ? v + (row0 + tok) * v_stride : k + (row0 + tok) * k_stride) + head * D + piece * 4;
-        float big = 0.0f;
-        T raw[4];
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(raw) = *reinterpret_cast<const float4 *>(src);
-        else *reinterpret_cast<uint2 *>(raw) = *reinterpret_cast<const uint2 *>(src);
+    for (int w = 0; w < 2; ++w) {
+        const T *src = (w ? v + row0 * v_stride : k + row0 * k_stride) + head * D;
+        const int64_t stride = w ? v_stride : k_stride;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float f = to_f32(raw[j]);
-            f = f == f ? fminf(fmaxf(f, -3.402823466e38f), 3.402823466e38f) : 0.0f;
-            x[i][j] = f;
-            big = fmaxf(big, fabsf(f));
+        for (int i = 0; i < ITER; ++i) {
+            const int it = i * 256 + tid;
+            if (it >= items) continue;
+            const T *at_row = src + (it / Q) * stride + it % Q * 4;
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(raw[w][i]) = *reinterpret_cast<const float4 *>(at_row);
+            else *reinterpret_cast<uint2 *>(raw[w][i]) = *reinterpret_cast<const uint2 *>(at_row);
         }
-        if (is_v) mv = fmaxf(mv, big);
-        else mk = fmaxf(mk, big);
     }
-    mk = wave_max(mk);
-    mv = wave_max(mv);
+    if (page < 0 || page >= pages) return;
+    const int64_t at = page * heads + head;
+    const float old_k = used ? k_scale[at] : 0.0f, old_v = used ? v_scale[at] : 0.0f;
+    float x[2][ITER][4];
+    uint32_t top[2] = {0, 0};  // largest magnitude as bits: NaN above inf above every number
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            if (i * 256 + tid >= items) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[w][i][j] = to_f32(raw[w][i][j]);
+                const uint32_t b = __float_as_uint(x[w][i][j]) & 0x7FFFFFFFu;
+                top[w] = b > top[w] ? b : top[w];
+            }
+        }
+    if (__any(top[0] > 0x7F7FFFFFu || top[1] > 0x7F7FFFFFu)) {
+        top[0] = top[1] = 0;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                if (i * 256 + tid >= items) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float f = x[w][i][j];
+                    f = f == f ? fminf(fmaxf(f, -3.402823466e38f), 3.402823466e38f) : 0.0f;
+                    x[w][i][j] = f;
+                    const uint32_t b = __float_as_uint(f) & 0x7FFFFFFFu;
+                    top[w] = b > top[w] ? b : top[w];
+                }
+            }
+    }
+    const float mk = wave_max(__uint_as_float(top[0])), mv = wave_max(__uint_as_float(top[1]));
     if ((tid & 63) == 0) {
         red[0][tid >> 6] = mk;
         red[1][tid >> 6] = mv;
@@ -118,14 +140,15 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const T *__restrict__
     const float ratio_k = old_k / sk, ratio_v = old_v / sv;
     const bool grow_k = used && ratio_k != 1.0f, grow_v = used && ratio_v != 1.0f;
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int it = i * 256 + tid;
-        if (it >= 2 * items) continue;
-        const bool is_v = it >= items;
-        const int e = is_v ? it - items : it, tok = e / Q, piece = e % Q;
-        const float inv = is_v ? inv_v : inv_k;
-        codes[is_v][used + tok][piece] = pack_low_bytes(quant_bits(x[i][0], inv), quant_bits(x[i][1], inv),
-                                                        quant_bits(x[i][2], inv), quant_bits(x[i][3], inv));
+    for (int w = 0; w < 2; ++w) {
+        const float inv = w ? inv_v : inv_k;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int it = i * 256 + tid;
+            if (it >= items) continue;
+            codes[w][used + it / Q][it % Q] = pack_low_bytes(quant_bits(x[w][i][0], inv), quant_bits(x[w][i][1], inv),
+                                                             quant_bits(x[w][i][2], inv), quant_bits(x[w][i][3], inv));
+        }
     }
     __syncthreads();
 
@@ -144,14 +167,36 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const T *__restrict__
             *dst = c;
         }
     }
-    // V: 16 tokens of a dim are one piece
+    // V: 16 tokens of a dim are one piece. Groups of 16 new tokens: 4 dims per
+    // thread, bytes transposed in registers
+    const int full0 = (used + 15) / 16, full1 = end / 16;
+    for (int it = tid; it < (full1 - full0) * Q; it += 256) {
+        const int first = 16 * (full0 + it / Q), piece = it % Q;
+        uint32_t o[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = codes[1][first + 4 * q + i][piece];
+            const uint32_t a01 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), a23 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u);
+            const uint32_t b01 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u), b23 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+            o[0][q] = __builtin_amdgcn_perm(a23, a01, 0x05040100u);
+            o[1][q] = __builtin_amdgcn_perm(a23, a01, 0x07060302u);
+            o[2][q] = __builtin_amdgcn_perm(b23, b01, 0x05040100u);
+            o[3][q] = __builtin_amdgcn_perm(b23, b01, 0x07060302u);
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            *reinterpret_cast<uint4 *>(vp + v_code_at(first, 4 * piece + d)) = make_uint4(o[d][0], o[d][1], o[d][2], o[d][3]);
+    }
+    // the others, at most one before and one behind unless the scale grew: a dim per thread
     const int g0 = grow_v ? 0 : used / 16, ng = (end + 15) / 16 - g0;
     for (int it = tid; it < ng * D; it += 256) {
         const int g = g0 + it / D, dim = it % D, first = 16 * g;
+        if (g >= full0 && g < full1) continue;
         uint4 *dst = reinterpret_cast<uint4 *>(vp + v_code_at(first, dim));
-        uint4 c;
+        uint4 c = *dst;
         int8_t *b = reinterpret_cast<int8_t *>(&c);
-        if (first < used || first + 16 > end) c = *dst;
         const int8_t *fresh = reinterpret_cast<const int8_t *>(&codes[1][0][0]) + dim;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
