@@ -1,8 +1,9 @@
 """MI355X (gfx950) BitNet b1.58 BitLinear: thin Python binding of libbitlinear.so.
 
 Every function here only marshals torch tensors (device memory) and the current
-HIP stream into the C ABI declared in include/bitlinear.h; all arithmetic runs in
-the library's HIP kernels. If the library is not built, importing works but every
+HIP stream into the C ABI declared in include/bitlinear.h (through ctypes, the
+attention calls through csrc/binding.cpp); all arithmetic runs in the library's
+HIP kernels. If the library is not built, importing works but every
 call raises -- there is no fallback.
 
 Functions mirror the C entry points:
@@ -31,7 +32,6 @@ Activations may be float32 or bfloat16 CUDA (HIP) tensors, contiguous, [m][k]; q
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import NamedTuple
 
@@ -423,91 +423,27 @@ def cache_alloc(pages: int, kv_heads: int, head_dim: int, device="cuda") -> KVCa
     return KVCache(*codes, *scales)
 
 
-# One token's calls take a few microseconds on the device, so what stands before the launch counts:
-# every tensor is looked at once, and a check that fails says what it expected.
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the address alone; the public call builds a Stream object (1.5 us)
-_current_device = torch._C._cuda_getDevice
-_I32, _I8, _U8, _F32T = torch.int32, torch.int8, torch.uint8, torch.float32
-_ACT = {torch.float32: _F32, torch.bfloat16: _BF16}
-_Tensor = torch.Tensor
+# One token's calls take a few microseconds on the device, as long as it takes to look at their
+# tensors from here: csrc/binding.cpp does that and calls the same C ABI. Its checks raise BitLinearError.
+_native = None
 
 
-def _device_of(t, name: str) -> int:
-    if not isinstance(t, _Tensor) or (device := t.get_device()) < 0:
-        raise BitLinearError(f"{name} must be a device (HIP) tensor")
-    return device
+def _attention_calls():
+    global _native
+    if _native is None:
+        load_library()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise BitLinearError(f"the binding of the attention calls is not built ({e}); run __graft_entry__.build() first") from e
+        module.bind(_LIB_PATH, BitLinearError)
+        _native = module
+    return _native
 
 
-def _heads(t: torch.Tensor, name: str, dtype, device: int):
-    """(address, elements between tokens, shape) of q, k or v [m][heads][head_dim]: heads of a token adjacent."""
-    if not isinstance(t, _Tensor):
-        raise BitLinearError(f"{name} must be a device (HIP) tensor")
-    if t.dtype != dtype or t.get_device() != device:
-        raise BitLinearError(f"{name} must be {dtype} on device {device}, got {t.dtype} on {t.device}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] != 1):
-        raise BitLinearError(f"{name} must be [m][heads][head_dim] with a token's heads adjacent")
-    # the stride of a single token means nothing; torch may report any
-    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2], shape
-
-
-def _dense(t: torch.Tensor, name: str, dtype, shape: tuple, device: int) -> int:
-    if not isinstance(t, _Tensor):
-        raise BitLinearError(f"{name} must be a device (HIP) tensor")
-    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        raise BitLinearError(f"{name} must be {dtype}, contiguous, of shape {tuple(shape)} on device {device}; got {t.dtype}, "
-                             f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _starts(cu, device: int):
-    if not isinstance(cu, _Tensor) or len(shape := cu.shape) != 1 or shape[0] < 2:
-        raise BitLinearError("cu_seqlens must be int32 [seqs + 1]")
-    return _dense(cu, "cu_seqlens", _I32, shape, device), shape[0] - 1
-
-
-def _cache_args(cache, kv_heads: int | None, head_dim: int, device: int):
-    """(K codes, V codes, K scales, V scales, pages, kv_heads)"""
-    if len(cache) != 4:
-        raise BitLinearError("cache must be a KVCache")
-    k, v, ks, vs = cache
-    if not isinstance(k, _Tensor) or len(shape := k.shape) != 3:
-        raise BitLinearError(f"cache.k must be int8 [pages][kv_heads][{CACHE_BLOCK} * head_dim]")
-    pages, heads, width = shape
-    if width != CACHE_BLOCK * head_dim or (kv_heads is not None and heads != kv_heads):
-        raise BitLinearError(f"cache holds {heads} heads of {width // CACHE_BLOCK}, not {kv_heads or heads} of {head_dim}")
-    per = (pages, heads)
-    return (_dense(k, "cache.k", _I8, shape, device), _dense(v, "cache.v", _I8, shape, device),
-            _dense(ks, "cache.k_scale", _F32T, per, device), _dense(vs, "cache.v_scale", _F32T, per, device), pages, heads)
-
-
-def _table_args(block_table, lens, cu_seqlens, m: int, device: int, name: str = "lens"):
-    """(cu, lens, seqs, table, max_blocks) of a paged call; without cu_seqlens one row per sequence."""
-    cu, seqs = (None, m) if cu_seqlens is None else _starts(cu_seqlens, device)
-    if not isinstance(block_table, _Tensor) or len(shape := block_table.shape) != 2:
-        raise BitLinearError("block_table must be int32 [seqs][max_blocks]")
-    wide = shape[1]
-    return cu, _dense(lens, name, _I32, (seqs,), device), seqs, _dense(block_table, "block_table", _I32, (seqs, wide), device), wide
-
-
-def _scratch(nbytes: int, workspace, device: torch.device):
-    """(tensor, address, bytes) of a call's workspace. The tensor is held until the launch: the caching
-    allocator hands its memory on to later work of the same stream only."""
-    if nbytes == 0:
-        return None, None, 0
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=_U8, device=device)
-        return workspace, workspace.data_ptr(), nbytes
-    _dev(workspace, "workspace")
-    have = workspace.numel() * workspace.element_size()
-    if have < nbytes or workspace.device != device:
-        raise BitLinearError(f"workspace holds {have} bytes on {workspace.device}, {nbytes} needed on {device}")
-    return workspace, workspace.data_ptr(), have
-
-
-@functools.lru_cache(maxsize=4096)
 def attention_workspace_size(dtype: torch.dtype, m: int, q_heads: int, kv_heads: int, head_dim: int, seqs: int) -> int:
-    return int(load_library().bitlinear_attention_workspace_size(_ACT.get(dtype, -1), m, q_heads, kv_heads, head_dim, seqs))
+    code = _F32 if dtype == torch.float32 else _BF16 if dtype == torch.bfloat16 else -1
+    return int(load_library().bitlinear_attention_workspace_size(code, m, q_heads, kv_heads, head_dim, seqs))
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
@@ -515,80 +451,25 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: tor
     """Causal attention over packed prompts. q [m][q_heads][head_dim], k and v [m][kv_heads][head_dim]
     (fp32 or bf16, possibly slices of one projection's rows), cu_seqlens int32 [seqs + 1]
     -> [m][q_heads * head_dim] of q's type. Rows outside the sequences are not written."""
-    device, dtype = _device_of(q, "q"), q.dtype
-    if device != _current_device():
-        with torch.cuda.device(device):
-            return attention(q, k, v, cu_seqlens, scale=scale, out=out, workspace=workspace)
-    lib = _lib or load_library()
-    qp, qs, (m, hq, d) = _heads(q, "q", dtype, device)
-    kp, ks, shape = _heads(k, "k", dtype, device)
-    vp, vs, vshape = _heads(v, "v", dtype, device)
-    mk, hkv, dk = shape
-    if mk != m or dk != d or vshape != shape:
-        raise BitLinearError(f"k and v must be [{m}][kv_heads][{d}], got {tuple(shape)} and {tuple(vshape)}")
-    cu, seqs = _starts(cu_seqlens, device)
-    code = _act_dtype(q)
-    if out is None:
-        out = torch.empty((m, hq * d), dtype=dtype, device=q.device)
-        op = out.data_ptr()
-    else:
-        op = _dense(out, "out", dtype, (m, hq * d), device)
-    need = attention_workspace_size(dtype, m, hq, hkv, d, seqs)
-    ws, wp, wn = _scratch(need, workspace, q.device)
-    status = lib.bitlinear_attention(qp, qs, kp, ks, vp, vs, code, m, hq, hkv, d, cu, seqs,
-                                     d ** -0.5 if scale is None else scale, op, wp, wn, _raw_stream(device))
-    if status:
-        _check(status, "bitlinear_attention")
-    return out
+    return (_native or _attention_calls()).attention(q, k, v, cu_seqlens, scale, out, workspace)
 
 
 def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
                  cu_seqlens: torch.Tensor | None = None) -> None:
     """Quantizes new tokens into the cache: row i of sequence s becomes token lens[s] + i. Without
     cu_seqlens, one row per sequence. lens is left as it is (a negative entry: an unused slot)."""
-    device, dtype = _device_of(k, "k"), k.dtype
-    if device != _current_device():
-        with torch.cuda.device(device):
-            return cache_append(cache, k, v, block_table, lens, cu_seqlens)
-    lib = _lib or load_library()
-    kp, ks, shape = _heads(k, "k", dtype, device)
-    vp, vs, vshape = _heads(v, "v", dtype, device)
-    m, heads, d = shape
-    if vshape != shape:
-        raise BitLinearError(f"v must have shape {tuple(shape)}, got {tuple(vshape)}")
-    code = _act_dtype(k)
-    kc, vc, kscale, vscale, pages, _ = _cache_args(cache, heads, d, device)
-    cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, device)
-    status = lib.bitlinear_cache_append(kp, ks, vp, vs, code, m, heads, d, cu, lp, seqs, tp, wide, kc, vc, kscale, vscale,
-                                        pages, _raw_stream(device))
-    if status:
-        _check(status, "bitlinear_cache_append")
+    (_native or _attention_calls()).cache_append(cache, k, v, block_table, lens, cu_seqlens)
 
 
 def cache_read(cache: KVCache, block_table: torch.Tensor, begin: torch.Tensor, cu_seqlens: torch.Tensor | None, m: int,
                dtype: torch.dtype = torch.float32):
     """The values of tokens begin[s] + i of every sequence, as many as cu_seqlens gives rows (m in all;
     None: one each) -> (k, v) [m][kv_heads][head_dim]. Rows outside the sequences are not written."""
-    device = _device_of(cache[0], "cache.k")
-    if device != _current_device():
-        with torch.cuda.device(device):
-            return cache_read(cache, block_table, begin, cu_seqlens, m, dtype)
-    lib = _lib or load_library()
-    if dtype not in _ACT:
+    if dtype not in (torch.float32, torch.bfloat16):
         raise BitLinearError(f"dtype must be float32 or bfloat16, got {dtype}")
-    d = cache[0].shape[-1] // CACHE_BLOCK
-    kc, vc, kscale, vscale, pages, heads = _cache_args(cache, None, d, device)
-    cu, bp, seqs, tp, wide = _table_args(block_table, begin, cu_seqlens, m, device, "begin")
-    k = torch.empty((m, heads, d), dtype=dtype, device=cache[0].device)
-    v = torch.empty_like(k)
-    status = lib.bitlinear_cache_read(kc, vc, kscale, vscale, pages, tp, wide, cu, bp, seqs, _ACT[dtype], m, heads, d,
-                                      k.data_ptr(), v.data_ptr(), _raw_stream(device))
-    if status:
-        _check(status, "bitlinear_cache_read")
-    return k, v
+    return (_native or _attention_calls()).cache_read(cache, block_table, begin, cu_seqlens, m, dtype == torch.bfloat16)
 
 
-@functools.lru_cache(maxsize=4096)
 def attention_cached_workspace_size(m: int, q_heads: int, kv_heads: int, head_dim: int, seqs: int, max_blocks: int,
                                     weights: bool = False) -> int:
     return int(load_library().bitlinear_attention_cached_workspace_size(m, q_heads, kv_heads, head_dim, seqs, max_blocks,
@@ -602,30 +483,7 @@ def attention_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     """Attention of new tokens, already appended, over the cache: row i of sequence s is token
     lens[s] + i and sees the tokens up to itself. q [m][q_heads][head_dim] -> [m][q_heads * head_dim]
     of q's type; weights fp32 [seqs][max_blocks] gets each block's attention weight added."""
-    device, dtype = _device_of(q, "q"), q.dtype
-    if device != _current_device():
-        with torch.cuda.device(device):
-            return attention_cached(q, cache, block_table, lens, cu_seqlens, scale=scale, weights=weights, out=out,
-                                    workspace=workspace)
-    lib = _lib or load_library()
-    qp, qs, (m, hq, d) = _heads(q, "q", dtype, device)
-    code = _act_dtype(q)
-    kc, vc, kscale, vscale, pages, hkv = _cache_args(cache, None, d, device)
-    cu, lp, seqs, tp, wide = _table_args(block_table, lens, cu_seqlens, m, device)
-    weighted = weights is not None
-    gp = _dense(weights, "weights", _F32T, (seqs, wide), device) if weighted else None
-    if out is None:
-        out = torch.empty((m, hq * d), dtype=dtype, device=q.device)
-        op = out.data_ptr()
-    else:
-        op = _dense(out, "out", dtype, (m, hq * d), device)
-    need = attention_cached_workspace_size(m, hq, hkv, d, seqs, wide, weighted)
-    ws, wp, wn = _scratch(need, workspace, q.device)
-    status = lib.bitlinear_attention_cached(qp, qs, code, m, hq, hkv, d, cu, lp, seqs, tp, wide, kc, vc, kscale, vscale, pages,
-                                            d ** -0.5 if scale is None else scale, op, gp, wp, wn, _raw_stream(device))
-    if status:
-        _check(status, "bitlinear_attention_cached")
-    return out
+    return (_native or _attention_calls()).attention_cached(q, cache, block_table, lens, cu_seqlens, scale, weights, out, workspace)
 
 
 def cache_evict(block_table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, keep: int, *, first: int = 0,
@@ -633,21 +491,4 @@ def cache_evict(block_table: torch.Tensor, lens: torch.Tensor, weights: torch.Te
     """Chooses the blocks every sequence keeps: its first `first`, its last `recent` and, up to `keep`
     in all, those of the largest weight -> (block_table, lens, weights) of the kept blocks, and
     (evicted, evicted_count): the pages that are free now, -1 behind them."""
-    device, shape = _device_of(block_table, "block_table"), block_table.shape
-    if device != _current_device():
-        with torch.cuda.device(device):
-            return cache_evict(block_table, lens, weights, keep, first=first, recent=recent)
-    lib = _lib or load_library()
-    if len(shape) != 2:
-        raise BitLinearError("block_table must be int32 [seqs][max_blocks]")
-    seqs, wide = shape
-    tp = _dense(block_table, "block_table", _I32, shape, device)
-    lp = _dense(lens, "lens", _I32, (seqs,), device)
-    wp = _dense(weights, "weights", _F32T, shape, device)
-    table_out, evicted, lens_out, count, weights_out = (torch.empty_like(t) for t in (block_table, block_table, lens, lens, weights))
-    status = lib.bitlinear_cache_evict(tp, lp, wp, seqs, wide, keep, first, recent, table_out.data_ptr(),
-                                       lens_out.data_ptr(), weights_out.data_ptr(), evicted.data_ptr(), count.data_ptr(),
-                                       _raw_stream(device))
-    if status:
-        _check(status, "bitlinear_cache_evict")
-    return table_out, lens_out, weights_out, evicted, count
+    return (_native or _attention_calls()).cache_evict(block_table, lens, weights, keep, first, recent)

@@ -1,6 +1,7 @@
 """Compile the gfx950 HIP sources into bit_ternary_weight_bitlinear_amd/libbitlinear.so
 (the product library) and libbitlinear_bench.so (the benchmark's plain read
-kernels, loaded by bench.py only).
+kernels, loaded by bench.py only), and the host-only module _binding.so, which
+marshals torch tensors to the library's attention calls.
 
 Flags: correctly rounded fp32 division, no FMA contraction, no fast-math, no
 denormal flushing (the quantizers decide integers in fp32 and must match the
@@ -11,6 +12,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ BENCH_LIB = os.path.join(HERE, "libbitlinear_bench.so")
 SOURCES = ["api.hip", "pack.hip", "act_quant.hip", "gemv.hip", "bgemv.hip", "gemm.hip", "skinny.hip",
            "sparse_down.hip", "bmma.hip", "attention.hip", "attention_cached.hip", "cache.hip"]
 BENCH_SOURCES = ["bench_read.hip"]
+BINDING = os.path.join(HERE, "_binding.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -29,6 +32,24 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
 ]
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The CPython module of the attention calls (csrc/binding.cpp, host code only)."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{base}/include", f"-I{base}/include/torch/csrc/api/include", "-I/opt/rocm/include",
+           f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp",
+           f"-L{base}/lib", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
 
 
 def build(verbose: bool = False, out_dir: str | None = None) -> str:
@@ -49,7 +70,9 @@ def build(verbose: bool = False, out_dir: str | None = None) -> str:
 
     all_src = SOURCES + BENCH_SOURCES
     with ThreadPoolExecutor(max_workers=min(len(all_src), os.cpu_count() or 1)) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = dict(zip(all_src, ex.map(compile_one, all_src)))
+    binding.result()
     for lib, srcs in ((LIB, SOURCES), (BENCH_LIB, BENCH_SOURCES)):
         cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *[objs[s] for s in srcs], "-o", lib + ".tmp"]
         if verbose:

@@ -17,9 +17,11 @@ NAN, INF = float("nan"), float("inf")
 @pytest.fixture(scope="module")
 def bl():
     import bit_ternary_weight_bitlinear_amd as m
+    from bit_ternary_weight_bitlinear_amd import build
     if not os.path.exists(m.library_path()):
-        from bit_ternary_weight_bitlinear_amd import build
         build.build()
+    elif not os.path.exists(build.BINDING):
+        build.build_binding()
     m.load_library()
     return m
 
