@@ -325,17 +325,87 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
     }
 }
 
-// Joins the splits: one workgroup per query row. The splits' sums become factors in
-// LDS; then every thread adds one dim of every other split (or fourth, of 64 dims),
-// all loads independent.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void attention_join_kernel(CachedArgs a)
+// Adds the attention weight of 64 blocks of a sequence, a block per lane and the
+// rows over the waves; their sums meet in LDS, in a fixed order. PARTS: the rows'
+// final exponents and sums are joined from the splits here (a few hundred values),
+// in the launch that joins their results, rather than in another one behind it.
+template <int W, bool PARTS>
+__device__ inline void add_weights(const CachedArgs &a, int s, int chunk64, float *weights, float2 *fin, float *part)
 {
-    constexpr int G = 256 / D;
-    __shared__ float factor[256];
-    __shared__ float red[8], jo[256];
+    constexpr int kChunkRows = 4 * W;  // 16 lanes join a row
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int64_t begin;
+    int n;
+    seq_rows(a.cu, s, a.m, begin, n);
+    const int64_t have = a.lens[s];
+    if (have < 0 || n == 0) return;
+    const int npages = pages_of(have, n, a.max_blocks), p = chunk64 * 64 + lane;
+    if (chunk64 * 64 >= npages) return;
+    const int chunk = pages_per_split(npages, a.splits, a.waves);
+    const int parts = npages <= chunk ? 1 : (npages + chunk - 1) / chunk;
+    const int64_t row0 = begin * a.q_heads, rows = (int64_t)n * a.q_heads, total_rows = a.m * a.q_heads;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml), *stat = reinterpret_cast<const float2 *>(a.stat);
+    float w = 0.0f;
+    for (int64_t r0 = 0; r0 < rows; r0 += kChunkRows) {
+        if constexpr (PARTS) {
+            const int64_t r = r0 + (tid >> 4);
+            float mx = kNegInf, l = 0.0f;
+            if (r < rows)
+                for (int i = tid & 15; i < parts; i += 16) {
+                    const float2 v = ml[i * total_rows + row0 + r];
+                    const float now = fmaxf(mx, v.x), to = now == kNegInf ? 0.0f : now;
+                    l = __builtin_fmaf(l, __builtin_amdgcn_exp2f(mx - to), v.y * __builtin_amdgcn_exp2f(v.x - to));
+                    mx = now;
+                }
+            const float top = row16_max(mx);
+            l = row16_sum(l * __builtin_amdgcn_exp2f(mx - (top == kNegInf ? 0.0f : top)));
+            __syncthreads();
+            if ((tid & 15) == 0) fin[tid >> 4] = final_of(top, l);
+            __syncthreads();
+        }
+        if (p < npages) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = r0 + wave + W * i;
+                if (r >= rows) continue;
+                const float2 f = PARTS ? fin[wave + W * i] : reinterpret_cast<const float2 *>(a.final_ml)[row0 + r];
+                const float2 st = stat[(row0 + r) * a.max_blocks + p];
+                const float add = st.y * f.y * __builtin_amdgcn_exp2f(st.x - f.x);
+                w += f.y > 0.0f && st.y > 0.0f ? add : 0.0f;
+            }
+        }
+    }
+    part[tid] = w;
+    __syncthreads();
+    if (wave || p >= npages) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) w += part[i * 64 + lane];
+    weights[(int64_t)s * a.max_blocks + p] += w;
+}
+
+__global__ __launch_bounds__(1024) void attention_weights_kernel(CachedArgs a, float *__restrict__ weights)
+{
+    __shared__ float part[1024];
+    add_weights<16, false>(a, blockIdx.x, blockIdx.y, weights, nullptr, part);
+}
+
+// Joins the splits: one workgroup per query row. The splits' sums become factors in
+// LDS; then every thread adds one dim of every fourth split (or eighth, of 64 dims),
+// all loads independent. The workgroups behind those add the blocks' weights.
+template <typename T, int D>
+__global__ __launch_bounds__(512) void attention_join_kernel(CachedArgs a, float *__restrict__ weights, int blocks64)
+{
+    constexpr int G = 512 / D;
+    __shared__ float factor[512], jo[512];
+    __shared__ float red[2][8];
+    __shared__ float2 fin[32];
+    const int64_t row = blockIdx.x, total_rows = a.m * a.q_heads;
+    if (row >= total_rows) {
+        const int w = (int)(row - total_rows);
+        add_weights<8, true>(a, w / blocks64, w % blocks64, weights, fin, jo);
+        return;
+    }
     SeqTile t;
-    const int64_t row = blockIdx.x;
     const int tok = (int)(row / a.q_heads), tid = threadIdx.x, wave = tid >> 6;
     if (!a.cu) {
         t.seq = tok;
@@ -349,21 +419,24 @@ __global__ __launch_bounds__(256) void attention_join_kernel(CachedArgs a)
     if (have < 0) return;
     const int npages = pages_of(have, t.n, a.max_blocks), chunk = pages_per_split(npages, a.splits, a.waves);
     const int parts = npages <= chunk ? 1 : (npages + chunk - 1) / chunk;
-    const int64_t total_rows = a.m * a.q_heads;
     float2 ml = make_float2(kNegInf, 0.0f);
     if (tid < parts) ml = reinterpret_cast<const float2 *>(a.part_ml)[tid * total_rows + row];
     const float wave_top = wave_max(ml.x);
-    if ((tid & 63) == 0) red[wave] = wave_top;
+    if ((tid & 63) == 0) red[0][wave] = wave_top;
     __syncthreads();
-    const float top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    float top = red[0][0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, red[0][w]);
     const float f = tid < parts ? __builtin_amdgcn_exp2f(ml.x - (top == kNegInf ? 0.0f : top)) : 0.0f;
     factor[tid] = f;
     float l = f * ml.y;
 #pragma unroll
     for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
-    if ((tid & 63) == 0) red[4 + wave] = l;
+    if ((tid & 63) == 0) red[1][wave] = l;
     __syncthreads();
-    l = (red[4] + red[5]) + (red[6] + red[7]);
+    l = red[1][0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) l += red[1][w];
     const int dim = tid % D;
     const float *src = a.part_o + row * D + dim;
     float o = 0.0f;
@@ -375,47 +448,16 @@ __global__ __launch_bounds__(256) void attention_join_kernel(CachedArgs a)
 #pragma unroll
     for (int g = 1; g < G; ++g) o += jo[g * D + tid];
     store_out(static_cast<T *>(a.out) + row * D + tid, l == 0.0f ? 0.0f : o / l);
-    if (a.stat && tid == 0) reinterpret_cast<float2 *>(a.final_ml)[row] = final_of(top, l);
-}
-
-// Adds each block's attention weight: 64 blocks of a sequence per workgroup, the
-// rows split over its waves and their sums met in LDS, in a fixed order.
-constexpr int kWeightWaves = 8;
-__global__ __launch_bounds__(64 * kWeightWaves) void attention_weights_kernel(CachedArgs a, float *__restrict__ weights)
-{
-    __shared__ float part[kWeightWaves][64];
-    const int s = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t begin;
-    int n;
-    seq_rows(a.cu, s, a.m, begin, n);
-    const int64_t have = a.lens[s];
-    if (have < 0 || n == 0) return;
-    const int npages = pages_of(have, n, a.max_blocks), p = blockIdx.y * 64 + lane;
-    if ((int)blockIdx.y * 64 >= npages) return;
-    const int64_t row0 = begin * a.q_heads, rows = (int64_t)n * a.q_heads;
-    float w = 0.0f;
-    if (p < npages) {
-#pragma unroll 4
-        for (int64_t r = wave; r < rows; r += kWeightWaves) {
-            const float2 fin = reinterpret_cast<const float2 *>(a.final_ml)[row0 + r];
-            const float2 st = reinterpret_cast<const float2 *>(a.stat)[(row0 + r) * a.max_blocks + p];
-            const float add = st.y * fin.y * __builtin_amdgcn_exp2f(st.x - fin.x);
-            w += fin.y > 0.0f && st.y > 0.0f ? add : 0.0f;
-        }
-    }
-    part[wave][lane] = w;
-    __syncthreads();
-    if (wave || p >= npages) return;
-#pragma unroll
-    for (int i = 1; i < kWeightWaves; ++i) w += part[i][lane];
-    weights[(int64_t)s * a.max_blocks + p] += w;
 }
 
 // ---------------------------------------------------------------- launcher
 
-// query rows per workgroup: 4, 8 or 16, as many as one token's group needs; more
-// tokens at once use 16
-static int row_tiles(bool one_token, int64_t group) { return one_token && group <= 4 ? 1 : one_token && group <= 8 ? 2 : 4; }
+// query rows per workgroup: 4, 8 or 16, as many as a sequence has on average
+static int row_tiles(const CachedProblem &p)
+{
+    const int64_t rows = ceil_div(p.m * (p.q_heads / p.kv_heads), p.seqs);
+    return rows <= 4 ? 1 : rows <= 8 ? 2 : 4;
+}
 
 static int64_t query_tiles(const CachedProblem &p, int rt)
 {
@@ -458,7 +500,7 @@ struct CachedLayout {
 };
 static CachedLayout cached_layout(const CachedProblem &p)
 {
-    const int64_t splits = launch_shape(p, row_tiles(!p.packed, p.q_heads / p.kv_heads)).splits, rows = p.m * p.q_heads;
+    const int64_t splits = launch_shape(p, row_tiles(p)).splits, rows = p.m * p.q_heads;
     CachedLayout L{};
     int64_t off = 0;
     if (splits > 1) off += round_up(splits * rows * p.head_dim * 4, 256);
@@ -467,7 +509,7 @@ static CachedLayout cached_layout(const CachedProblem &p)
     L.stat = off;
     if (p.want_weights) off += round_up(rows * p.max_blocks * 8, 256);
     L.final_ml = off;
-    if (p.want_weights) off += round_up(rows * 8, 256);
+    if (p.want_weights && splits == 1) off += round_up(rows * 8, 256);
     L.bytes = off;
     return L;
 }
@@ -477,7 +519,7 @@ int64_t attention_cached_workspace(const CachedProblem &p) { return cached_layou
 hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t st)
 {
     const int64_t group = p.q_heads / p.kv_heads;
-    const int rt = row_tiles(!p.packed, group);
+    const int rt = row_tiles(p);
     const Shape shape = launch_shape(p, rt);
     const CachedLayout L = cached_layout(p);
     char *base = static_cast<char *>(ws);
@@ -497,9 +539,10 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
     }
     if (p.weights) {
         a.stat = reinterpret_cast<float *>(base + L.stat);
-        a.final_ml = reinterpret_cast<float *>(base + L.final_ml);
+        if (a.splits == 1) a.final_ml = reinterpret_cast<float *>(base + L.final_ml);
     }
 
+    const int64_t blocks64 = ceil_div(p.max_blocks, 64);
     const dim3 grid((unsigned)query_tiles(p, rt), (unsigned)p.kv_heads, (unsigned)a.splits);
     auto go_waves = [&](auto type, auto width, auto tiles, auto waves) {
         using T = decltype(type);
@@ -507,7 +550,8 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
         if (p.weights) hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, true>), grid, dim3(64 * W), 0, st, a);
         else hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, false>), grid, dim3(64 * W), 0, st, a);
         if (a.splits > 1)
-            hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(p.m * p.q_heads)), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(p.m * p.q_heads + (p.weights ? p.seqs * blocks64 : 0))),
+                               dim3(512), 0, st, a, p.weights, (int)blocks64);
     };
     auto go = [&](auto type, auto width, auto tiles) {
         constexpr int RT = decltype(tiles)::value;
@@ -521,9 +565,8 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
     };
     if (p.bf16) p.head_dim == 128 ? go_rt(bf16_t{}, Width<128>{}) : go_rt(bf16_t{}, Width<64>{});
     else p.head_dim == 128 ? go_rt(float{}, Width<128>{}) : go_rt(float{}, Width<64>{});
-    if (p.weights)
-        hipLaunchKernelGGL(attention_weights_kernel, dim3((unsigned)p.seqs, (unsigned)ceil_div(p.max_blocks, 64)),
-                           dim3(64 * kWeightWaves), 0, st, a, p.weights);
+    if (p.weights && a.splits == 1)
+        hipLaunchKernelGGL(attention_weights_kernel, dim3((unsigned)p.seqs, (unsigned)blocks64), dim3(1024), 0, st, a, p.weights);
     return hipGetLastError();
 }
 
