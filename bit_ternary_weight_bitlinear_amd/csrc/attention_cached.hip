@@ -125,13 +125,22 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
     const int chunk = pages_per_split(npages, a.splits, W);
     const int p0 = split * chunk, p1 = p0 + chunk < npages ? p0 + chunk : npages;
     if (p0 >= npages && split > 0) return;  // the join knows; split 0 writes rows that see nothing
-    const int64_t rows = (int64_t)t.n * a.group;
+    // row r of the tile is query `head * group + h` of the sequence's row `tok`
+    const int64_t first = (int64_t)t.tile * R, left = (int64_t)t.n * a.group - first;
+    const int rows = left < R ? (int)left : R;
+    const int tok0 = (int)(first / a.group);
+    const uint32_t rem0 = (uint32_t)(first - (int64_t)tok0 * a.group), group = (uint32_t)a.group;
+    auto place = [&](int r, int &tok, int &hq) {
+        const uint32_t u = rem0 + (uint32_t)r, q = u / group;
+        tok = tok0 + (int)q;
+        hq = head * a.group + (int)(u - q * group);
+    };
 
     // ---- query rows as digits, 16 lanes per row
     for (int r = tid >> 4; r < R; r += 4 * W) {
-        const int64_t rj = (int64_t)t.tile * R + r;
-        const bool there = rj < rows;
-        const int tok = there ? (int)(rj / a.group) : 0, hq = head * a.group + (there ? (int)(rj % a.group) : 0);
+        const bool there = r < rows;
+        int tok, hq;
+        place(there ? r : 0, tok, hq);
         const T *src = static_cast<const T *>(a.q) + (t.begin + tok) * a.q_stride + (int64_t)hq * D + E * c;
         T raw[E];
         if constexpr (E * sizeof(T) == 8) *reinterpret_cast<uint2 *>(raw) = *reinterpret_cast<const uint2 *>(src);
@@ -178,12 +187,16 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
     float qs[RT];          // scale of query row j of each tile
     int limit[RT];         // last token that it sees (-1: none; tokens past the table are in no page)
     bool poor[RT];         // it is not finite
+    float2 *stat[RT];      // its blocks' largest exponents and sums
     v4i qd[RT][H];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int64_t rj = (int64_t)t.tile * R + 4 * rt + j;
-        const int64_t last = have + rj / a.group;
-        limit[rt] = rj >= rows ? -1 : last < 0x7FFFFFFF ? (int)last : 0x7FFFFFFF;
+        const bool there = 4 * rt + j < rows;
+        int tok, hq;
+        place(there ? 4 * rt + j : 0, tok, hq);
+        const int64_t last = have + tok;
+        limit[rt] = !there ? -1 : last < 0x7FFFFFFF ? (int)last : 0x7FFFFFFF;
+        if (STAT) stat[rt] = there ? reinterpret_cast<float2 *>(a.stat) + ((t.begin + tok) * a.q_heads + hq) * a.max_blocks : nullptr;
         qs[rt] = row_scale[4 * rt + j];
         poor[rt] = !(qs[rt] == qs[rt]);
         if (poor[rt]) qs[rt] = 0.0f;
@@ -261,13 +274,7 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
                 const v4i pd = *reinterpret_cast<const v4i *>(&dig[c * 16 + 4 * j]);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
-                if (STAT && c == 0) {
-                    const int64_t rj = (int64_t)t.tile * R + 4 * rt + j;
-                    if (rj < rows) {
-                        const int64_t row = (t.begin + rj / a.group) * a.q_heads + head * a.group + rj % a.group;
-                        reinterpret_cast<float2 *>(a.stat)[row * a.max_blocks + p] = make_float2(big, total);
-                    }
-                }
+                if (STAT && c == 0 && stat[rt]) stat[rt][p] = make_float2(big, total);
                 const float now = fmaxf(mx[rt], big);
                 const float to = now == kNegInf ? 0.0f : now;
                 const float keep = __builtin_amdgcn_exp2f(mx[rt] - to), add = __builtin_amdgcn_exp2f(big - to);
@@ -301,8 +308,7 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
     const int64_t total_rows = a.m * a.q_heads;
     for (int it = tid; it < R * D; it += 64 * W) {
         const int r = it / D, dim = it % D;
-        const int64_t rj = (int64_t)t.tile * R + r;
-        if (rj >= rows) break;
+        if (r >= rows) break;
         float top = kNegInf;
 #pragma unroll
         for (int w = 0; w < W; ++w) top = fmaxf(top, jm[2 * (w * R + r)]);
@@ -314,7 +320,9 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
             o = __builtin_fmaf(f, jo[(w * R + r) * D + dim], o);
             l = __builtin_fmaf(f, jm[2 * (w * R + r) + 1], l);
         }
-        const int64_t row = (t.begin + rj / a.group) * a.q_heads + head * a.group + rj % a.group;
+        int tok, hq;
+        place(r, tok, hq);
+        const int64_t row = (t.begin + tok) * a.q_heads + hq;
         if (a.splits > 1) {
             a.part_o[((int64_t)split * total_rows + row) * D + dim] = o;
             if (dim == 0) reinterpret_cast<float2 *>(a.part_ml)[(int64_t)split * total_rows + row] = make_float2(top, l);
