@@ -115,7 +115,7 @@ __device__ inline bool set_aside(char *tile, char *counts)
 }
 
 template <int D, int KS>
-__global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem a, int group)
+__global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem a, int group, int first_group)
 {
     constexpr int ROWS = 128 / KS, C = D / 16, DT = D / 32, NB = 2 / KS;
     constexpr int kTile = kKeys * D * 2;                  // bytes of a K or V tile
@@ -127,9 +127,9 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, col = lane & 31;
-    const int head = blockIdx.x % (int)a.kv_heads;
+    const int index = first_group + (int)blockIdx.x, head = index % (int)a.kv_heads;
     SeqTile t;
-    if (!find_tile(a.cu, (int)a.seqs, a.m, blockIdx.x / (int)a.kv_heads,
+    if (!find_tile(a.cu, (int)a.seqs, a.m, index / (int)a.kv_heads,
                    [=](int, int n) { return (int)(((int64_t)n * group + ROWS - 1) / ROWS); }, t))
         return;
     const int rows = t.n * group;
@@ -380,10 +380,10 @@ __device__ inline void split_f16(float v, _Float16 &hi, _Float16 &lo)
 // D / 4 lanes per row of K or V (blockIdx.y: 0, 1)
 template <int D>
 __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a, char *__restrict__ planes,
-                                                              float *__restrict__ scales)
+                                                              float *__restrict__ scales, int first_group)
 {
     constexpr int L = D / 4;
-    const int64_t rows = a.m * a.kv_heads, n = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const int64_t rows = a.m * a.kv_heads, n = ((int64_t)first_group + blockIdx.x) * (256 / L) + threadIdx.x / L;
     if (n >= rows) return;
     const int64_t tok = n / a.kv_heads, head = n % a.kv_heads, at = head * a.m + tok;
     const int is_v = blockIdx.y, lane = threadIdx.x % L;
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a
 // The loop of attention_bf16_kernel with the four 16-bit planes of a tile of
 // 32 * KS keys, 32 keys per wave.
 template <int D, int KS>
-__global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(AttentionProblem a, int group,
+__global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(AttentionProblem a, int group, int first_group,
                                                                             const char *__restrict__ planes,
                                                                             const float *__restrict__ scales)
 {
@@ -419,9 +419,9 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, col = lane & 31;
-    const int head = blockIdx.x % (int)a.kv_heads;
+    const int index = first_group + (int)blockIdx.x, head = index % (int)a.kv_heads;
     SeqTile t;
-    if (!find_tile(a.cu, (int)a.seqs, a.m, blockIdx.x / (int)a.kv_heads,
+    if (!find_tile(a.cu, (int)a.seqs, a.m, index / (int)a.kv_heads,
                    [=](int, int n) { return (int)(((int64_t)n * group + ROWS - 1) / ROWS); }, t))
         return;
     const int rows = t.n * group;
@@ -696,15 +696,15 @@ hipError_t launch_attention(const AttentionProblem &p, void *ws, hipStream_t st)
     float *scales = p.bf16 ? nullptr : reinterpret_cast<float *>(planes + round_up(2 * rows * p.head_dim * 4, 256));
     auto go = [&](auto width, auto splits) {
         constexpr int D = decltype(width)::value, KS = decltype(splits)::value;
-        const dim3 grid((unsigned)((p.m * group * KS / 128 + p.seqs) * p.kv_heads));
-        if (p.bf16) {
-            hipLaunchKernelGGL((attention_bf16_kernel<D, KS>), grid, dim3(256), 0, st, p, group);
-        } else {
-            hipLaunchKernelGGL((attention_split_kernel<D>), dim3((unsigned)ceil_div(rows * (D / 4), 256), 2), dim3(256), 0, st, p,
-                               planes, scales);
-            hipLaunchKernelGGL((attention_f32_kernel<D, KS>), grid, dim3(256), 0, st, p, group, (const char *)planes,
-                               (const float *)scales);
-        }
+        if (!p.bf16)
+            in_launches(ceil_div(rows * (D / 4), 256), [&](int first, unsigned n) {
+                hipLaunchKernelGGL((attention_split_kernel<D>), dim3(n, 2), dim3(256), 0, st, p, planes, scales, first);
+            });
+        in_launches((p.m * group * KS / 128 + p.seqs) * p.kv_heads, [&](int first, unsigned n) {
+            if (p.bf16) hipLaunchKernelGGL((attention_bf16_kernel<D, KS>), dim3(n), dim3(256), 0, st, p, group, first);
+            else hipLaunchKernelGGL((attention_f32_kernel<D, KS>), dim3(n), dim3(256), 0, st, p, group, first,
+                                    (const char *)planes, (const float *)scales);
+        });
     };
     const int64_t groups = (p.m * group / 128 + p.seqs) * p.kv_heads;
     const bool few = few_groups(p, groups);

@@ -70,7 +70,8 @@ __device__ inline bool find_tile(const int32_t *cu, int seqs, int64_t m, int idx
             const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)begin, w);
             t.begin = (int64_t)lo;  // at most BL_MAX_TOKENS rows
             t.n = __builtin_amdgcn_readlane(n, w);
-            return true;
+            // offsets out of order can make the counts wrap: no tile beyond its sequence
+            return t.tile >= 0 && t.tile < __builtin_amdgcn_readlane(cnt, w);
         }
         before += __builtin_amdgcn_readlane(incl, 63);
     }
@@ -106,5 +107,15 @@ __device__ inline float row16_sum(float v)
 }
 
 constexpr int kBlock = 64;  // tokens per cache page
+
+// A launch holds fewer than 2^32 threads in x: longer grids go in several launches,
+// each with the index of its first workgroup.
+constexpr int64_t kMostGroups = (int64_t)1 << 21;
+template <typename F>
+inline void in_launches(int64_t groups, F launch)
+{
+    for (int64_t first = 0; first < groups; first += kMostGroups)
+        launch((int)first, (unsigned)(groups - first < kMostGroups ? groups - first : kMostGroups));
+}
 
 }  // namespace bl

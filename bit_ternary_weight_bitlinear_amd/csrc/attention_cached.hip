@@ -15,7 +15,7 @@
 //
 // A page is one step of a wave: 8 KB of K, 8 KB of V (head_dim 128), each lane
 // 16 bytes per load, every load of a wave contiguous. Bound by HBM for up to 16
-// query rows a page: ~170 VALU operations and 16 matrix instructions per 16 KB
+// query rows a page: ~130 VALU operations and 16 matrix instructions per 16 KB
 // and four query rows.
 #include "attention.hpp"
 
@@ -24,9 +24,9 @@ namespace bl {
 constexpr float kDigitMax = 8355711.0f;  // 0x7F7F7F: every digit within -128..127
 
 // Signed base-256 digits: with 0x80 added to each, the bytes of n + 0x808080. For
-// |x| <= kDigitMax the fp32 sum x * scale + 0x808080 is at least 2^23 but for
-// x * scale < -32896, so its rounding is the one to an integer (or, there, to half
-// of one, and the conversion's): one fma and one conversion per value.
+// |x * scale| <= kDigitMax the fp32 sum x * scale + 0x808080 is at least 2^23, where
+// fp32 holds integers only, or (for x * scale < -32896) is cut to one by the
+// conversion: one fma and one conversion per value, off by less than 1.
 __device__ inline uint32_t biased_digits(float x, float scale)
 {
     return (uint32_t)__builtin_fmaf(x, scale, 8421504.0f);
@@ -98,7 +98,7 @@ __device__ inline bool find_rows(const CachedArgs &a, int idx, SeqTile &t)
 __device__ inline float2 final_of(float top, float l) { return make_float2(top, l > 0.0f ? 1.0f / l : 0.0f); }
 
 template <typename T, int D, int RT, int W, bool STAT>
-__global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kernel(CachedArgs a)
+__global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kernel(CachedArgs a, int first_tile)
 {
     constexpr int H = D / 64;   // matrix steps over the head width
     constexpr int N = D / 16;   // 16-dim tiles of the output
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane >> 4, c = lane & 15;
     SeqTile t;
-    if (!find_rows<RT>(a, blockIdx.x, t)) return;
+    if (!find_rows<RT>(a, first_tile + (int)blockIdx.x, t)) return;
     const int head = blockIdx.y, split = blockIdx.z;
     const int32_t *table = a.table + (int64_t)t.seq * a.max_blocks;
     // one split: the wave's pages do not depend on the length, which is on its way
@@ -220,7 +220,8 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
         if (a.splits > 1 || base != wave) ids = mine < p1 ? table[mine] : -1;
         const bool ok = mine < p1 && ids >= 0 && ids < a.pages;
         const int64_t my_at = ok ? (int64_t)ids * a.kv_heads + head : 0;
-        const float my_ks = a.k_scale[my_at], my_vs = a.v_scale[my_at];
+        // a block without a page reads page 0, of which nothing may enter
+        const float my_ks = ok ? a.k_scale[my_at] : 0.0f, my_vs = ok ? a.v_scale[my_at] : 0.0f;
         for (int p = base, i = 0; p < p1 && i < 64; p += W, ++i) {
             const int id = __builtin_amdgcn_readlane(ids, i);
             const bool there = id >= 0 && id < a.pages;
@@ -391,10 +392,10 @@ __device__ inline void add_weights(const CachedArgs &a, int s, int chunk64, floa
     weights[(int64_t)s * a.max_blocks + p] += w;
 }
 
-__global__ __launch_bounds__(1024) void attention_weights_kernel(CachedArgs a, float *__restrict__ weights)
+__global__ __launch_bounds__(1024) void attention_weights_kernel(CachedArgs a, float *__restrict__ weights, int first_seq)
 {
     __shared__ float part[1024];
-    add_weights<16, false>(a, blockIdx.x, blockIdx.y, weights, nullptr, part);
+    add_weights<16, false>(a, first_seq + (int)blockIdx.x, blockIdx.y, weights, nullptr, part);
 }
 
 // Joins the splits: one workgroup per query row. The splits' sums become factors in
@@ -551,12 +552,14 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
     }
 
     const int64_t blocks64 = ceil_div(p.max_blocks, 64);
-    const dim3 grid((unsigned)query_tiles(p, rt), (unsigned)p.kv_heads, (unsigned)a.splits);
     auto go_waves = [&](auto type, auto width, auto tiles, auto waves) {
         using T = decltype(type);
         constexpr int D = decltype(width)::value, RT = decltype(tiles)::value, W = decltype(waves)::value;
-        if (p.weights) hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, true>), grid, dim3(64 * W), 0, st, a);
-        else hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, false>), grid, dim3(64 * W), 0, st, a);
+        in_launches(query_tiles(p, rt), [&](int first, unsigned n) {
+            const dim3 grid(n, (unsigned)p.kv_heads, (unsigned)a.splits);
+            if (p.weights) hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, true>), grid, dim3(64 * W), 0, st, a, first);
+            else hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, false>), grid, dim3(64 * W), 0, st, a, first);
+        });
         if (a.splits > 1)
             hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(p.m * p.q_heads + (p.weights ? p.seqs * blocks64 : 0))),
                                dim3(512), 0, st, a, p.weights, (int)blocks64);
@@ -574,7 +577,9 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
     if (p.bf16) p.head_dim == 128 ? go_rt(bf16_t{}, Width<128>{}) : go_rt(bf16_t{}, Width<64>{});
     else p.head_dim == 128 ? go_rt(float{}, Width<128>{}) : go_rt(float{}, Width<64>{});
     if (p.weights && a.splits == 1)
-        hipLaunchKernelGGL(attention_weights_kernel, dim3((unsigned)p.seqs, (unsigned)blocks64), dim3(1024), 0, st, a, p.weights);
+        in_launches(p.seqs, [&](int first, unsigned n) {
+            hipLaunchKernelGGL(attention_weights_kernel, dim3(n, (unsigned)blocks64), dim3(1024), 0, st, a, p.weights, first);
+        });
     return hipGetLastError();
 }
 

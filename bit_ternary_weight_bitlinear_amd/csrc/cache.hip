@@ -282,13 +282,13 @@ __global__ __launch_bounds__(kEvictThreads) void cache_evict_kernel(
     const int32_t *__restrict__ table, const int32_t *__restrict__ lens, const float *__restrict__ weights,
     int64_t max_blocks, int64_t keep, int64_t first, int64_t recent, int32_t *__restrict__ table_out,
     int32_t *__restrict__ lens_out, float *__restrict__ weights_out, int32_t *__restrict__ evicted,
-    int32_t *__restrict__ evicted_count)
+    int32_t *__restrict__ evicted_count, int first_seq)
 {
     constexpr int W = kEvictThreads / 64;
     __shared__ int hist[256];
     __shared__ int pick[2];
     __shared__ int sums[2][2][W];
-    const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int s = first_seq + (int)blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = (int64_t)s * max_blocks;
     table += row; weights += row; table_out += row; weights_out += row; evicted += row;
     const int have = lens[s], wide = (int)max_blocks;
@@ -433,8 +433,10 @@ hipError_t launch_cache_evict(const int32_t *table, const int32_t *lens, const f
                               int32_t *lens_out, float *weights_out, int32_t *evicted, int32_t *evicted_count,
                               hipStream_t st)
 {
-    hipLaunchKernelGGL(cache_evict_kernel, dim3((unsigned)seqs), dim3(kEvictThreads), 0, st, table, lens, weights,
-                       max_blocks, keep, first, recent, table_out, lens_out, weights_out, evicted, evicted_count);
+    in_launches(seqs, [&](int at, unsigned n) {
+        hipLaunchKernelGGL(cache_evict_kernel, dim3(n), dim3(kEvictThreads), 0, st, table, lens, weights, max_blocks, keep,
+                           first, recent, table_out, lens_out, weights_out, evicted, evicted_count, at);
+    });
     return hipGetLastError();
 }
 

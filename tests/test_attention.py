@@ -70,6 +70,8 @@ PROMPTS = [
     ([1], 20, 5, 128), ([2, 1, 3], 4, 4, 64), ([63], 8, 2, 128), ([64, 65, 0, 127, 1], 8, 2, 64), ([128, 129], 7, 1, 128),
     ([31, 32, 33], 6, 2, 128), ([0, 0, 5, 0], 3, 3, 64), ([257, 1, 190], 16, 2, 128), ([511], 5, 5, 64), ([700, 300], 4, 1, 128),
     ([1] * 70 + [40], 4, 2, 64), ([1030], 12, 4, 128),
+    # more workgroups than the rule that splits a tile's keys over two waves admits
+    ([37] * 60 + [130, 1, 0, 200], 20, 5, 128), ([50] * 150, 8, 8, 64), ([9] * 400, 7, 1, 128), ([1100], 64, 64, 128),
 ]
 
 
@@ -113,9 +115,11 @@ def test_prompt_growing_logits(bl, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_prompt_rows_do_not_see_later_or_foreign_values(bl, dtype, bad):
-    """NaN and infinities in a later row, or in another sequence, leave a row's bits as they are."""
-    lens, hq, hkv, d = [100, 37, 200], 8, 2, 128
+@pytest.mark.parametrize("more", [0, 250])
+def test_prompt_rows_do_not_see_later_or_foreign_values(bl, dtype, bad, more):
+    """NaN and infinities in a later row, or in another sequence, leave a row's bits as they are, whether a tile's
+    keys are split over two waves or (with many sequences more) not."""
+    lens, hq, hkv, d = [100, 37, 200] + [20] * more, 8, 2, 128
     m = sum(lens)
     q, k, v = (_rand((m, h, d), 11 + i, DTYPES[dtype]) for i, h in enumerate((hq, hkv, hkv)))
     clean = bl.attention(q, k, v, _starts(lens))
@@ -297,6 +301,9 @@ CACHED = [
     ([0], [1], 4, 1, 128), ([1022], [1], 20, 5, 128), ([63, 64, 65, 0], [1] * 4, 8, 8, 64), ([300, 5, 700], [1, 1, 1], 16, 2, 128),
     ([100, 90], [1, 1], 7, 1, 64), ([64, 200, 10], [4, 1, 7], 20, 5, 128), ([130, 0, 77], [2, 30, 0], 6, 2, 64), ([0], [150], 4, 1, 128),
     ([4000], [1], 4, 4, 128), ([10, -1, 500, -1], [1] * 4, 8, 2, 128), ([33, -3, 60], [3, 2, 1], 12, 4, 64), ([190], [5], 40, 2, 64),
+    # one workgroup per sequence and head; some more than there are CUs, split; 8 and 16 rows over many blocks
+    ([(37 * i) % 300 for i in range(300)], [1] * 300, 8, 2, 64), ([(41 * i) % 200 for i in range(149)] + [1500], [1] * 150, 8, 2, 128),
+    ([5000], [1], 16, 2, 128), ([3000, 20], [6, 2], 40, 2, 64), ([700] * 3, [2] * 3, 8, 2, 128),
 ]
 
 
@@ -345,6 +352,16 @@ def test_cached_stale_codes_behind_the_last_token(bl):
     assert torch.equal(before, after)
 
 
+def test_cached_nothing_of_page_0_enters_for_a_missing_one(bl):
+    """Page 0 of a cache that was never written may hold anything, NaN scales among it."""
+    c = _Paged(bl, [130], [1], 1, 128, 4)
+    c.table = np.array([[2, -1, 3]])
+    for t in (c.cache.k_scale, c.cache.v_scale):
+        t[0] = float("nan")
+    c.ks[0] = c.vs[0] = np.nan
+    _check_cached(bl, c, [130], [1], 4, "f32", True, 5)
+
+
 def test_cached_rows_that_are_not_finite(bl):
     c = _Paged(bl, [300], [3], 2, 64, 4)
     q = _rand((3, 8, 64), 1, torch.float32)
@@ -378,6 +395,53 @@ def test_cached_offsets_past_32_bits(bl):
     bl.cache_append(c.cache, k, k, _i32(c.table), _i32([101]))
     for big, small in zip(cache, c.cache):
         assert torch.equal(big[idx], small)
+
+
+@pytest.mark.parametrize("cu", [[0, 300, 0, 300, 0], [300, 0, 300], [-4, 2**31 - 1, 5], [0] + [300, 0] * 40])
+def test_paged_offsets_out_of_order_stay_in_bounds(bl, cu):
+    """Offsets that the rule for bad values covers: nothing outside the rows, the cache and the table is touched."""
+    seqs, hkv, d = len(cu) - 1, 2, 64
+    c = _Paged(bl, [100] * seqs, [300] * seqs, hkv, d, 6)
+    rows = [torch.full((302, h, d), 3.0, dtype=torch.float32, device="cuda") for h in (8, hkv, hkv)]
+    guard = torch.full((302, 8 * d), 5.0, device="cuda")
+    lens = _i32([100] * seqs)
+    bl.cache_append(c.cache, rows[1][1:301], rows[2][1:301], _i32(c.table), lens, _i32(cu))
+    bl.attention_cached(rows[0][1:301], c.cache, _i32(c.table), lens, _i32(cu), out=guard[1:301])
+    bl.cache_read(c.cache, _i32(c.table), lens, _i32(cu), 300)
+    assert (guard[0] == 5).all() and (guard[301] == 5).all() and torch.isfinite(guard).all()
+
+
+def test_binding_refusals(bl):
+    """What the tensors themselves get wrong, before anything is enqueued."""
+    q, k = _rand((6, 4, 64), 1, torch.bfloat16), _rand((6, 2, 64), 2, torch.bfloat16)
+    cu, cache = _starts([6]), bl.cache_alloc(4, 2, 64)
+    table, lens = _i32([[0, 1]]), _i32([3])
+    fused = _rand((6, 521), 3, torch.bfloat16)
+    good = bl.attention(q, k, k, cu)
+    for call in (
+        lambda: bl.attention(q.half(), k.half(), k.half(), cu), lambda: bl.attention(q, k.float(), k, cu),
+        lambda: bl.attention(q, k, k[:5], cu), lambda: bl.attention(q, k, k, cu.long()), lambda: bl.attention(q, k, k, cu[:1]),
+        lambda: bl.attention(q.transpose(0, 1).contiguous().transpose(0, 1), k, k, cu), lambda: bl.attention(q.cpu(), k, k, cu),
+        lambda: bl.attention(q, k[:, :1].expand(6, 3, 64), k[:, :1].expand(6, 3, 64), cu),
+        lambda: bl.attention(fused[:, :256].unflatten(1, (4, 64)), k, k, cu),           # rows not a multiple of 16 bytes
+        lambda: bl.attention(fused.view(-1)[1:1537].view(6, 4, 64), k, k, cu),          # nor their start
+        lambda: bl.attention(q, k, k, cu, scale=float("inf")), lambda: bl.attention(q, k, k, cu, out=good.float()),
+        lambda: bl.attention(q.float(), k.float(), k.float(), cu, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+        lambda: bl.attention_cached(q, cache, table, lens, None), lambda: bl.attention_cached(q, cache, table[0], lens, cu),
+        lambda: bl.attention_cached(q, cache, table, lens, cu, weights=torch.zeros((1, 3), device="cuda")),
+        lambda: bl.attention_cached(_rand((6, 4, 128), 1, torch.bfloat16), cache, table, lens, cu),
+        lambda: bl.attention_cached(_rand((6, 3, 64), 1, torch.bfloat16), cache, table, lens, cu),
+        lambda: bl.cache_append(cache, q, q, table, lens, cu), lambda: bl.cache_append(cache[:3], k, k, table, lens, cu),
+        lambda: bl.cache_append(bl.KVCache(cache.k, cache.v[:2], *cache[2:]), k, k, table, lens, cu),
+        lambda: bl.cache_read(cache, table, lens, cu, 0), lambda: bl.cache_read(cache, table, lens, cu, 6, torch.float16),
+        lambda: bl.cache_evict(table, lens, torch.zeros((1, 2), device="cuda"), 0),
+        lambda: bl.cache_evict(table, lens.float(), torch.zeros((1, 2), device="cuda"), 1),
+    ):
+        with pytest.raises(bl.BitLinearError):
+            call()
+    with pytest.raises(TypeError):
+        bl.attention(q, k, k, cu, scale="much")
+    assert torch.equal(bl.attention(q, k, k, cu, scale=0.125), good)
 
 
 # ---------------------------------------------------------------- eviction
