@@ -25,11 +25,15 @@ namespace bl {
 // P is rounded to bf16 for its product with V, as the inputs are; sums and
 // statistics stay in fp32.
 // Bound by the matrix cores and the softmax's VALU work in about equal parts (55 %
-// and 50 % of the cycles at 8192 tokens), which two waves per SIMD overlap poorly.
-// Measured and not kept: eight waves per workgroup (536 against 543 us at 8192
-// tokens, 57.9 against 46.4 at 2048), raised wave priority around the products
-// (545 to 551), the row sum by dot products of pairs (551), 64 rows per wave with
-// the next tile's logits formed beside the softmax (registers spill: 1757 us).
+// and 50 % of the cycles at 8192 tokens), which two waves per SIMD overlap poorly:
+// 510 to 545 us there (box to box), 1.01 to 1.08 PFLOP/s, where a plain bf16
+// product of 16384^3 reaches 1.39.
+// Measured and not kept, at 8192 tokens beside 520 to 543 us: eight waves per
+// workgroup (536; 57.9 against 46.4 at 2048 tokens), those in two groups of four,
+// half a step apart, so that one's products meet the other's softmax (577), raised
+// wave priority around the products (545 to 551), the row sum by dot products of
+// pairs (551), V's operands read before the softmax (533 beside 509), 64 rows per
+// wave with the next tile's logits formed beside the softmax (registers spill: 1757).
 constexpr int kKeys = 64;
 
 template <int D>
@@ -404,7 +408,10 @@ __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a
 }
 
 // The loop of attention_bf16_kernel with the four 16-bit planes of a tile of
-// 32 * KS keys, 32 keys per wave.
+// 32 * KS keys, 32 keys per wave. Bound by the matrix cores: 8192 tokens, 32/8
+// heads of 128: 1.60 ms, 344 TFLOP/s of fp32 (three times that in fp16 products;
+// the fp32 matrix cores reach 153 in a plain product). Two accumulators for the
+// logits' main and cross terms instead of one measured the same.
 template <int D, int KS>
 __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(AttentionProblem a, int group, int first_group,
                                                                             const char *__restrict__ planes,
