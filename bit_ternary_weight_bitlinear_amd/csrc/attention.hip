@@ -353,17 +353,19 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 // fp32 products from fp16 ones: x = 2^a (hi + lo) with hi the nearest fp16 of
 // x / 2^a and lo that of the rest (22 bits and a sign), a such that the row's
 // largest magnitude lies in 2^14 .. 2^15; then xy ~ hi hi' + hi lo' + lo hi', off
-// by 2^-22 of |x||y| at most, with fp32 sums. Rows' elements below 2^-16 of the
-// largest keep 2^-40 of it. Three matrix products instead of one on the fp32
+// by 3 * 2^-22 of |x||y| at most, with fp32 sums. Rows' elements below 2^-17 of the
+// largest keep 2^-39 of it (fp16's smallest step is 2^-24). Three matrix products instead of one on the fp32
 // matrix cores, whose rate is a sixteenth.
 // A first kernel writes K and V in this form, once per row (the rows that read
 // them split nothing): [head][token][hi, lo][D], and 2^a per row.
 // The scale of K's rows multiplies the logits. That of V's rows goes into the
-// weights: w_j = p_j 2^(a_j - r) with r the running maximum of a_j over the keys
-// that the row sees, so that hi and lo of w keep 22 bits of the largest products.
+// weights: w_j = p_j 2^a_j / ref with ref the running maximum of p_j 2^a_j, so that
+// hi and lo of w keep 22 bits of the largest products (and a row of V counts for as
+// much as its weight lets it, however large it is).
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-constexpr float kSlackF32 = 3.0f;      // as kSlack: p stays below 2^3 ...
-constexpr float kWeightOne = 2048.0f;  // ... and w times this below 2^14
+constexpr float kSlackF32 = 3.0f;      // as kSlack
+constexpr float kMostWeight = 8.0f;    // the same for w ...
+constexpr float kWeightOne = 2048.0f;  // ... so that w times this stays below 2^14
 
 // 2^a of a row whose largest finite magnitude is big, and its reciprocal
 __device__ inline void row_scale(float big, float &scale, float &inv)
@@ -379,6 +381,15 @@ __device__ inline void split_f16(float v, _Float16 &hi, _Float16 &lo)
     hi = (_Float16)v;
     const float rest = v - (float)hi;
     lo = (_Float16)(rest - rest == 0.0f ? rest : 0.0f);
+}
+
+// A product as the fp32 number it rounds to. Without this the compiler may round it
+// to fp16 in one step where hi is used and in two where the rest is formed; near a
+// tie these differ by a unit of hi.
+__device__ inline float rounded(float v)
+{
+    asm("" : "+v"(v));
+    return v;
 }
 
 // D / 4 lanes per row of K or V (blockIdx.y: 0, 1)
@@ -516,7 +527,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
     };
 
     v16f o[DT];
-    float mx = kNegInf, sum = 0.0f, ref_v = 0.0f;  // ref_v: largest scale of V seen, o is relative to it
+    float mx = kNegInf, sum = 0.0f, ref_w = 0.0f;  // o is relative to ref_w, which is relative to 2^mx as sum is
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = v16f{};
 
@@ -584,38 +595,45 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
                 gv[i] = seen ? gv[i] : 0.0f;
             }
         }
-        float big = kNegInf, top_v = 0.0f, lo, up;
+        float big = kNegInf, lo, up;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            big = fmaxf(big, s[i]);
-            top_v = fmaxf(top_v, gv[i]);
-        }
+        for (int i = 0; i < 16; ++i) big = fmaxf(big, s[i]);
         both_halves(big, lo, up);
         big = fmaxf(lo, up) * c;
-        both_halves(top_v, lo, up);
-        top_v = fmaxf(lo, up);
-        if (__any(big > mx + kSlackF32 || top_v > ref_v)) {
+        if (__any(big > mx + kSlackF32)) {
             // only where it has grown: a row's result does not depend on its neighbours
             const float now = big > mx + kSlackF32 ? big : mx;
             const float keep = now == mx ? 1.0f : __builtin_amdgcn_exp2f(mx - now);
-            const float now_v = fmaxf(ref_v, top_v), keep_v = now_v == ref_v ? 1.0f : ref_v / now_v;
             mx = now;
-            ref_v = now_v;
             sum *= keep;
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[d][i] *= keep * keep_v;
+            ref_w *= keep;
         }
         const float ref = KS > 1 && mx == kNegInf ? 0.0f : mx;
-        const float to_w = KS > 1 && ref_v == 0.0f ? 0.0f : kWeightOne / ref_v;
-        v8h ph[2], pl[2];
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ref));
             sum += e;
+            gv[i] *= e;
+            top = fmaxf(top, gv[i]);
+        }
+        both_halves(top, lo, up);
+        top = fmaxf(lo, up);
+        if (__any(top > kMostWeight * ref_w)) {
+            const float now = top > kMostWeight * ref_w ? top : ref_w;
+            const float keep = now == ref_w ? 1.0f : ref_w / now;
+            ref_w = now;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= keep;
+        }
+        const float to_w = ref_w == 0.0f ? 0.0f : kWeightOne / ref_w;  // 0: none of the wave's keys is seen yet
+        v8h ph[2], pl[2];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
             _Float16 hi, lo16;
-            const float w = e * (gv[i] * to_w);
+            const float w = rounded(gv[i] * to_w);
             hi = (_Float16)w;
             lo16 = (_Float16)(w - (float)hi);
             ph[i >> 3][i & 7] = hi;
@@ -644,16 +662,16 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
                         v4f{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
             part[DT * 1024 + lane] = mx;
             part[DT * 1024 + 64 + lane] = sum;
-            part[DT * 1024 + 128 + lane] = ref_v;
+            part[DT * 1024 + 128 + lane] = ref_w;
         }
         __syncthreads();
         if (b0) return;
         const float other = part[DT * 1024 + lane], top = fmaxf(mx, other);
-        const float other_v = part[DT * 1024 + 128 + lane], top_v = fmaxf(ref_v, other_v);
         const float f0 = __builtin_amdgcn_exp2f(mx - top), f1 = __builtin_amdgcn_exp2f(other - top);
-        const float g0 = f0 * (ref_v / top_v), g1 = f1 * (other_v / top_v);
+        const float w0 = ref_w * f0, w1 = part[DT * 1024 + 128 + lane] * f1, top_w = fmaxf(w0, w1);
+        const float g0 = w0 / top_w, g1 = w1 / top_w;
         sum = __builtin_fmaf(sum, f0, part[DT * 1024 + 64 + lane] * f1);
-        ref_v = top_v;
+        ref_w = top_w;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -665,7 +683,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
     }
     float lo, up;
     both_halves(sum, lo, up);
-    const float inv = (ref_v / kWeightOne) / (lo + up);
+    const float inv = (ref_w / kWeightOne) / (lo + up);
     const int r = r_wave + col;
     if (r >= rows) return;
     float *dst = static_cast<float *>(a.out) + ((t.begin + tok) * a.q_heads + head * group + r % group) * D + 4 * h;

@@ -333,7 +333,7 @@ bl_status bitlinear_gemm_i32(const int8_t *q, int64_t m, int64_t k,
  * read by the kernels, so a call can be captured and replayed with others;
  * values outside 0..m are taken as the nearest of the two, and a sequence that
  * ends before it begins is empty. Rows before the first and behind the last
- * sequence are neither read nor written.
+ * sequence are not written and enter nothing.
  */
 #define BL_MAX_HEADS ((int64_t)1 << 12)
 
@@ -347,7 +347,10 @@ size_t bitlinear_attention_workspace_size(bl_dtype dtype, int64_t m, int64_t q_h
  *   out       [m][q_heads * head_dim] of type `dtype` (output)
  *   scale     finite (BL_ERR_VALUE otherwise); usually 1 / sqrt(head_dim)
  * BL_BF16: products of the bf16 inputs summed in fp32, softmax in fp32, p
- * rounded to bf16 for its product with v. BL_F32: as fp32 throughout.
+ * rounded to bf16 for its product with v. BL_F32: sums and softmax in fp32, the
+ * factors of the two products held to 2^-22 of their value, but elements of q, k
+ * and v no closer than 2^-39 of the largest of their row (one token and head), and
+ * the weights no closer than 2^-36 of the row's largest p_ij max |v_j|.
  * A row depends on rows 0..i of its own sequence only: infinities and NaN in
  * later rows or in other sequences do not reach it. BL_ERR_SHAPE also where
  * m * q_heads / kv_heads, or its 64th part (plus seqs) times kv_heads, passes

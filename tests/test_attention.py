@@ -114,6 +114,27 @@ def test_prompt_growing_logits(bl, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power,logit", [(90, -70.0), (30, -25.0), (100, -300.0), (-60, 40.0)])
+def test_prompt_values_count_by_their_weight(bl, d, power, logit, dtype):
+    """A few rows of V are 2^power times the others, but their keys' logits make their weight small (or, the other
+    way round, tiny values have nearly all of it): the result is the products', whichever row is the largest."""
+    lens, hq, hkv = [150, 70], 6, 2
+    for more in (0, 300):  # a tile's keys split over two waves, and not
+        all_lens = lens + [16] * more
+        m = sum(all_lens)
+        q, k, v = (_rand((m, h, d), 61 + i, DTYPES[dtype]) for i, h in enumerate((hq, hkv, hkv)))
+        q[:, :, 0] = 8.0
+        k[:, :, 0] = 0.0
+        for row in (0, 45, 64, 149, 160):
+            k[row, :, 0] = logit / (8.0 * d ** -0.5)
+            v[row] *= 2.0 ** power
+        out = bl.attention(q, k, v, _starts(all_lens))
+        want, spread, reach = ref.attention(_np(q), _np(k), _np(v), np.concatenate([[0], np.cumsum(all_lens)]), d ** -0.5)
+        _assert_within(_np(out).reshape(m, hq, d), want, _prompt_tolerance(want, spread, reach, max(lens), d, dtype), f"{more}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("more", [0, 250])
 def test_prompt_rows_do_not_see_later_or_foreign_values(bl, dtype, bad, more):
