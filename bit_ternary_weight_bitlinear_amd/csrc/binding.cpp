@@ -158,15 +158,19 @@ int64_t int_of(PyObject *o)
     return v;
 }
 
-// a caller's workspace, checked, or one of the call's own
-at::Tensor scratch(size_t bytes, PyObject *given, at::Device device)
+// a caller's workspace, or undefined
+at::Tensor given_workspace(PyObject *o) { return o == Py_None ? at::Tensor() : tensor(o, "workspace"); }
+
+// A caller's workspace checked against the call's size, or one of the call's own.
+// Runs without the interpreter's lock, so it sees no Python objects.
+void *scratch(size_t bytes, at::Tensor &ws, at::Device device)
 {
-    if (bytes == 0) return {};
-    if (given == Py_None) return at::empty({(int64_t)bytes}, at::TensorOptions(at::kByte).device(device));
-    const at::Tensor &t = tensor(given, "workspace");
-    if (t.device() != device || !t.is_contiguous() || (size_t)(t.numel() * t.element_size()) < bytes)
-        refuse("workspace must be contiguous and hold " + std::to_string(bytes) + " bytes on " + device.str() + "; got " + tensor_text(t));
-    return t;
+    if (bytes == 0) return nullptr;
+    if (!ws.defined())
+        ws = at::empty({(int64_t)bytes}, at::TensorOptions(at::kByte).device(device));
+    else if (ws.device() != device || !ws.is_contiguous() || ws.nbytes() < bytes)
+        refuse("workspace must be contiguous and hold " + std::to_string(bytes) + " bytes on " + device.str() + "; got " + tensor_text(ws));
+    return ws.data_ptr();
 }
 
 // The caching allocator hands the memory of a call's own tensors on to later work
@@ -183,6 +187,16 @@ struct WithoutGil {
     ~WithoutGil() { PyEval_RestoreThread(s); }
 };
 
+// torch's own exception class
+void out_of_memory(const char *what)
+{
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, what);
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+}
+
 // No C++ exception leaves an entry
 template <typename F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f)
@@ -195,6 +209,8 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f)
         return f();
     } catch (const Refused &r) {
         if (!PyErr_Occurred()) PyErr_SetString(g_error, r.what.c_str());
+    } catch (const c10::OutOfMemoryError &e) {
+        out_of_memory(e.what_without_backtrace());
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {
@@ -220,7 +236,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         const bl_dtype dtype = act_dtype(type);
         const float scale = scale_of(a[4], q.d);
         const int64_t shape[2] = {q.m, q.heads * q.d};
-        at::Tensor out, ws;
+        at::Tensor out, ws = given_workspace(a[6]);
         if (a[5] != Py_None) {
             out = tensor(a[5], "out");
             dense(out, "out", type, shape, device);
@@ -229,10 +245,10 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
             WithoutGil free;
             const c10::DeviceGuard guard(device);
             if (!out.defined()) out = at::empty(shape, tq.options());
-            ws = scratch(g_lib.attention_workspace_size(dtype, q.m, q.heads, k.heads, q.d, seqs), a[6], device);
+            const size_t bytes = g_lib.attention_workspace_size(dtype, q.m, q.heads, k.heads, q.d, seqs);
+            void *const space = scratch(bytes, ws, device);
             done(g_lib.attention(q.p, q.stride, k.p, k.stride, v.p, v.stride, dtype, q.m, q.heads, k.heads, q.d, cu, seqs, scale,
-                                 out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0,
-                                 stream_of(device)),
+                                 out.data_ptr(), space, bytes, stream_of(device)),
                  "bitlinear_attention");
         }
         return THPVariable_Wrap(out);
@@ -306,7 +322,7 @@ PyObject *attention_cached(PyObject *, PyObject *const *a, Py_ssize_t n)
             weights = static_cast<float *>(dense(tensor(a[6], "weights"), "weights", at::kFloat, both, device));
         }
         const int64_t shape[2] = {q.m, q.heads * q.d};
-        at::Tensor out, ws;
+        at::Tensor out, ws = given_workspace(a[8]);
         if (a[7] != Py_None) {
             out = tensor(a[7], "out");
             dense(out, "out", type, shape, device);
@@ -315,11 +331,12 @@ PyObject *attention_cached(PyObject *, PyObject *const *a, Py_ssize_t n)
             WithoutGil free;
             const c10::DeviceGuard guard(device);
             if (!out.defined()) out = at::empty(shape, tq.options());
-            ws = scratch(g_lib.attention_cached_workspace_size(q.m, q.heads, c.heads, q.d, t.seqs, t.wide, weights != nullptr), a[8],
-                         device);
+            const size_t bytes =
+                g_lib.attention_cached_workspace_size(q.m, q.heads, c.heads, q.d, t.seqs, t.wide, weights != nullptr);
+            void *const space = scratch(bytes, ws, device);
             done(g_lib.attention_cached(q.p, q.stride, dtype, q.m, q.heads, c.heads, q.d, t.cu, t.lens, t.seqs, t.table, t.wide, c.k,
-                                        c.v, c.ks, c.vs, c.pages, scale, out.data_ptr(), weights,
-                                        ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream_of(device)),
+                                        c.v, c.ks, c.vs, c.pages, scale, out.data_ptr(), weights, space,
+                                        bytes, stream_of(device)),
                  "bitlinear_attention_cached");
         }
         return THPVariable_Wrap(out);

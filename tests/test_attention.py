@@ -549,6 +549,25 @@ def test_a_layer_from_prompt_to_eviction(bl, dtype):
     np.testing.assert_allclose(_np(out).reshape(2, hq, d), want, rtol=2.0**-7 if dtype == "bf16" else 1e-4, atol=1e-4)
 
 
+def test_a_callers_workspace(bl):
+    """Any contiguous tensor that is large enough, subclasses included, and one larger than needed or not needed."""
+    q, k = _rand((70, 8, 64), 1, torch.float32), _rand((70, 2, 64), 2, torch.float32)
+    cu = _starts([70])
+    need = bl.attention_workspace_size(torch.float32, 70, 8, 2, 64, 1)
+    want = bl.attention(q, k, k, cu)
+    for ws in (torch.nn.Parameter(torch.empty(need, dtype=torch.uint8, device="cuda"), requires_grad=False),
+               torch.empty((need + 3) // 4, device="cuda"), torch.empty(2 * need, dtype=torch.uint8, device="cuda")):
+        assert torch.equal(bl.attention(q, k, k, cu, workspace=ws), want)
+    b = [x.bfloat16() for x in (q, k, k)]
+    assert torch.equal(bl.attention(*b, cu, workspace=torch.empty(1, device="cuda")), bl.attention(*b, cu))
+    c = _Paged(bl, [9000], [1], 2, 64, 8)
+    need = bl.attention_cached_workspace_size(1, 8, 2, 64, 1, c.wide)
+    assert need > 0
+    ws = torch.nn.Parameter(torch.empty(need, dtype=torch.uint8, device="cuda"), requires_grad=False)
+    args = (q[:1], c.cache, _i32(c.table), _i32([9000]))
+    assert torch.equal(bl.attention_cached(*args, workspace=ws), bl.attention_cached(*args))
+
+
 def test_captured_calls_follow_their_inputs(bl):
     """Append, attention (split and joined) with weights, prompt attention and eviction in one graph; each replay, on
     new inputs and with eager calls between, gives what eager calls give."""
