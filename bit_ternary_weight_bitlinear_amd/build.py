@@ -32,6 +32,10 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
 ]
+# Where LDS lets one workgroup of four waves onto a CU, a wave may have more than 256
+# registers and the compiler puts matrix results into the accumulation half of them,
+# which vector instructions reach by copies only: this keeps them in the other.
+EXTRA_FLAGS = {"attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def build_binding(verbose: bool = False) -> str:
@@ -58,7 +62,7 @@ def build(verbose: bool = False, out_dir: str | None = None) -> str:
 
     def compile_one(src):
         obj = os.path.join(out_dir, src.replace(".hip", ".o"))
-        cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [HIPCC, *FLAGS, *EXTRA_FLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)

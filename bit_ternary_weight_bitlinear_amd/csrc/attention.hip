@@ -27,14 +27,21 @@ namespace bl {
 // Bound by the matrix cores and the softmax's VALU work in about equal parts (55 %
 // and 50 % of the cycles at 8192 tokens), which two waves per SIMD overlap poorly:
 // 510 to 545 us there (box to box), 1.01 to 1.08 PFLOP/s, where a plain bf16
-// product of 16384^3 reaches 1.39.
+// product of 16384^3 reaches 1.39. The clock falls to 1.6 GHz meanwhile (2.4 in
+// shorter calls), so power bounds it too.
+// With KS = 2 a SIMD mostly has one wave, whose products, softmax and LDS reads would
+// follow one another: there K runs a tile ahead, the next tile's logits are formed
+// beside this one's softmax, and all operands are read ahead of both (2048 tokens,
+// 20/5 heads: 33.5 us beside 36.5; 2500 tokens of 6/2 heads 32.3 beside 36.5). Two
+// waves per SIMD gain nothing from it (343 beside 337 at 8192 tokens, 20/5 heads).
 // Measured and not kept, at 8192 tokens beside 520 to 543 us: eight waves per
 // workgroup (536; 57.9 against 46.4 at 2048 tokens), those in two groups of four,
 // half a step apart, so that one's products meet the other's softmax (577), raised
 // wave priority around the products (545 to 551), the row sum by dot products of
 // pairs (551), V's operands read before the softmax (533 beside 509), 64 rows per
 // wave with the next tile's logits formed beside the softmax (registers spill: 1757).
-constexpr int kKeys = 64;
+// With KS = 2, at 2500 tokens of 6/2 heads beside 32.5 us: four buffers instead of
+// two (35.2), products and softmax interleaved by hand (33.8 to 39).
 
 template <int D>
 __device__ inline int k_swizzle(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
@@ -89,25 +96,27 @@ __device__ inline float counted_value(float n)
     return c >= 1 << 14 || (plus && minus) ? __builtin_nanf("") : plus ? __builtin_inff() : minus ? kNegInf : 0.0f;
 }
 
-// The first half of it, by a workgroup of four waves: whether the tile held any
-template <typename B, int BYTES>
+// The first half of it, by the workgroup: whether the tile held any
+template <typename B, int BYTES, int WAVES>
 __device__ inline bool set_aside(char *tile, char *counts)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    char *vt = tile + wave * (BYTES / 4) + lane * 16, *ct = counts + wave * (BYTES / 4) + lane * 16;
+    char *vt = tile + wave * (BYTES / WAVES) + lane * 16, *ct = counts + wave * (BYTES / WAVES) + lane * 16;
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < BYTES / 4096; ++i) {
+    for (int i = 0; i < BYTES / (1024 * WAVES); ++i) {
         const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
         bad = bad || not_finite_pair<B>(w.x) || not_finite_pair<B>(w.y) || not_finite_pair<B>(w.z) || not_finite_pair<B>(w.w);
     }
-    int *flags = reinterpret_cast<int *>(counts);
+    int *flags = reinterpret_cast<int *>(counts), any = 0;
     bad = __any(bad);
     if (lane == 0) flags[wave] = bad;
     __syncthreads();
-    if (!(flags[0] | flags[1] | flags[2] | flags[3])) return false;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) any |= flags[i];
+    if (!any) return false;
     __syncthreads();
-    for (int i = 0; i < BYTES / 4096; ++i) {
+    for (int i = 0; i < BYTES / (1024 * WAVES); ++i) {
         const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
         *reinterpret_cast<uint4 *>(vt + i * 1024) =
             make_uint4(finite_pair<B>(w.x), finite_pair<B>(w.y), finite_pair<B>(w.z), finite_pair<B>(w.w));
@@ -118,14 +127,75 @@ __device__ inline bool set_aside(char *tile, char *counts)
     return true;
 }
 
+// registers 4 * (i % 4) .. +3 of accumulator i / 4
+template <int DT>
+__device__ inline v4f o_group(const v16f (&o)[DT], int i)
+{
+    const int d = i >> 2, g = 4 * (i & 3);
+    return v4f{o[d][g], o[d][g + 1], o[d][g + 2], o[d][g + 3]};
+}
+
+// KS neighbouring waves hold the same rows over different keys: each writes its
+// accumulators, maximum, sum and the scale of its accumulators (relative to 2^mx) and
+// joins a KS-th of the dims, which it gives to store with what they are to be
+// multiplied by.
+template <int DT, int KS, typename F>
+__device__ inline void join_waves(char *lds, const v16f (&o)[DT], float mx, float sum, float scale, F store)
+{
+    constexpr int kPart = DT * 4096 + 3 * 256, N = 4 * DT / KS;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), mine = wave % KS;
+    char *parts = lds + wave / KS * KS * kPart;
+    __syncthreads();
+    {
+        float *to = reinterpret_cast<float *>(parts + mine * kPart);
+        float lo, up;
+        both_halves(sum, lo, up);
+#pragma unroll
+        for (int i = 0; i < 4 * DT; ++i) *reinterpret_cast<v4f *>(to + (i * 64 + lane) * 4) = o_group(o, i);
+        to[DT * 1024 + lane] = mx;
+        to[DT * 1024 + 64 + lane] = lo + up;
+        to[DT * 1024 + 128 + lane] = scale;
+    }
+    __syncthreads();
+    float top = kNegInf, most = 0.0f, all = 0.0f, f[KS];
+    const float *from = reinterpret_cast<const float *>(parts);
+    constexpr int kStep = kPart / 4;
+#pragma unroll
+    for (int p = 0; p < KS; ++p) top = fmaxf(top, from[p * kStep + DT * 1024 + lane]);
+#pragma unroll
+    for (int p = 0; p < KS; ++p) {
+        const float e = __builtin_amdgcn_exp2f(from[p * kStep + DT * 1024 + lane] - top);
+        all = __builtin_fmaf(from[p * kStep + DT * 1024 + 64 + lane], e, all);
+        f[p] = from[p * kStep + DT * 1024 + 128 + lane] * e;
+        most = fmaxf(most, f[p]);
+    }
+#pragma unroll
+    for (int p = 0; p < KS; ++p) f[p] /= most;
+    const float inv = most / all;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = mine * N + n;
+        v4f v = {};
+#pragma unroll
+        for (int p = 0; p < KS; ++p) {
+            const v4f w = *reinterpret_cast<const v4f *>(from + p * kStep + (i * 64 + lane) * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(w[e], f[p], v[e]);
+        }
+        store(i, v, inv);
+    }
+}
+
 template <int D, int KS>
 __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem a, int group, int first_group)
 {
-    constexpr int ROWS = 128 / KS, C = D / 16, DT = D / 32, NB = 2 / KS;
-    constexpr int kTile = kKeys * D * 2;                  // bytes of a K or V tile
-    constexpr int kLoads = kTile / (1024 * 4);            // direct loads per wave and tile
+    constexpr bool AHEAD = KS > 1;
+    constexpr int WAVES = 4, ROWS = 32 * WAVES / KS, KEYS = 64;
+    constexpr int C = D / 16, DT = D / 32, NB = KEYS / 32 / KS;
+    constexpr int kTile = KEYS * D * 2;                   // bytes of a K or V tile
+    constexpr int kLoads = kTile / (1024 * WAVES);        // direct loads per wave and tile
     constexpr int kChunks = D / 8;                        // 16-byte chunks per row
-    constexpr int kLoadRows = kKeys / kLoads;             // rows that one load of the four waves brings
+    constexpr int kLoadRows = KEYS / kLoads;              // rows that one load of all waves brings
     // K, K, V, V, counts of what is not finite
     __shared__ __align__(1024) char lds[5 * kTile];
 
@@ -160,36 +230,34 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
         }
     }
     const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
-    const int tiles = last_row / group / kKeys + 1;
+    const int tiles = last_row / group / KEYS + 1;
     // first tile that some row of the workgroup, of the wave, does not see whole
-    const int group_masked = (t.tile * ROWS / group + 1) / kKeys;
-    const int wave_masked = ((r_wave < rows ? r_wave : rows - 1) / group + 1) / kKeys;
+    const int group_masked = (t.tile * ROWS / group + 1) / KEYS;
+    const int wave_masked = ((r_wave < rows ? r_wave : rows - 1) / group + 1) / KEYS;
 
-    // direct loads: load i of the four waves brings rows kLoadRows*i .. kLoadRows*(i+1)-1 of a tile
+    // direct loads: load i of the waves brings rows kLoadRows*i .. kLoadRows*(i+1)-1 of a tile
     const uint32_t base = lds_addr(lds);
-    const int load_row = wave * (kLoadRows / 4) + lane / kChunks;
+    const int load_row = wave * (kLoadRows / WAVES) + lane / kChunks;
     const int k_chunk = ((lane % kChunks) ^ k_swizzle<D>(load_row)) * 16, v_chunk = ((lane % kChunks) ^ v_swizzle<D>(load_row)) * 16;
     const uint32_t k_off = (uint32_t)load_row * (uint32_t)(a.k_stride * 2) + k_chunk;
     const uint32_t v_off = (uint32_t)load_row * (uint32_t)(a.v_stride * 2) + v_chunk;
     auto bring = [&](const void *x, int64_t stride, uint32_t off, int chunk, int tile, uint32_t to) {
-        const int64_t first = t.begin + (int64_t)tile * kKeys;
-        const int left = t.n - 1 - tile * kKeys;
+        const int64_t first = t.begin + (int64_t)tile * KEYS;
+        const int left = t.n - 1 - tile * KEYS;
         const bf16_t *from = static_cast<const bf16_t *>(x) + first * stride + (int64_t)head * D;
-        if (left >= kKeys - 1) {
+        if (left >= KEYS - 1) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) dma16(from + i * kLoadRows * stride, off, to + (4 * i + wave) * 1024);
+            for (int i = 0; i < kLoads; ++i) dma16(from + i * kLoadRows * stride, off, to + (WAVES * i + wave) * 1024);
         } else {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int row = i * kLoadRows + load_row;
-                dma16(from, (uint32_t)(row < left ? row : left) * (uint32_t)(stride * 2) + chunk, to + (4 * i + wave) * 1024);
+                dma16(from, (uint32_t)(row < left ? row : left) * (uint32_t)(stride * 2) + chunk, to + (WAVES * i + wave) * 1024);
             }
         }
     };
-    auto request = [&](int tile) {
-        bring(a.k, a.k_stride, k_off, k_chunk, tile, base + (tile & 1) * kTile);
-        bring(a.v, a.v_stride, v_off, v_chunk, tile, base + (2 + (tile & 1)) * kTile);
-    };
+    auto request_k = [&](int tile) { bring(a.k, a.k_stride, k_off, k_chunk, tile, base + (tile & 1) * kTile); };
+    auto request_v = [&](int tile) { bring(a.v, a.v_stride, v_off, v_chunk, tile, base + (2 + (tile & 1)) * kTile); };
 
     // operand addresses inside a tile; rows 32 keys further on, and 8 keys for V, are constant offsets
     int k_at[C], v_at[DT];
@@ -220,7 +288,7 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 
     // V of a masked tile, once it is there: keeps what is not finite from rows that do not see it
     auto clean = [&](int tile) {
-        if (!set_aside<Bf16Bits, kTile>(lds + (2 + (tile & 1)) * kTile, lds + 4 * kTile)) return;
+        if (!set_aside<Bf16Bits, kTile, WAVES>(lds + (2 + (tile & 1)) * kTile, lds + 4 * kTile)) return;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             v16f count = {};
@@ -230,7 +298,7 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
                 v8bf seen;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    seen[i] = (__bf16)(tile * kKeys + 16 * kc + 8 * (i >> 2) + 4 * h + (i & 3) <= tok ? 1.0f : 0.0f);
+                    seen[i] = (__bf16)(tile * KEYS + 16 * kc + 8 * (i >> 2) + 4 * h + (i & 3) <= tok ? 1.0f : 0.0f);
                 count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_fragment(4, n, d), seen, count, 0, 0, 0);
             }
 #pragma unroll
@@ -238,33 +306,58 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
         }
     };
 
-    request(0);
+    v16f s[NB];
+    // the fragments in the order of their use: n / NB is the 16 dims, n % NB the block of keys
+    auto k_nth = [&](int tile, int n) { return k_fragment(tile, n % NB, n / NB); };
+    auto logits = [&](v16f (&to)[NB], auto fragment) {
+#pragma unroll
+        for (int n = 0; n < NB * C; ++n)
+            to[n % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fragment(n), qf[n / NB], n / NB ? to[n % NB] : v16f{}, 0, 0, 0);
+    };
+    v8bf kf[AHEAD ? NB * C : 1];
+    auto read_k = [&](int tile) {
+#pragma unroll
+        for (int n = 0; n < NB * C; ++n) kf[n] = k_nth(tile, n);
+    };
+    auto k_read = [&](int n) { return kf[n]; };
+
+    request_k(0);
+    if constexpr (AHEAD) {
+        ring_barrier<0>();
+        request_v(0);
+        if (tiles > 1) request_k(1);
+        read_k(0);
+        logits(s, k_read);
+    } else {
+        request_v(0);
+    }
     for (int tile = 0; tile < tiles; ++tile) {
         ring_barrier<0>();
-        if (tile + 1 < tiles) request(tile + 1);
+        if (!AHEAD && tile + 1 < tiles) request_k(tile + 1);
+        if (tile + 1 < tiles) request_v(tile + 1);
+        if (AHEAD && tile + 2 < tiles) request_k(tile + 2);
         if (tile >= group_masked) clean(tile);
 
-        v16f s[NB];
+        if constexpr (AHEAD) {
+            read_k(tile + 1);  // old bytes of the buffer, and of no use, behind the last tile
+        } else {
+            logits(s, [&](int n) { return k_nth(tile, n); });
+            // the operand reads run kAhead fragments ahead of the products
+            constexpr int kAhead = 6;
+            __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, kAhead, 0);
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_fragment(tile, b, i), qf[i], i ? s[b] : v16f{}, 0, 0, 0);
-        // the operand reads run kAhead fragments ahead of the products
-        constexpr int kAhead = 6;
-        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, kAhead, 0);
-#pragma unroll
-        for (int i = 0; i < NB * C - kAhead; ++i) {
-            __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+            for (int i = 0; i < NB * C - kAhead; ++i) {
+                __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kAhead, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, kAhead, 0);
         if (tile >= wave_masked) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int key = tile * kKeys + 32 * (b0 + b) + 8 * (i >> 2) + 4 * h + (i & 3);
+                    const int key = tile * KEYS + 32 * (b0 + b) + 8 * (i >> 2) + 4 * h + (i & 3);
                     s[b][i] = key <= tok ? s[b][i] : kNegInf;
                 }
         }
@@ -287,6 +380,19 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
                 for (int i = 0; i < 16; ++i) o[d][i] *= keep;
         }
         const float ref = KS > 1 && mx == kNegInf ? 0.0f : mx;  // -inf: none of the wave's keys is seen yet
+        v8bf vf[AHEAD ? 2 * NB : 1][DT];
+        v16f next[NB];
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) vf[n][d] = v_fragment(2 + (tile & 1), n, d);
+            logits(next, k_read);
+        }
+        auto v_nth = [&](int n, int d) {
+            if constexpr (AHEAD) return vf[n][d];
+            else return v_fragment(2 + (tile & 1), n, d);
+        };
         v8bf p[2 * NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -300,52 +406,32 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
         for (int n = 0; n < 2 * NB; ++n)
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_fragment(2 + (tile & 1), n, d), p[n], o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_nth(n, d), p[n], o[d], 0, 0, 0);
+        if constexpr (AHEAD) {
+            __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 4 * NB * DT, 0);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) s[b] = next[b];
+        }
     }
 
-    if constexpr (KS > 1) {
-        // the wave with the tiles' upper keys hands its part over, 4 lanes' values of 16 bytes at a time
-        __syncthreads();
-        float *part = reinterpret_cast<float *>(lds + wave / KS * (DT * 4096 + 512));
-        if (b0) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *reinterpret_cast<v4f *>(part + ((d * 4 + g) * 64 + lane) * 4) =
-                        v4f{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
-            part[DT * 1024 + lane] = mx;
-            part[DT * 1024 + 64 + lane] = sum;
-        }
-        __syncthreads();
-        if (b0) return;
-        const float other = part[DT * 1024 + lane], top = fmaxf(mx, other);
-        const float f0 = __builtin_amdgcn_exp2f(mx - top), f1 = __builtin_amdgcn_exp2f(other - top);
-        sum = __builtin_fmaf(sum, f0, part[DT * 1024 + 64 + lane] * f1);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const v4f w = *reinterpret_cast<const v4f *>(part + ((d * 4 + g) * 64 + lane) * 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[d][4 * g + i] = __builtin_fmaf(o[d][4 * g + i], f0, w[i] * f1);
-            }
-    }
-    float lo, up;
-    both_halves(sum, lo, up);
-    const float inv = 1.0f / (lo + up);
     const int r = r_wave + col;
-    if (r >= rows) return;
     bf16_t *dst = static_cast<bf16_t *>(a.out) + ((t.begin + tok) * a.q_heads + head * group + r % group) * D + 4 * h;
+    auto store = [&](int i, const v4f &v, float inv) {  // dims 32 * (i / 4) + 8 * (i % 4) + 4 * h .. +3
+        bf16_t w[4];
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+        for (int e = 0; e < 4; ++e) store_out(&w[e], v[e] * inv);
+        *reinterpret_cast<uint2 *>(dst + 32 * (i >> 2) + 8 * (i & 3)) = *reinterpret_cast<const uint2 *>(w);
+    };
+    if constexpr (KS == 1) {
+        float lo, up;
+        both_halves(sum, lo, up);
+        const float inv = 1.0f / (lo + up);
+        if (r >= rows) return;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            bf16_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) store_out(&w[i], o[d][4 * g + i] * inv);
-            *reinterpret_cast<uint2 *>(dst + 32 * d + 8 * g) = *reinterpret_cast<const uint2 *>(w);
-        }
+        for (int i = 0; i < 4 * DT; ++i) store(i, o_group(o, i), inv);
+    } else {
+        join_waves<DT, KS>(lds, o, mx, sum, 1.0f, [&](int i, const v4f &v, float inv) { if (r < rows) store(i, v, inv); });
+    }
 }
 
 // ---------------------------------------------------------------- fp32 on the matrix cores
@@ -418,10 +504,13 @@ __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a
     if (lane == 0) scales[is_v * rows + at] = scale;
 }
 
-// The loop of attention_bf16_kernel with the four 16-bit planes of a tile of
-// 32 * KS keys, 32 keys per wave. Bound by the matrix cores: 8192 tokens, 32/8
-// heads of 128: 1.60 ms, 344 TFLOP/s of fp32 (three times that in fp16 products;
-// the fp32 matrix cores reach 153 in a plain product). Two accumulators for the
+// The loop of attention_bf16_kernel (as it is there with KS = 1) with the four 16-bit
+// planes of a tile of 32 * KS keys, 32 keys per wave. Bound by the matrix cores: 8192
+// tokens, 32/8 heads of 128: 1.54 ms, 357 TFLOP/s of fp32 (three times that in
+// fp16 products; the fp32 matrix cores reach 153 in a plain product). With KS = 2, 2500
+// tokens of 6/2 heads: 82.5 us; 97.5 with matrix results in accumulation registers
+// (build.py), 84.2 with V's operands read as they are used, 88.2 with the next tile's
+// logits formed beside the softmax (too many registers). Two accumulators for the
 // logits' main and cross terms instead of one measured the same.
 template <int D, int KS>
 __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(AttentionProblem a, int group, int first_group,
@@ -533,7 +622,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 
     auto clean = [&](int tile) {
         const uint32_t counts = base + 2 * kStage;
-        if (!set_aside<F16Bits, kPlane>(lds + (tile & 1) * kStage + 2 * kPlane, lds + 2 * kStage)) return;
+        if (!set_aside<F16Bits, kPlane, 4>(lds + (tile & 1) * kStage + 2 * kPlane, lds + 2 * kStage)) return;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             v16f count = {};
@@ -648,63 +737,39 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vh, pl[n], o[d], 0, 0, 0);
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vh, ph[n], o[d], 0, 0, 0);
             }
+        // V's operand reads all go ahead of the weights
+        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 8 * DT, 0);
     }
 
-    if constexpr (KS > 1) {
-        __syncthreads();
-        float *part = reinterpret_cast<float *>(lds + wave / KS * (DT * 4096 + 768));
-        if (b0) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *reinterpret_cast<v4f *>(part + ((d * 4 + g) * 64 + lane) * 4) =
-                        v4f{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
-            part[DT * 1024 + lane] = mx;
-            part[DT * 1024 + 64 + lane] = sum;
-            part[DT * 1024 + 128 + lane] = ref_w;
-        }
-        __syncthreads();
-        if (b0) return;
-        const float other = part[DT * 1024 + lane], top = fmaxf(mx, other);
-        const float f0 = __builtin_amdgcn_exp2f(mx - top), f1 = __builtin_amdgcn_exp2f(other - top);
-        const float w0 = ref_w * f0, w1 = part[DT * 1024 + 128 + lane] * f1, top_w = fmaxf(w0, w1);
-        const float g0 = w0 / top_w, g1 = w1 / top_w;
-        sum = __builtin_fmaf(sum, f0, part[DT * 1024 + 64 + lane] * f1);
-        ref_w = top_w;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const v4f w = *reinterpret_cast<const v4f *>(part + ((d * 4 + g) * 64 + lane) * 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[d][4 * g + i] = __builtin_fmaf(o[d][4 * g + i], g0, w[i] * g1);
-            }
-    }
-    float lo, up;
-    both_halves(sum, lo, up);
-    const float inv = (ref_w / kWeightOne) / (lo + up);
     const int r = r_wave + col;
-    if (r >= rows) return;
     float *dst = static_cast<float *>(a.out) + ((t.begin + tok) * a.q_heads + head * group + r % group) * D + 4 * h;
+    auto store = [&](int i, const v4f &v, float inv) {
+        *reinterpret_cast<v4f *>(dst + 32 * (i >> 2) + 8 * (i & 3)) = v4f{v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    };
+    if constexpr (KS == 1) {
+        float lo, up;
+        both_halves(sum, lo, up);
+        const float inv = (ref_w / kWeightOne) / (lo + up);
+        if (r >= rows) return;
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<float4 *>(dst + 32 * d + 8 * g) =
-                make_float4(o[d][4 * g] * inv, o[d][4 * g + 1] * inv, o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv);
+        for (int i = 0; i < 4 * DT; ++i) store(i, o_group(o, i), inv);
+    } else {
+        join_waves<DT, KS>(lds, o, mx, sum, ref_w / kWeightOne, [&](int i, const v4f &v, float inv) { if (r < rows) store(i, v, inv); });
+    }
 }
 
 // Few workgroups: a tile's keys are split over two waves (KS = 2), so that there
-// are twice as many and the longest takes half as long. It pays up to one and a
-// half workgroups per CU in bf16, one in fp32 (whose KS = 2 fills a CU's LDS), and
-// twice as many of 64-wide heads, whose tiles are half as large. 20/5 heads of 128,
-// one prompt, KS = 1 / 2: bf16 1024 tokens 24.3 / 21.1 us, 2048 44.2 / 39.2, 3000
-// 68.2 / 72.7, 4096 103 / 119; fp32 1024 tokens 70.8 / 53.5, 2048 130 / 137. 16/4
-// heads of 64: bf16 4096 tokens 62.6 / 53.4, fp32 2048 tokens 82.5 / 60.7.
-static bool few_groups(const AttentionProblem &p, int64_t groups)
+// are twice as many and the longest takes half as long. It pays up to 420 workgroups
+// in bf16, 340 in fp32 (whose KS = 2 fills a CU's LDS), and half as many again of
+// 64-wide heads. One prompt, KS = 1 / 2, 20/5 heads of 128: bf16 1024 tokens 24.2 /
+// 19.5 us, 2300 48.6 / 44.0, 2600 (415 workgroups) 56.1 / 54.1, 2900 (460) 63.7 /
+// 64.9, 4096 99 / 107; fp32 1300 tokens 74.6 / 56.0, 2048 (325) 116 / 114. 16/4 heads
+// of 64: bf16 4096 tokens (516) 62.3 / 53.0, 5000 (629) 80.6 / 80.8, fp32 2500 tokens
+// 90.8 / 67.7, 4096 (516) 160 / 154.
+static int key_splits(const AttentionProblem &p)
 {
-    return groups <= (p.bf16 ? 384 : 256) * (128 / p.head_dim);
+    const int64_t groups = (p.m * (p.q_heads / p.kv_heads) / 128 + p.seqs) * p.kv_heads;
+    return groups <= (p.bf16 ? 420 : 340) * (p.head_dim == 64 ? 3 : 2) / 2 ? 2 : 1;
 }
 
 int64_t attention_workspace(const AttentionProblem &p)
@@ -721,20 +786,25 @@ hipError_t launch_attention(const AttentionProblem &p, void *ws, hipStream_t st)
     float *scales = p.bf16 ? nullptr : reinterpret_cast<float *>(planes + round_up(2 * rows * p.head_dim * 4, 256));
     auto go = [&](auto width, auto splits) {
         constexpr int D = decltype(width)::value, KS = decltype(splits)::value;
+        const int64_t rows_each = 128 / KS;
         if (!p.bf16)
             in_launches(ceil_div(rows * (D / 4), 256), [&](int first, unsigned n) {
                 hipLaunchKernelGGL((attention_split_kernel<D>), dim3(n, 2), dim3(256), 0, st, p, planes, scales, first);
             });
-        in_launches((p.m * group * KS / 128 + p.seqs) * p.kv_heads, [&](int first, unsigned n) {
+        in_launches((p.m * group / rows_each + p.seqs) * p.kv_heads, [&](int first, unsigned n) {
             if (p.bf16) hipLaunchKernelGGL((attention_bf16_kernel<D, KS>), dim3(n), dim3(256), 0, st, p, group, first);
-            else hipLaunchKernelGGL((attention_f32_kernel<D, KS>), dim3(n), dim3(256), 0, st, p, group, first,
-                                    (const char *)planes, (const float *)scales);
+            else if constexpr (KS < 4) hipLaunchKernelGGL((attention_f32_kernel<D, KS>), dim3(n), dim3(256), 0, st, p, group, first,
+                                                          (const char *)planes, (const float *)scales);
         });
     };
-    const int64_t groups = (p.m * group / 128 + p.seqs) * p.kv_heads;
-    const bool few = few_groups(p, groups);
-    if (p.head_dim == 128) few ? go(Width<128>{}, Width<2>{}) : go(Width<128>{}, Width<1>{});
-    else few ? go(Width<64>{}, Width<2>{}) : go(Width<64>{}, Width<1>{});
+    auto go_width = [&](auto width) {
+        switch (key_splits(p)) {
+        case 1: return go(width, Width<1>{});
+        default: return go(width, Width<2>{});
+        }
+    };
+    if (p.head_dim == 128) go_width(Width<128>{});
+    else go_width(Width<64>{});
     return hipGetLastError();
 }
 
