@@ -39,7 +39,8 @@ namespace bl {
 // half a step apart, so that one's products meet the other's softmax (577), raised
 // wave priority around the products (545 to 551), the row sum by dot products of
 // pairs (551), V's operands read before the softmax (533 beside 509), 64 rows per
-// wave with the next tile's logits formed beside the softmax (registers spill: 1757).
+// wave, one's products beside the other's softmax (580 beside 518: the 512 registers
+// that it needs are half accumulation registers, reached by copies).
 // With KS = 2, at 2500 tokens of 6/2 heads beside 32.5 us: four buffers instead of
 // two (35.2), products and softmax interleaved by hand (33.8 to 39).
 

@@ -341,7 +341,6 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
 template <int W, bool PARTS>
 __device__ inline void add_weights(const CachedArgs &a, int s, int chunk64, float *weights, float2 *fin, float *part)
 {
-    constexpr int kChunkRows = 4 * W;  // 16 lanes join a row
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int64_t begin;
     int n;
@@ -355,35 +354,48 @@ __device__ inline void add_weights(const CachedArgs &a, int s, int chunk64, floa
     const int64_t row0 = begin * a.q_heads, rows = (int64_t)n * a.q_heads, total_rows = a.m * a.q_heads;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml), *stat = reinterpret_cast<const float2 *>(a.stat);
     float w = 0.0f;
-    for (int64_t r0 = 0; r0 < rows; r0 += kChunkRows) {
-        if constexpr (PARTS) {
-            const int64_t r = r0 + (tid >> 4);
-            float mx = kNegInf, l = 0.0f;
-            if (r < rows)
-                for (int i = tid & 15; i < parts; i += 16) {
-                    const float2 v = ml[i * total_rows + row0 + r];
-                    const float now = fmaxf(mx, v.x), to = now == kNegInf ? 0.0f : now;
-                    l = __builtin_fmaf(l, __builtin_amdgcn_exp2f(mx - to), v.y * __builtin_amdgcn_exp2f(v.x - to));
-                    mx = now;
-                }
-            const float top = row16_max(mx);
-            l = row16_sum(l * __builtin_amdgcn_exp2f(mx - (top == kNegInf ? 0.0f : top)));
-            __syncthreads();
-            if ((tid & 15) == 0) fin[tid >> 4] = final_of(top, l);
-            __syncthreads();
-        }
-        if (p < npages) {
+    // a thread adds kRows rows per round; LANES lanes join a row's splits
+    auto add = [&](auto lanes) {
+        constexpr int LANES = decltype(lanes)::value, kRows = 64 / LANES;
+        for (int64_t r0 = 0; r0 < rows; r0 += kRows * W) {
+            float2 st[kRows];  // asked for before the rows' exponents and sums
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kRows; ++i) {
+                const int64_t r = r0 + wave + W * i;
+                st[i] = r < rows && p < npages ? stat[(row0 + r) * a.max_blocks + p] : make_float2(0.0f, 0.0f);
+            }
+            if constexpr (PARTS) {
+                const int64_t r = r0 + tid / LANES;
+                float mx = kNegInf, l = 0.0f;
+                if (r < rows)
+                    for (int i = tid % LANES; i < parts; i += LANES) {
+                        const float2 v = ml[i * total_rows + row0 + r];
+                        const float now = fmaxf(mx, v.x), to = now == kNegInf ? 0.0f : now;
+                        l = __builtin_fmaf(l, __builtin_amdgcn_exp2f(mx - to), v.y * __builtin_amdgcn_exp2f(v.x - to));
+                        mx = now;
+                    }
+                float top = mx;
+#pragma unroll
+                for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+                l *= __builtin_amdgcn_exp2f(mx - (top == kNegInf ? 0.0f : top));
+#pragma unroll
+                for (int d = 1; d < LANES; d <<= 1) l += __shfl_xor(l, d);
+                __syncthreads();
+                if (tid % LANES == 0) fin[tid / LANES] = final_of(top, l);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
                 const int64_t r = r0 + wave + W * i;
                 if (r >= rows) continue;
                 const float2 f = PARTS ? fin[wave + W * i] : reinterpret_cast<const float2 *>(a.final_ml)[row0 + r];
-                const float2 st = stat[(row0 + r) * a.max_blocks + p];
-                const float add = st.y * f.y * __builtin_amdgcn_exp2f(st.x - f.x);
-                w += f.y > 0.0f && st.y > 0.0f ? add : 0.0f;
+                const float share = st[i].y * f.y * __builtin_amdgcn_exp2f(st[i].x - f.x);
+                w += f.y > 0.0f && st[i].y > 0.0f ? share : 0.0f;
             }
         }
-    }
+    };
+    if (rows > 4 * W) add(Width<4>{});
+    else add(Width<16>{});
     part[tid] = w;
     __syncthreads();
     if (wave || p >= npages) return;
@@ -398,24 +410,31 @@ __global__ __launch_bounds__(1024) void attention_weights_kernel(CachedArgs a, f
     add_weights<16, false>(a, first_seq + (int)blockIdx.x, blockIdx.y, weights, nullptr, part);
 }
 
-// Joins the splits: one workgroup per query row. The splits' sums become factors in
-// LDS; then every thread adds one dim of every fourth split (or eighth, of 64 dims),
-// all loads independent. The workgroups behind those add the blocks' weights.
-template <typename T, int D>
+// Joins the splits. Up to kFewSplits, a thread per dim of a row does by itself, all its
+// loads independent; otherwise one workgroup per query row: the splits' sums become
+// factors in LDS, then every thread adds one dim of every fourth split (or eighth, of
+// 64 dims). The workgroups behind those add the blocks' weights. 12 sequences of four
+// tokens and 8 splits, 20 heads: 4.1 us beside 6.1 with a workgroup per row.
+constexpr int kFewSplits = 16;
+
+template <typename T, int D, bool FEW>
 __global__ __launch_bounds__(512) void attention_join_kernel(CachedArgs a, float *__restrict__ weights, int blocks64)
 {
     constexpr int G = 512 / D;
     __shared__ float factor[512], jo[512];
     __shared__ float red[2][8];
-    __shared__ float2 fin[32];
-    const int64_t row = blockIdx.x, total_rows = a.m * a.q_heads;
-    if (row >= total_rows) {
-        const int w = (int)(row - total_rows);
+    __shared__ float2 fin[128];
+    const int tid = threadIdx.x, wave = tid >> 6, dim = tid % D;
+    const int64_t total_rows = a.m * a.q_heads, groups = FEW ? (total_rows + G - 1) / G : total_rows;
+    if (blockIdx.x >= groups) {
+        const int w = (int)(blockIdx.x - groups);
         add_weights<8, true>(a, w / blocks64, w % blocks64, weights, fin, jo);
         return;
     }
+    const int64_t row = FEW ? (int64_t)blockIdx.x * G + tid / D : blockIdx.x;
+    if (row >= total_rows) return;
     SeqTile t;
-    const int tok = (int)(row / a.q_heads), tid = threadIdx.x, wave = tid >> 6;
+    const int tok = (int)(row / a.q_heads);
     if (!a.cu) {
         t.seq = tok;
         t.n = 1;
@@ -428,35 +447,54 @@ __global__ __launch_bounds__(512) void attention_join_kernel(CachedArgs a, float
     if (have < 0) return;
     const int npages = pages_of(have, t.n, a.max_blocks), chunk = pages_per_split(npages, a.splits, a.waves);
     const int parts = npages <= chunk ? 1 : (npages + chunk - 1) / chunk;
-    float2 ml = make_float2(kNegInf, 0.0f);
-    if (tid < parts) ml = reinterpret_cast<const float2 *>(a.part_ml)[tid * total_rows + row];
-    const float wave_top = wave_max(ml.x);
-    if ((tid & 63) == 0) red[0][wave] = wave_top;
-    __syncthreads();
-    float top = red[0][0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) top = fmaxf(top, red[0][w]);
-    const float f = tid < parts ? __builtin_amdgcn_exp2f(ml.x - (top == kNegInf ? 0.0f : top)) : 0.0f;
-    factor[tid] = f;
-    float l = f * ml.y;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
-    if ((tid & 63) == 0) red[1][wave] = l;
-    __syncthreads();
-    l = red[1][0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) l += red[1][w];
-    const int dim = tid % D;
+    const float2 *mls = reinterpret_cast<const float2 *>(a.part_ml) + row;
     const float *src = a.part_o + row * D + dim;
-    float o = 0.0f;
-#pragma unroll 8
-    for (int s = tid / D; s < parts; s += G) o = __builtin_fmaf(factor[s], src[s * total_rows * D], o);
-    jo[tid] = o;
-    __syncthreads();
-    if (tid >= D) return;
+    float o = 0.0f, l = 0.0f;
+    if constexpr (FEW) {
+        float2 ml[kFewSplits];
+        float part[kFewSplits], top = kNegInf;
 #pragma unroll
-    for (int g = 1; g < G; ++g) o += jo[g * D + tid];
-    store_out(static_cast<T *>(a.out) + row * D + tid, l == 0.0f ? 0.0f : o / l);
+        for (int s = 0; s < kFewSplits; ++s) {
+            ml[s] = s < parts ? mls[s * total_rows] : make_float2(kNegInf, 0.0f);
+            part[s] = s < parts ? src[s * total_rows * D] : 0.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < kFewSplits; ++s) top = fmaxf(top, ml[s].x);
+        const float to = top == kNegInf ? 0.0f : top;
+#pragma unroll
+        for (int s = 0; s < kFewSplits; ++s) {
+            const float f = __builtin_amdgcn_exp2f(ml[s].x - to);
+            o = __builtin_fmaf(f, part[s], o);
+            l = __builtin_fmaf(f, ml[s].y, l);
+        }
+    } else {
+        float2 ml = make_float2(kNegInf, 0.0f);
+        if (tid < parts) ml = mls[tid * total_rows];
+        const float wave_top = wave_max(ml.x);
+        if ((tid & 63) == 0) red[0][wave] = wave_top;
+        __syncthreads();
+        float top = red[0][0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) top = fmaxf(top, red[0][w]);
+        const float f = tid < parts ? __builtin_amdgcn_exp2f(ml.x - (top == kNegInf ? 0.0f : top)) : 0.0f;
+        factor[tid] = f;
+        l = f * ml.y;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+        if ((tid & 63) == 0) red[1][wave] = l;
+        __syncthreads();
+        l = red[1][0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) l += red[1][w];
+#pragma unroll 8
+        for (int s = tid / D; s < parts; s += G) o = __builtin_fmaf(factor[s], src[s * total_rows * D], o);
+        jo[tid] = o;
+        __syncthreads();
+        if (tid >= D) return;
+#pragma unroll
+        for (int g = 1; g < G; ++g) o += jo[g * D + tid];
+    }
+    store_out(static_cast<T *>(a.out) + row * D + dim, l == 0.0f ? 0.0f : o / l);
 }
 
 // ---------------------------------------------------------------- launcher
@@ -477,8 +515,10 @@ static int64_t query_tiles(const CachedProblem &p, int rt)
 // Waves per workgroup, and workgroups per sequence, head and tile of query rows
 // (a unit). 16 waves per workgroup (as many as their results fit LDS for: 16 / RT)
 // are a CU's share for 4 query rows, and need few or no launches to join:
-//  - no more blocks than four per wave: one workgroup per unit, no joining launch
-//    (one sequence of 1023 tokens, 20/5 heads: 6.8 us; split over 4: 10.0);
+//  - no more blocks than two per wave (four of 64-wide heads): one workgroup per unit,
+//    no joining launch (one sequence of 1023 tokens, 20/5 heads: 6.8 us, split over 4
+//    10.0; 2500 tokens 9.6 and 9.6; 3999 12.4 and 9.8; 3000 of 16/4 heads of 64 8.1 and
+//    8.5);
 //  - up to one unit per CU: as many workgroups as give every CU 16 waves (8 with 8
 //    query rows, whose registers allow no more; of 16 rows' workgroups about half
 //    turn out empty), but at least a page per wave;
@@ -496,7 +536,7 @@ static Shape launch_shape(const CachedProblem &p, int rt)
     const int64_t units = query_tiles(p, rt) * p.kv_heads, cus = 256;
     const bool wide = units <= cus || (2 * units >= 3 * cus && units < 2 * cus);
     const int waves = wide ? 16 / rt : 4;
-    if (p.max_blocks <= 4 * waves) return {waves, 1};
+    if (p.max_blocks * p.head_dim <= 256 * waves) return {waves, 1};
     int64_t s = (rt == 2 ? 8 : 16) * cus / (waves * units);
     const int64_t most = ceil_div(p.max_blocks, waves);
     s = s > most ? most : s;
@@ -560,9 +600,14 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
             if (p.weights) hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, true>), grid, dim3(64 * W), 0, st, a, first);
             else hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, false>), grid, dim3(64 * W), 0, st, a, first);
         });
-        if (a.splits > 1)
-            hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(p.m * p.q_heads + (p.weights ? p.seqs * blocks64 : 0))),
-                               dim3(512), 0, st, a, p.weights, (int)blocks64);
+        if (a.splits == 1) return;
+        const int64_t rows = p.m * p.q_heads, extra = p.weights ? p.seqs * blocks64 : 0;
+        if (a.splits <= kFewSplits)
+            hipLaunchKernelGGL((attention_join_kernel<T, D, true>), dim3((unsigned)(ceil_div(rows, 512 / D) + extra)), dim3(512), 0, st,
+                               a, p.weights, (int)blocks64);
+        else
+            hipLaunchKernelGGL((attention_join_kernel<T, D, false>), dim3((unsigned)(rows + extra)), dim3(512), 0, st, a, p.weights,
+                               (int)blocks64);
     };
     auto go = [&](auto type, auto width, auto tiles) {
         constexpr int RT = decltype(tiles)::value;
