@@ -80,11 +80,9 @@ CACHED_OK = dict(q=A, qs=1024, dtype=1, m=2, hq=8, hkv=2, d=128, cu=None, lens=A
 
 
 @pytest.mark.parametrize("change,status", [
-    ({n: None}, BL_ERR_NULL) for n in "q lens table kc vc kscale vscale out".split()] + [
+    ({n: None}, BL_ERR_NULL) for n in "q lens table kc vc kscale vscale out ws".split()] + [
     ({"dtype": 9}, BL_ERR_DTYPE), ({"seqs": 3}, BL_ERR_SHAPE), ({"hkv": 5}, BL_ERR_SHAPE), ({"d": 256}, BL_ERR_SHAPE), ({"scale": NAN}, BL_ERR_VALUE),
-    ({"q": MIS}, BL_ERR_ALIGN), ({"w": ODD}, BL_ERR_ALIGN),
-    # a table this wide is read by several workgroups per sequence, which need the workspace
-    ({"wide": 2048, "ws": None}, BL_ERR_NULL), ({"wide": 2048, "ws": A + 16}, BL_ERR_ALIGN), ({"wide": 2048, "wn": 8}, BL_ERR_WORKSPACE)])
+    ({"q": MIS}, BL_ERR_ALIGN), ({"w": ODD}, BL_ERR_ALIGN), ({"ws": A + 16}, BL_ERR_ALIGN), ({"wn": 8}, BL_ERR_WORKSPACE)])
 def test_cached_refusals(bl, change, status):
     assert _call(bl.load_library().bitlinear_attention_cached, CACHED, CACHED_OK, **change) == status
 
