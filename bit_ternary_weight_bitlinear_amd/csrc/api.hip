@@ -235,12 +235,8 @@ int64_t cached_workspace(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t h
 {
     CachedProblem p{};
     p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads; p.head_dim = head_dim; p.seqs = seqs;
-    p.max_blocks = max_blocks; p.want_weights = weights; p.packed = true;
-    const int64_t packed = attention_cached_workspace(p);
-    if (m != seqs) return packed;
-    p.packed = false;  // one row per sequence may come without cu_seqlens
-    const int64_t single = attention_cached_workspace(p);
-    return packed > single ? packed : single;
+    p.max_blocks = max_blocks; p.want_weights = weights;
+    return attention_cached_workspace(p);
 }
 
 }  // namespace

@@ -111,11 +111,12 @@ constexpr int kBlock = 64;  // tokens per cache page
 // A launch holds fewer than 2^32 threads in x: longer grids go in several launches,
 // each with the index of its first workgroup.
 constexpr int64_t kMostGroups = (int64_t)1 << 21;
+constexpr int64_t kMostInZ = 1 << 15;  // and in y or z no more than 2^16 workgroups
 template <typename F>
-inline void in_launches(int64_t groups, F launch)
+inline void in_launches(int64_t groups, F launch, int64_t most = kMostGroups)
 {
-    for (int64_t first = 0; first < groups; first += kMostGroups)
-        launch((int)first, (unsigned)(groups - first < kMostGroups ? groups - first : kMostGroups));
+    for (int64_t first = 0; first < groups; first += most)
+        launch((int)first, (unsigned)(groups - first < most ? groups - first : most));
 }
 
 }  // namespace bl

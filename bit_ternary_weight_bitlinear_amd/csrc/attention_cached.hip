@@ -114,8 +114,8 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane >> 4, c = lane & 15;
     SeqTile t;
-    if (!find_rows<RT>(a, first_tile + (int)blockIdx.x, t)) return;
-    const int head = blockIdx.y, split = blockIdx.z;
+    if (!find_rows<RT>(a, first_tile + (int)blockIdx.z, t)) return;
+    const int head = blockIdx.y, split = blockIdx.x;
     const int32_t *table = a.table + (int64_t)t.seq * a.max_blocks;
     // one split: the wave's pages do not depend on the length, which is on its way
     int ids = -1;
@@ -499,17 +499,34 @@ __global__ __launch_bounds__(512) void attention_join_kernel(CachedArgs a, float
 
 // ---------------------------------------------------------------- launcher
 
-// query rows per workgroup: 4, 8 or 16, as many as a sequence has on average
-static int row_tiles(const CachedProblem &p)
-{
-    const int64_t rows = ceil_div(p.m * (p.q_heads / p.kv_heads), p.seqs);
-    return rows <= 4 ? 1 : rows <= 8 ? 2 : 4;
-}
+// rows of a kv head that a sequence has on average
+static int64_t rows_each(const CachedProblem &p) { return ceil_div(p.m * (p.q_heads / p.kv_heads), p.seqs); }
 
+// tiles of 4 * rt query rows, of all sequences and heads
+static int64_t units_of(const CachedProblem &p, int rt) { return p.seqs * ceil_div(rows_each(p), 4 * rt) * p.kv_heads; }
+
+// A bound of the tiles per head, whatever the sequences' rows are
 static int64_t query_tiles(const CachedProblem &p, int rt)
 {
     const int64_t group = p.q_heads / p.kv_heads, r = 4 * rt;
     return p.packed ? p.m * group / r + p.seqs : p.seqs * ceil_div(group, r);
+}
+
+// Row tiles per workgroup: 4 * rt query rows share a page's loads, but a wave works on
+// them one after the other (0.5 us per page and tile of rows, 16 rows 2.3). Where four
+// rows give no more workgroups than CUs and there is little to read, that spreads the
+// work (4 tokens of 20/5 heads over 1000: 6.9 us with 4 rows, 8.6 with 8, 12.5 with
+// 16); where there is much, the pages are read less often (32 x 8 tokens of 32/8 heads
+// over 2500: 195, 104, 62 us). In between it is 8 rows (16 x 4 tokens of 32/8 heads over
+// 2500: 53.5, 30.6, 40.7 us). Pages counted for every tile, as of 128-wide heads; 482
+// shapes take 1.04 times their best on average by this rule (16 rows wherever a sequence
+// has more than 8: 1.42).
+static int row_tiles(const CachedProblem &p)
+{
+    const int64_t rows = rows_each(p), pages = p.max_blocks * p.head_dim / 64;  // twice them
+    if (rows <= 4) return 1;
+    if (rows > 8 && units_of(p, 4) * pages >= 20000) return 4;
+    return units_of(p, 1) <= 256 && units_of(p, 1) * pages <= 12000 ? 1 : 2;
 }
 
 // Waves per workgroup, and workgroups per sequence, head and tile of query rows
@@ -519,12 +536,13 @@ static int64_t query_tiles(const CachedProblem &p, int rt)
 //    no joining launch (one sequence of 1023 tokens, 20/5 heads: 6.8 us, split over 4
 //    10.0; 2500 tokens 9.6 and 9.6; 3999 12.4 and 9.8; 3000 of 16/4 heads of 64 8.1 and
 //    8.5);
-//  - up to one unit per CU: as many workgroups as give every CU 16 waves (8 with 8
-//    query rows, whose registers allow no more; of 16 rows' workgroups about half
-//    turn out empty), but at least a page per wave;
+//  - up to one unit per CU: as many workgroups as give every CU 16 waves (8 with 8 and
+//    16 query rows, whose registers allow no more), but at least a page per wave;
 //  - between one and one and a half, where whole workgroups would leave the second
 //    round half empty: four waves, split for a thousand workgroups (35 sequences of
-//    7800 tokens, 32/8 heads: 107 against 122 us);
+//    7800 tokens, 32/8 heads: 107 against 122 us); up to two, where there are more
+//    blocks than two per wave, whole ones again (48 x 2 tokens over 300: 14.8 us, with
+//    four waves 11.4);
 //  - two and more: one workgroup per unit, of four waves, which even out unequal
 //    lengths (200 sequences of 2000: 118 against 124 us; 64 of 7800: 168 and 167).
 struct Shape {
@@ -533,11 +551,12 @@ struct Shape {
 };
 static Shape launch_shape(const CachedProblem &p, int rt)
 {
-    const int64_t units = query_tiles(p, rt) * p.kv_heads, cus = 256;
-    const bool wide = units <= cus || (2 * units >= 3 * cus && units < 2 * cus);
+    const int64_t units = units_of(p, rt), cus = 256;
+    const bool lengthy = p.max_blocks * p.head_dim > 256 * 16 / rt;
+    const bool wide = units <= cus || (lengthy && 2 * units >= 3 * cus && units < 2 * cus);
     const int waves = wide ? 16 / rt : 4;
     if (p.max_blocks * p.head_dim <= 256 * waves) return {waves, 1};
-    int64_t s = (rt == 2 ? 8 : 16) * cus / (waves * units);
+    int64_t s = (rt == 1 ? 16 : 8) * cus / (waves * units);
     const int64_t most = ceil_div(p.max_blocks, waves);
     s = s > most ? most : s;
     if (units >= 2 * cus || s < 1) s = 1;
@@ -596,10 +615,10 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
         using T = decltype(type);
         constexpr int D = decltype(width)::value, RT = decltype(tiles)::value, W = decltype(waves)::value;
         in_launches(query_tiles(p, rt), [&](int first, unsigned n) {
-            const dim3 grid(n, (unsigned)p.kv_heads, (unsigned)a.splits);
+            const dim3 grid((unsigned)a.splits, (unsigned)p.kv_heads, n);
             if (p.weights) hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, true>), grid, dim3(64 * W), 0, st, a, first);
             else hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, false>), grid, dim3(64 * W), 0, st, a, first);
-        });
+        }, kMostInZ);
         if (a.splits == 1) return;
         const int64_t rows = p.m * p.q_heads, extra = p.weights ? p.seqs * blocks64 : 0;
         if (a.splits <= kFewSplits)

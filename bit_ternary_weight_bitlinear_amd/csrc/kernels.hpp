@@ -195,9 +195,8 @@ struct CachedProblem {
     float scale;
     void *out;
     float *weights;     // optional [seqs][max_blocks], added to
-    // what the layout of the workspace depends on beside the sizes
     bool packed;        // cu given
-    bool want_weights;
+    bool want_weights;  // the layout of the workspace depends on it and the sizes
 };
 int64_t attention_cached_workspace(const CachedProblem &p);
 hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t st);

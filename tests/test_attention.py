@@ -353,6 +353,22 @@ def test_cached_many_sequences(bl):
     _check_cached(bl, c, lens, new, 4, "f32", True, 2)
 
 
+def test_cached_more_sequences_than_a_launch_holds(bl):
+    """33000 sequences over 7 pages: every one has the bits that it has among the first few with its table, length and query."""
+    seqs, hkv, d = 33000, 2, 64
+    c = _Paged(bl, [400], [40], hkv, d, 5)
+    pages = torch.arange(c.pages - 2, device="cuda", dtype=torch.int32)
+    s = torch.arange(seqs, device="cuda")
+    table = torch.stack([pages[s % 5], pages[(s + 1) % 7]], 1).to(torch.int32).contiguous()
+    lens = (s % 120).to(torch.int32)
+    q = _rand((35, 4, d), 9, torch.bfloat16)[s % 35]
+    for cu in (None, _starts([1] * seqs)):
+        out = bl.attention_cached(q, c.cache, table, lens, cu)
+        n = 840  # after so many everything repeats
+        few = bl.attention_cached(q[:n].contiguous(), c.cache, table[:n].contiguous(), lens[:n].contiguous(), None if cu is None else cu[:n + 1].contiguous())
+        assert torch.equal(out, few[s % n])
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 4.0])
 def test_cached_scales(bl, scale):
     c = _Paged(bl, [500], [2], 2, 64, 4)
