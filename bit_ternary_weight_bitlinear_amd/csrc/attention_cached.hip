@@ -17,8 +17,8 @@
 // 16 bytes per load, every load of a wave contiguous. ~200 VALU operations and 16
 // matrix instructions per 16 KB and four query rows (0.5 us of a SIMD): bound by HBM
 // with four rows a page (64 tokens over 7900, 32/8 heads: 168 us, 6.1 TB/s), by the
-// VALU from eight on. Not kept: the next page's loads ahead of this one's use
-// (registers spill; where they do not, 15.0 beside 15.6 us for four pages per wave).
+// VALU from eight on. Not kept: the next page's V too ahead of its use (registers
+// spill).
 #include "attention.hpp"
 
 namespace bl {
@@ -138,6 +138,41 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
         hq = head * a.group + (int)(u - q * group);
     };
 
+    // ---- the wave's pages: ids and scales of 64 of them, one per lane
+    float my_ks = 0.0f, my_vs = 0.0f;
+    auto fetch_ids = [&](int base) {
+        const int mine = base + W * lane;
+        if (a.splits > 1 || base != wave) ids = mine < p1 ? table[mine] : -1;
+        const bool ok = mine < p1 && ids >= 0 && ids < a.pages;
+        const int64_t my_at = ok ? (int64_t)ids * a.kv_heads + head : 0;
+        // a block without a page reads page 0, of which nothing may enter
+        my_ks = ok ? a.k_scale[my_at] : 0.0f;
+        my_vs = ok ? a.v_scale[my_at] : 0.0f;
+    };
+    auto page_at = [&](int i, bool &there) {
+        const int id = __builtin_amdgcn_readlane(ids, i);
+        there = id >= 0 && id < a.pages;
+        return ((int64_t)(there ? id : 0) * a.kv_heads + head) * (kBlock * D);
+    };
+    v4i kf[4][H];
+    auto load_k = [&](int i) {
+        bool there;
+        const uint4 *kp = reinterpret_cast<const uint4 *>(a.k_codes + page_at(i, there)) + lane;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int h = 0; h < H; ++h) kf[tt][h] = *reinterpret_cast<const v4i *>(kp + (tt * H + h) * 64);
+    };
+    // K of a page is asked for as soon as the one before has been used, the first while
+    // the query rows are made ready (one token over 1024, 20/5 heads: 6.3 us beside 6.7);
+    // 16 rows leave no registers for it
+    constexpr bool EARLY = RT < 4;
+    int base = p0 + wave;
+    if (EARLY && base < p1) {
+        fetch_ids(base);
+        load_k(0);
+    }
+
     // ---- query rows as digits, 16 lanes per row
     for (int r = tid >> 4; r < R; r += 4 * W) {
         const bool there = r < rows;
@@ -216,25 +251,16 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
         for (int n = 0; n < N; ++n) acc[rt][n] = 0.0f;
     }
 
-    for (int base = p0 + wave; base < p1; base += 64 * W) {
-        // ids and scales of the wave's next 64 pages, one per lane
-        const int mine = base + W * lane;
-        if (a.splits > 1 || base != wave) ids = mine < p1 ? table[mine] : -1;
-        const bool ok = mine < p1 && ids >= 0 && ids < a.pages;
-        const int64_t my_at = ok ? (int64_t)ids * a.kv_heads + head : 0;
-        // a block without a page reads page 0, of which nothing may enter
-        const float my_ks = ok ? a.k_scale[my_at] : 0.0f, my_vs = ok ? a.v_scale[my_at] : 0.0f;
+    for (; base < p1; base += 64 * W) {
+        if (!EARLY || base != p0 + wave) {
+            fetch_ids(base);
+            if (EARLY) load_k(0);
+        }
         for (int p = base, i = 0; p < p1 && i < 64; p += W, ++i) {
-            const int id = __builtin_amdgcn_readlane(ids, i);
-            const bool there = id >= 0 && id < a.pages;
-            const int64_t at = (int64_t)(there ? id : 0) * a.kv_heads + head;
-            const uint4 *kp = reinterpret_cast<const uint4 *>(a.k_codes + at * (kBlock * D)) + lane;
-            const uint4 *vp = reinterpret_cast<const uint4 *>(a.v_codes + at * (kBlock * D)) + lane;
-            v4i kf[4][H], vf[N];
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                for (int h = 0; h < H; ++h) kf[tt][h] = *reinterpret_cast<const v4i *>(kp + (tt * H + h) * 64);
+            bool there;
+            const uint4 *vp = reinterpret_cast<const uint4 *>(a.v_codes + page_at(i, there)) + lane;
+            if (!EARLY) load_k(i);
+            v4i vf[N];
 #pragma unroll
             for (int n = 0; n < N; ++n) vf[n] = *reinterpret_cast<const v4i *>(vp + n * 64);
             const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_ks), i)) / 127.0f;
@@ -257,6 +283,7 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
                     x[tt] = seen ? join_digits(s) * f : kNegInf;
                     big = fmaxf(big, x[tt]);
                 }
+                if (EARLY && rt == RT - 1 && p + W < p1 && i < 63) load_k(i + 1);  // the next page's
                 big = row16_max(big);
                 const float ref = big == kNegInf ? 0.0f : big;
                 float total = 0.0f;
