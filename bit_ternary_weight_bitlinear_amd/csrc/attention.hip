@@ -537,6 +537,38 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
     const int r_wave = t.tile * ROWS + wave / KS * 32;
     const int b0 = KS == 1 ? 0 : wave % KS;               // the wave's 32 keys of a tile
 
+    const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
+    const int tiles = last_row / group / KEYS + 1;
+    const int group_masked = (t.tile * ROWS / group + 1) / KEYS;
+    const int wave_masked = ((r_wave < rows ? r_wave : rows - 1) / group + 1) / KEYS;
+
+    const uint32_t base = lds_addr(lds);
+    const int load_row = wave * (kLoadRows / 4) + lane / kChunks;
+    const int k_chunk = ((lane % kChunks) ^ k_swizzle<D>(load_row)) * 16, v_chunk = ((lane % kChunks) ^ v_swizzle<D>(load_row)) * 16;
+    const int64_t plane_rows = a.m * a.kv_heads, first_row = (int64_t)head * a.m + t.begin;
+    auto request = [&](int tile) {
+        const uint32_t to = base + (tile & 1) * kStage;
+        const int left = t.n - 1 - tile * KEYS;
+#pragma unroll
+        for (int is_v = 0; is_v < 2; ++is_v) {
+            const char *from = planes + (is_v * plane_rows + first_row + (int64_t)tile * KEYS) * (D * 4);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int row = i * kLoadRows + load_row;
+                const uint32_t off = (uint32_t)(row < left ? row : left) * (D * 4) + (is_v ? v_chunk : k_chunk);
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo) dma16(from + lo * D * 2, off, to + (2 * is_v + lo) * kPlane + (4 * i + wave) * 1024);
+            }
+        }
+        if (wave < 2) {  // scales of K, V: 64 keys (32 of them twice where a tile has no more)
+            const int key = lane % KEYS;
+            dma4(scales + wave * plane_rows + first_row + (int64_t)tile * KEYS, (uint32_t)(key < left ? key : left) * 4,
+                 to + 4 * kPlane + wave * 256);
+        }
+    };
+
+    request(0);
+
     int tok;
     float c;
     v8h qh[C], ql[C];
@@ -569,36 +601,6 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
                 ql[i][e] = lo16;
             }
     }
-    const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
-    const int tiles = last_row / group / KEYS + 1;
-    const int group_masked = (t.tile * ROWS / group + 1) / KEYS;
-    const int wave_masked = ((r_wave < rows ? r_wave : rows - 1) / group + 1) / KEYS;
-
-    const uint32_t base = lds_addr(lds);
-    const int load_row = wave * (kLoadRows / 4) + lane / kChunks;
-    const int k_chunk = ((lane % kChunks) ^ k_swizzle<D>(load_row)) * 16, v_chunk = ((lane % kChunks) ^ v_swizzle<D>(load_row)) * 16;
-    const int64_t plane_rows = a.m * a.kv_heads, first_row = (int64_t)head * a.m + t.begin;
-    auto request = [&](int tile) {
-        const uint32_t to = base + (tile & 1) * kStage;
-        const int left = t.n - 1 - tile * KEYS;
-#pragma unroll
-        for (int is_v = 0; is_v < 2; ++is_v) {
-            const char *from = planes + (is_v * plane_rows + first_row + (int64_t)tile * KEYS) * (D * 4);
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int row = i * kLoadRows + load_row;
-                const uint32_t off = (uint32_t)(row < left ? row : left) * (D * 4) + (is_v ? v_chunk : k_chunk);
-#pragma unroll
-                for (int lo = 0; lo < 2; ++lo) dma16(from + lo * D * 2, off, to + (2 * is_v + lo) * kPlane + (4 * i + wave) * 1024);
-            }
-        }
-        if (wave < 2) {  // scales of K, V: 64 keys (32 of them twice where a tile has no more)
-            const int key = lane % KEYS;
-            dma4(scales + wave * plane_rows + first_row + (int64_t)tile * KEYS, (uint32_t)(key < left ? key : left) * 4,
-                 to + 4 * kPlane + wave * 256);
-        }
-    };
-
     int k_at[C], v_at[DT];
 #pragma unroll
     for (int i = 0; i < C; ++i) k_at[i] = (32 * b0 + col) * (D * 2) + (((2 * i + h) ^ k_swizzle<D>(col)) << 4);
@@ -640,7 +642,6 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
         }
     };
 
-    request(0);
     for (int tile = 0; tile < tiles; ++tile) {
         ring_barrier<0>();
         if (tile + 1 < tiles) request(tile + 1);
