@@ -63,69 +63,78 @@ constexpr float kSlack = 8.0f;
 
 constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;
 
-// Where a tile's mask leaves out keys, 0 * v must not bring a NaN or infinity of
-// theirs into the sum. The workgroup looks through such a tile of V (the last one
-// or two) when it has arrived; what is not finite becomes 0 there, and a second
-// tile holds what it was: +inf as 1, -inf as 2^7, NaN as 2^14. A product of that
-// tile with the mask counts per dim and row what the row sees (at most 64 of each,
-// so fp32 holds all three counts).
-struct Bf16Bits {
-    static constexpr uint32_t kExp = 0x7F80, kMan = 0x7F, kOne = 0x3F80, k128 = 0x4300, k16384 = 0x4680;
-};
-struct F16Bits {
-    static constexpr uint32_t kExp = 0x7C00, kMan = 0x3FF, kOne = 0x3C00, k128 = 0x5800, k16384 = 0x7400;
-};
-template <typename B>
-__device__ inline bool not_finite_pair(uint32_t w) { return (w & B::kExp) == B::kExp || (w >> 16 & B::kExp) == B::kExp; }
-template <typename B>
+// Elements of V that are not finite: 0 * v must not bring them into rows that do not see
+// them, and a rescale by 2^-inf must not make a NaN of an infinity. Where a tile's mask
+// leaves out keys, the workgroup looks through such a tile of V (the last one or two) when
+// it has arrived and sets them to 0. What they make of a row is settled when it is stored.
+__device__ inline bool not_finite_pair(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w >> 16 & 0x7F80u) == 0x7F80u; }
 __device__ inline uint32_t finite_pair(uint32_t w)
 {
-    if ((w >> 16 & B::kExp) == B::kExp) w &= 0x0000FFFFu;
-    if ((w & B::kExp) == B::kExp) w &= 0xFFFF0000u;
+    if ((w >> 16 & 0x7F80u) == 0x7F80u) w &= 0x0000FFFFu;
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
     return w;
 }
-template <typename B>
-__device__ inline uint32_t counted(uint32_t b)
-{
-    return (b & B::kExp) != B::kExp ? 0u : b & B::kMan ? B::k16384 : b & 0x8000u ? B::k128 : B::kOne;
-}
-template <typename B>
-__device__ inline uint32_t counted_pair(uint32_t w) { return counted<B>(w & 0xFFFFu) | counted<B>(w >> 16) << 16; }
-__device__ inline float counted_value(float n)
-{
-    const int c = (int)n, plus = c & 127, minus = (c >> 7) & 127;
-    return c >= 1 << 14 || (plus && minus) ? __builtin_nanf("") : plus ? __builtin_inff() : minus ? kNegInf : 0.0f;
-}
 
-// The first half of it, by the workgroup: whether the tile held any
-template <typename B, int BYTES, int WAVES>
-__device__ inline bool set_aside(char *tile, char *counts)
+// by the workgroup: whether the tile held any
+template <int BYTES, int WAVES>
+__device__ inline bool set_aside(char *tile, int *flags)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    char *vt = tile + wave * (BYTES / WAVES) + lane * 16, *ct = counts + wave * (BYTES / WAVES) + lane * 16;
+    char *vt = tile + wave * (BYTES / WAVES) + lane * 16;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < BYTES / (1024 * WAVES); ++i) {
         const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
-        bad = bad || not_finite_pair<B>(w.x) || not_finite_pair<B>(w.y) || not_finite_pair<B>(w.z) || not_finite_pair<B>(w.w);
+        bad = bad || not_finite_pair(w.x) || not_finite_pair(w.y) || not_finite_pair(w.z) || not_finite_pair(w.w);
     }
-    int *flags = reinterpret_cast<int *>(counts), any = 0;
+    int any = 0;
     bad = __any(bad);
     if (lane == 0) flags[wave] = bad;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) any |= flags[i];
     if (!any) return false;
-    __syncthreads();
     for (int i = 0; i < BYTES / (1024 * WAVES); ++i) {
         const uint4 w = *reinterpret_cast<const uint4 *>(vt + i * 1024);
-        *reinterpret_cast<uint4 *>(vt + i * 1024) =
-            make_uint4(finite_pair<B>(w.x), finite_pair<B>(w.y), finite_pair<B>(w.z), finite_pair<B>(w.w));
-        *reinterpret_cast<uint4 *>(ct + i * 1024) =
-            make_uint4(counted_pair<B>(w.x), counted_pair<B>(w.y), counted_pair<B>(w.z), counted_pair<B>(w.w));
+        *reinterpret_cast<uint4 *>(vt + i * 1024) = make_uint4(finite_pair(w.x), finite_pair(w.y), finite_pair(w.z), finite_pair(w.w));
     }
     __syncthreads();
     return true;
+}
+
+// Groups first .. first+n-1 of a stored row (dims 32 * (i / 4) + 8 * (i % 4) + 4h .. +3),
+// once more where they are not finite, or V was set aside: an element becomes NaN where
+// the row sees a NaN, or infinities of both signs, among its `keys` elements of V, and the
+// infinity where it sees one. Only inputs that hold such values come here.
+template <typename T>
+__device__ inline void settle(T *dst, const T *v, int64_t stride, int keys, int first, int n, bool aside)
+{
+    for (int i = first; i < first + n; ++i) {
+        const int at = 32 * (i >> 2) + 8 * (i & 3);
+        float zero = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zero = __builtin_fmaf(to_f32(dst[at + e]), 0.0f, zero);
+        if (!aside && zero == 0.0f) continue;
+        const T *from = v + at;
+        int plus = 0, minus = 0;  // bit e: element e has met one (both: NaN)
+#pragma unroll 4
+        for (int j = 0; j < keys; ++j, from += stride) {
+            T w[4];
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(from);
+            else *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(from);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float f = to_f32(w[e]);
+                const bool finite = fabsf(f) <= 3.402823466e38f;
+                plus |= !finite && f != kNegInf ? 1 << e : 0;
+                minus |= !finite && f != -kNegInf ? 1 << e : 0;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((plus | minus) >> e & 1)
+                store_out(dst + at + e, plus & minus & 1 << e ? __builtin_nanf("") : plus >> e & 1 ? -kNegInf : kNegInf);
+    }
 }
 
 // registers 4 * (i % 4) .. +3 of accumulator i / 4
@@ -136,14 +145,16 @@ __device__ inline v4f o_group(const v16f (&o)[DT], int i)
     return v4f{o[d][g], o[d][g + 1], o[d][g + 2], o[d][g + 3]};
 }
 
+template <int DT>
+constexpr int kJoinPart = DT * 4096 + 3 * 256;  // bytes of a wave's results
+
 // KS neighbouring waves hold the same rows over different keys: each writes its
 // accumulators, maximum, sum and the scale of its accumulators (relative to 2^mx) and
-// joins a KS-th of the dims, which it gives to store with what they are to be
-// multiplied by.
+// joins a KS-th of the dims, which it gives to store with 1 / sum and the scale.
 template <int DT, int KS, typename F>
 __device__ inline void join_waves(char *lds, const v16f (&o)[DT], float mx, float sum, float scale, F store)
 {
-    constexpr int kPart = DT * 4096 + 3 * 256, N = 4 * DT / KS;
+    constexpr int kPart = kJoinPart<DT>, N = 4 * DT / KS;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), mine = wave % KS;
     char *parts = lds + wave / KS * KS * kPart;
     __syncthreads();
@@ -172,7 +183,7 @@ __device__ inline void join_waves(char *lds, const v16f (&o)[DT], float mx, floa
     }
 #pragma unroll
     for (int p = 0; p < KS; ++p) f[p] /= most;
-    const float inv = most / all;
+    const float inv = 1.0f / all;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int i = mine * N + n;
@@ -183,7 +194,7 @@ __device__ inline void join_waves(char *lds, const v16f (&o)[DT], float mx, floa
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(w[e], f[p], v[e]);
         }
-        store(i, v, inv);
+        store(i, v, inv, most);
     }
 }
 
@@ -197,8 +208,9 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
     constexpr int kLoads = kTile / (1024 * WAVES);        // direct loads per wave and tile
     constexpr int kChunks = D / 8;                        // 16-byte chunks per row
     constexpr int kLoadRows = KEYS / kLoads;              // rows that one load of all waves brings
-    // K, K, V, V, counts of what is not finite
-    __shared__ __align__(1024) char lds[5 * kTile];
+    constexpr int kTiles = 4 * kTile, kJoin = KS > 1 ? WAVES * kJoinPart<DT> : 0;
+    __shared__ __align__(1024) char lds[kTiles > kJoin ? kTiles : kJoin];  // K, K, V, V; the waves' results
+    __shared__ int flags[WAVES];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, col = lane & 31;
@@ -287,26 +299,7 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = v16f{};
 
-    // V of a masked tile, once it is there: keeps what is not finite from rows that do not see it
-    auto clean = [&](int tile) {
-        if (!set_aside<Bf16Bits, kTile, WAVES>(lds + (2 + (tile & 1)) * kTile, lds + 4 * kTile)) return;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            v16f count = {};
-#pragma unroll
-            for (int n = 0; n < 2 * NB; ++n) {
-                const int kc = 2 * b0 + n;
-                v8bf seen;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    seen[i] = (__bf16)(tile * KEYS + 16 * kc + 8 * (i >> 2) + 4 * h + (i & 3) <= tok ? 1.0f : 0.0f);
-                count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_fragment(4, n, d), seen, count, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[d][i] += counted_value(count[i]);
-        }
-    };
-
+    bool aside = false;  // a masked tile of V held values that are not finite
     v16f s[NB];
     // the fragments in the order of their use: n / NB is the 16 dims, n % NB the block of keys
     auto k_nth = [&](int tile, int n) { return k_fragment(tile, n % NB, n / NB); };
@@ -337,7 +330,7 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
         if (!AHEAD && tile + 1 < tiles) request_k(tile + 1);
         if (tile + 1 < tiles) request_v(tile + 1);
         if (AHEAD && tile + 2 < tiles) request_k(tile + 2);
-        if (tile >= group_masked) clean(tile);
+        if (tile >= group_masked) aside |= set_aside<kTile, WAVES>(lds + (2 + (tile & 1)) * kTile, flags);
 
         if constexpr (AHEAD) {
             read_k(tile + 1);  // old bytes of the buffer, and of no use, behind the last tile
@@ -417,11 +410,14 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 
     const int r = r_wave + col;
     bf16_t *dst = static_cast<bf16_t *>(a.out) + ((t.begin + tok) * a.q_heads + head * group + r % group) * D + 4 * h;
-    auto store = [&](int i, const v4f &v, float inv) {  // dims 32 * (i / 4) + 8 * (i % 4) + 4 * h .. +3
+    float all = 0.0f, norm = 0.0f;
+    auto store = [&](int i, const v4f &v, float inv, float) {  // dims 32 * (i / 4) + 8 * (i % 4) + 4 * h .. +3
         bf16_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) store_out(&w[e], v[e] * inv);
         *reinterpret_cast<uint2 *>(dst + 32 * (i >> 2) + 8 * (i & 3)) = *reinterpret_cast<const uint2 *>(w);
+        all += (v[0] + v[1]) + (v[2] + v[3]);
+        norm = inv;
     };
     if constexpr (KS == 1) {
         float lo, up;
@@ -429,10 +425,13 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
         const float inv = 1.0f / (lo + up);
         if (r >= rows) return;
 #pragma unroll
-        for (int i = 0; i < 4 * DT; ++i) store(i, o_group(o, i), inv);
+        for (int i = 0; i < 4 * DT; ++i) store(i, o_group(o, i), inv, 1.0f);
     } else {
-        join_waves<DT, KS>(lds, o, mx, sum, 1.0f, [&](int i, const v4f &v, float inv) { if (r < rows) store(i, v, inv); });
+        join_waves<DT, KS>(lds, o, mx, sum, 1.0f, [&](int i, const v4f &v, float inv, float one) { if (r < rows) store(i, v, inv, one); });
     }
+    // not where the weights have no sum: such a row is NaN whatever V holds
+    if ((aside || all - all != 0.0f) && norm - norm == 0.0f && r < rows)
+        settle(dst, static_cast<const bf16_t *>(a.v) + t.begin * a.v_stride + head * D + 4 * h, a.v_stride, tok + 1, wave % KS * (4 * DT / KS), 4 * DT / KS, aside);
 }
 
 // ---------------------------------------------------------------- fp32 on the matrix cores
@@ -448,7 +447,9 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 // The scale of K's rows multiplies the logits. That of V's rows goes into the
 // weights: w_j = p_j 2^a_j / ref with ref the running maximum of p_j 2^a_j, so that
 // hi and lo of w keep 22 bits of the largest products (and a row of V counts for as
-// much as its weight lets it, however large it is).
+// much as its weight lets it, however large it is). Elements of V that are not finite are
+// 0 in both parts, and their row's scale is negative: rows that see one are settled when
+// they are stored.
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 constexpr float kSlackF32 = 3.0f;      // as kSlack
 constexpr float kMostWeight = 8.0f;    // the same for w ...
@@ -497,12 +498,19 @@ __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a
     float scale, inv;
     row_scale(big, scale, inv);
     _Float16 hi[4], lo[4];
+    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split_f16((&x.x)[i] * inv, hi[i], lo[i]);
+    for (int i = 0; i < 4; ++i) {
+        const float f = (&x.x)[i];
+        const bool odd = is_v && !(fabsf(f) <= 3.402823466e38f);
+        split_f16(odd ? 0.0f : f * inv, hi[i], lo[i]);
+        bad |= odd;
+    }
+    const uint64_t any = __ballot(bad) >> (threadIdx.x & 63 & ~(L - 1)) & ((1ull << L) - 1);
     char *dst = planes + (is_v * rows + at) * (D * 4) + lane * 8;
     *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(hi);
     *reinterpret_cast<uint2 *>(dst + D * 2) = *reinterpret_cast<const uint2 *>(lo);
-    if (lane == 0) scales[is_v * rows + at] = scale;
+    if (lane == 0) scales[is_v * rows + at] = any ? -scale : scale;
 }
 
 // The loop of attention_bf16_kernel (as it is there with KS = 1) with the four 16-bit
@@ -523,7 +531,8 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
     constexpr int kLoads = kPlane / (1024 * 4);           // direct loads per wave and plane
     constexpr int kChunks = D / 8, kLoadRows = KEYS / kLoads;
     constexpr int kStage = 4 * kPlane + 512;              // K hi, lo, V hi, lo, scales of K and V
-    __shared__ __align__(1024) char lds[2 * kStage + kPlane];
+    static_assert(KS == 1 || 2 * kStage >= 4 * kJoinPart<DT>, "the waves' results fit");
+    __shared__ __align__(1024) char lds[2 * kStage];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, col = lane & 31;
@@ -539,7 +548,6 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 
     const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
     const int tiles = last_row / group / KEYS + 1;
-    const int group_masked = (t.tile * ROWS / group + 1) / KEYS;
     const int wave_masked = ((r_wave < rows ? r_wave : rows - 1) / group + 1) / KEYS;
 
     const uint32_t base = lds_addr(lds);
@@ -623,29 +631,10 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = v16f{};
 
-    auto clean = [&](int tile) {
-        const uint32_t counts = base + 2 * kStage;
-        if (!set_aside<F16Bits, kPlane, 4>(lds + (tile & 1) * kStage + 2 * kPlane, lds + 2 * kStage)) return;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            v16f count = {};
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                v8h seen;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    seen[i] = (_Float16)(tile * KEYS + 32 * b0 + 16 * n + 8 * (i >> 2) + 4 * h + (i & 3) <= tok ? 1.0f : 0.0f);
-                count = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_fragment(counts, n, d), seen, count, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[d][i] += counted_value(count[i]);
-        }
-    };
-
+    int aside = 0;  // negative: a tile of V held values that are not finite
     for (int tile = 0; tile < tiles; ++tile) {
         ring_barrier<0>();
         if (tile + 1 < tiles) request(tile + 1);
-        if (tile >= group_masked) clean(tile);
         const char *stage = lds + (tile & 1) * kStage;
         const uint32_t vt = base + (tile & 1) * kStage + 2 * kPlane;
 
@@ -668,6 +657,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
         __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 3 * kAhead, 0);
         // scales of keys 8g + 4h .. +3
         const float *sc = reinterpret_cast<const float *>(stage + 4 * kPlane) + 32 * b0 + 4 * h;
+        aside |= reinterpret_cast<const int *>(stage + 4 * kPlane)[64 + lane];
         float gv[16];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -675,7 +665,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s[4 * g + i] *= (&k4.x)[i];
-                gv[4 * g + i] = (&v4.x)[i];
+                gv[4 * g + i] = fabsf((&v4.x)[i]);
             }
         }
         if (tile >= wave_masked) {
@@ -745,19 +735,26 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 
     const int r = r_wave + col;
     float *dst = static_cast<float *>(a.out) + ((t.begin + tok) * a.q_heads + head * group + r % group) * D + 4 * h;
-    auto store = [&](int i, const v4f &v, float inv) {
-        *reinterpret_cast<v4f *>(dst + 32 * (i >> 2) + 8 * (i & 3)) = v4f{v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    const bool any_aside = __any(aside < 0);
+    float all = 0.0f, norm = 0.0f;
+    auto store = [&](int i, const v4f &v, float inv, float scale) {
+        *reinterpret_cast<v4f *>(dst + 32 * (i >> 2) + 8 * (i & 3)) = v4f{v[0] * inv * scale, v[1] * inv * scale, v[2] * inv * scale, v[3] * inv * scale};
+        all += (v[0] + v[1]) + (v[2] + v[3]);
+        norm = inv;
     };
     if constexpr (KS == 1) {
         float lo, up;
         both_halves(sum, lo, up);
-        const float inv = (ref_w / kWeightOne) / (lo + up);
+        const float inv = 1.0f / (lo + up);
         if (r >= rows) return;
 #pragma unroll
-        for (int i = 0; i < 4 * DT; ++i) store(i, o_group(o, i), inv);
+        for (int i = 0; i < 4 * DT; ++i) store(i, o_group(o, i), inv, ref_w / kWeightOne);
     } else {
-        join_waves<DT, KS>(lds, o, mx, sum, ref_w / kWeightOne, [&](int i, const v4f &v, float inv) { if (r < rows) store(i, v, inv); });
+        join_waves<DT, KS>(lds, o, mx, sum, ref_w / kWeightOne,
+                           [&](int i, const v4f &v, float inv, float scale) { if (r < rows) store(i, v, inv, scale); });
     }
+    if ((any_aside || all - all != 0.0f) && norm - norm == 0.0f && r < rows)
+        settle(dst, static_cast<const float *>(a.v) + t.begin * a.v_stride + head * D + 4 * h, a.v_stride, tok + 1, wave % KS * (4 * DT / KS), 4 * DT / KS, any_aside);
 }
 
 // Few workgroups: a tile's keys are split over two waves (KS = 2), so that there
