@@ -447,9 +447,12 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 // The scale of K's rows multiplies the logits. That of V's rows goes into the
 // weights: w_j = p_j 2^a_j / ref with ref the running maximum of p_j 2^a_j, so that
 // hi and lo of w keep 22 bits of the largest products (and a row of V counts for as
-// much as its weight lets it, however large it is). Elements of V that are not finite are
-// 0 in both parts, and their row's scale is negative: rows that see one are settled when
-// they are stored.
+// much as its weight lets it, however large it is).
+// An infinity times a second part, which may be 0 or of the other sign, is not what the
+// definition has. K's elements that are not finite are lo, with a hi of 0: lo meets q's
+// first part only, and the product has q's sign (q's own make their rows NaN either way).
+// V's are 0 in both parts, and their row's scale is negative: rows that see one are
+// settled when they are stored.
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 constexpr float kSlackF32 = 3.0f;      // as kSlack
 constexpr float kMostWeight = 8.0f;    // the same for w ...
@@ -502,9 +505,10 @@ __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float f = (&x.x)[i];
-        const bool odd = is_v && !(fabsf(f) <= 3.402823466e38f);
+        const bool odd = !(fabsf(f) <= 3.402823466e38f);
         split_f16(odd ? 0.0f : f * inv, hi[i], lo[i]);
-        bad |= odd;
+        if (odd && !is_v) lo[i] = (_Float16)f;
+        bad |= odd && is_v;
     }
     const uint64_t any = __ballot(bad) >> (threadIdx.x & 63 & ~(L - 1)) & ((1ull << L) - 1);
     char *dst = planes + (is_v * rows + at) * (D * 4) + lane * 8;

@@ -352,12 +352,14 @@ size_t bitlinear_attention_workspace_size(bl_dtype dtype, int64_t m, int64_t q_h
  * and v no closer than 2^-39 of the largest of their row (one token and head), and
  * the weights no closer than 2^-36 of the row's largest p_ij max |v_j|.
  * A row depends on rows 0..i of its own sequence only: infinities and NaN in
- * later rows or in other sequences do not reach it. An element of v_j that is not
+ * later rows or in other sequences do not reach it. Those that a row sees count as
+ * the formula has them: a logit of -inf gives its key no weight; one of +inf or NaN
+ * makes the row NaN, as -inf in all of them does. An element of v_j that is not
  * finite reaches every row that sees it, whatever its weight: as NaN where the row
  * sees a NaN or infinities of both signs in that dim, otherwise as the infinity
- * (but a row of NaN weights is NaN throughout). BL_ERR_SHAPE also where
- * m * q_heads / kv_heads, or its 64th part (plus seqs) times kv_heads, passes
- * 2^31 - 1024.
+ * (but a row of NaN weights is NaN throughout).
+ * BL_ERR_SHAPE also where m * q_heads / kv_heads, or its 64th part (plus seqs)
+ * times kv_heads, passes 2^31 - 1024.
  *   workspace  >= bitlinear_attention_workspace_size() bytes
  */
 bl_status bitlinear_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,

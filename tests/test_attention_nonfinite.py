@@ -1,9 +1,11 @@
-"""Prompt attention where q, k or v hold infinities or NaN that a row sees: an element of V that is not finite reaches
-every row that sees it, whatever its weight: NaN for NaN or infinities of both signs, otherwise that infinity."""
+"""Prompt attention where q, k or v hold infinities or NaN that a row sees: a logit of -inf gives its key no weight;
+one of +inf or NaN, or only -inf ones, make the row NaN; an element of V that is not finite reaches every row that sees
+it, whatever its weight: NaN for NaN or infinities of both signs, otherwise that infinity."""
 import numpy as np
 import pytest
 
-from tests.test_attention import DTYPES, _rand, _starts, bl, torch  # noqa: F401
+from oracle import attention as ref
+from tests.test_attention import DTYPES, _assert_within, _np, _prompt_tolerance, _rand, _starts, bl, torch  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +64,55 @@ def test_no_value_reaches_a_row_without_weights(bl, dtype, more):  # noqa: F811
     out = bl.attention(q, k, v, _starts(lens)).view(m, hq, d)
     assert torch.isnan(out[50, 1]).all() and torch.isnan(out[70]).all() and torch.isnan(out[0, 2:]).all()
     assert (out[50, 0, 7] == INF).all() and torch.isfinite(out[1, :2]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [None, -0.2])
+@pytest.mark.parametrize("more", [0, 300])
+def test_keys_that_are_not_finite(bl, dtype, d, scale, more):  # noqa: F811
+    """An infinity in a key is a logit of its sign times q's: -inf and the key has no weight, +inf and the row is NaN, as
+    it is for 0 * inf, for infinities of both signs, and for NaN."""
+    lens, hq, hkv = [40, 333, 120] + [9] * more, 6, 2
+    m, group, sign = sum(lens), 3, -1.0 if scale else 1.0
+    q, k, v = (_rand((m, h, d), 101 + i, DTYPES[dtype]) for i, h in enumerate((hq, hkv, hkv)))
+    q[::3, :, 2] = 1.0                    # values without a second part
+    q[::5, :, 2] = -1.0
+    q[60, :, 2] = 0.0
+    k[7, :, 2], k[41, :, 2], k[100, 0, 3], k[373 + 64, 1, d - 1] = INF, INF, -INF, INF
+    k[200, 0, 4], k[200, 0, 5] = INF, -INF
+    k[330, 1, 8] = NAN
+    out = _np(bl.attention(q, k, v, _starts(lens), scale=scale)).reshape(m, hq, d)
+    qn, kn, vn = _np(q).astype(np.float64), _np(k).astype(np.float64), _np(v)
+    with np.errstate(invalid="ignore"):
+        logits = sign * np.stack([_odd_products(qn[:, h], kn[:, h // group]) for h in range(hq)])
+    bound = np.concatenate([[0], np.cumsum(lens)])
+    finite = np.where(np.isfinite(kn), kn, 0.0)
+    checked = {"nan": 0, "no weight": 0}
+    use = d ** -0.5 if scale is None else scale
+    for a, b in zip(bound[:3], bound[1:4]):
+        seen = np.tril(np.ones((b - a, b - a), bool))
+        for h in range(hq):
+            odd = logits[h, a:b, a:b]
+            nan_row = (seen & (np.isnan(odd) | (odd == INF))).any(1)
+            none = seen & (odd == -INF)
+            kk, vv = finite[a:b, h // group], vn[a:b, h // group]
+            nan_row |= ~(seen & ~none).any(1)
+            assert np.isnan(out[a:b, h][nan_row]).all(), (a, h)
+            p = ref._softmax(use * (qn[a:b, h] @ kk.T), seen & ~none)
+            reach = np.where(seen, abs(use) * (np.abs(qn[a:b, h]) @ np.abs(kk).T), 0).max(1)[:, None]
+            ok = ~nan_row
+            _assert_within(out[a:b, h][ok], (p @ vv)[ok], _prompt_tolerance(p @ vv, p @ np.abs(vv), reach, b - a, d, dtype)[ok], f"{a} {h}")
+            checked["nan"] += int(nan_row.sum())
+            checked["no weight"] += int((none.any(1) & ok).sum())
+    assert checked["nan"] > 50 and checked["no weight"] > 50
+    assert np.isfinite(out[bound[3]:]).all()
+
+
+def _odd_products(q, k):
+    """Sums of q_d k_d over the dims in which k is not finite (0 for keys that are), [rows][keys]."""
+    out = np.zeros((q.shape[0], k.shape[0]))
+    for j in np.flatnonzero(~np.isfinite(k).all(1)):
+        dims = ~np.isfinite(k[j])
+        out[:, j] = (q[:, dims] * k[j, dims]).sum(1)
+    return out
