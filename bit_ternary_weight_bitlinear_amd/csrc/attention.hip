@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[d][i] *= keep;
         }
-        const float ref = KS > 1 && mx == kNegInf ? 0.0f : mx;  // -inf: none of the wave's keys is seen yet
+        const float ref = mx == kNegInf ? 0.0f : mx;  // -inf: no key with a weight yet
         v8bf vf[AHEAD ? 2 * NB : 1][DT];
         v16f next[NB];
         if constexpr (AHEAD) {
@@ -693,7 +693,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
             sum *= keep;
             ref_w *= keep;
         }
-        const float ref = KS > 1 && mx == kNegInf ? 0.0f : mx;
+        const float ref = mx == kNegInf ? 0.0f : mx;
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -713,7 +713,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[d][i] *= keep;
         }
-        const float to_w = ref_w == 0.0f ? 0.0f : kWeightOne / ref_w;  // 0: none of the wave's keys is seen yet
+        const float to_w = ref_w == 0.0f ? 0.0f : kWeightOne / ref_w;  // 0: no key with a weight yet
         v8h ph[2], pl[2];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {

@@ -68,6 +68,29 @@ def test_no_value_reaches_a_row_without_weights(bl, dtype, more):  # noqa: F811
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("more", [0, 300])
+def test_a_first_tile_of_keys_without_weight(bl, dtype, d, more):  # noqa: F811
+    """Every key of the first 64 (and 130) rows has the logit -inf: rows behind them are the rest's, rows among them NaN."""
+    lens, hq, hkv = [90, 300] + [9] * more, 4, 2
+    m, cu = sum(lens), np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = (_rand((m, h, d), 91 + i, DTYPES[dtype]) for i, h in enumerate((hq, hkv, hkv)))
+    q[..., 5] = -q[..., 5].abs() - 0.25
+    k[:64, :, 5] = INF
+    k[90:90 + 130, :, 5] = INF
+    out = _np(bl.attention(q, k, v, _starts(lens))).reshape(m, hq, d)
+    assert np.isnan(out[:64]).all() and np.isnan(out[90:220]).all()
+    finite = k.clone()
+    finite[:64, :, 5], finite[90:220, :, 5] = 0.0, 0.0
+    want, spread, reach = np.zeros((m, hq, d)), np.zeros((m, hq, d)), np.zeros((m, hq, 1))
+    for a, skip, b in [(0, 64, 90), (90, 130, 390)] + [(int(x), 0, int(y)) for x, y in zip(cu[2:-1], cu[3:])]:
+        w = ref.attention(_np(q)[a + skip:b], _np(finite)[a + skip:b], _np(v)[a + skip:b], [0, b - a - skip], d ** -0.5)
+        want[a + skip:b], spread[a + skip:b], reach[a + skip:b] = w
+    rows = np.concatenate([np.arange(64, 90), np.arange(220, m)])
+    _assert_within(out[rows], want[rows], _prompt_tolerance(want, spread, reach, max(lens), d, dtype)[rows])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("scale", [None, -0.2])
 @pytest.mark.parametrize("more", [0, 300])
 def test_keys_that_are_not_finite(bl, dtype, d, scale, more):  # noqa: F811
