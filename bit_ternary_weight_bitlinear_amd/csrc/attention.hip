@@ -61,6 +61,9 @@ __device__ inline void both_halves(float v, float &lower, float &upper)
 // which neither bf16 nor the fp32 sums notice.
 constexpr float kSlack = 8.0f;
 
+// |scale| log2 e; neither 0 nor infinite, so that it leaves masked logits, and ones of 0, as they are
+__device__ inline float logit_factor(float scale) { return fminf(fmaxf(fabsf(scale) * kLog2e, 1e-45f), 3.402823466e38f); }
+
 constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;
 
 // Elements of V that are not finite: 0 * v must not bring them into rows that do not see
@@ -225,7 +228,7 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
     const int b0 = KS == 1 ? 0 : wave % KS;               // the wave's 32-key blocks of a tile: b0 .. b0+NB-1
 
     // query rows (rows past the last one repeat it and are not stored)
-    const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+    const float c = logit_factor(a.scale);
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     int tok;
     v8bf qf[C];
@@ -440,10 +443,12 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
 // x / 2^a and lo that of the rest (22 bits and a sign), a such that the row's
 // largest magnitude lies in 2^14 .. 2^15; then xy ~ hi hi' + hi lo' + lo hi', off
 // by 3 * 2^-22 of |x||y| at most, with fp32 sums. Rows' elements below 2^-17 of the
-// largest keep 2^-39 of it (fp16's smallest step is 2^-24). Three matrix products instead of one on the fp32
-// matrix cores, whose rate is a sixteenth.
+// largest keep 2^-39 of it (fp16's smallest step is 2^-24), and with a >= -112 none is
+// held closer than 2^-137. Three matrix products instead of one on the fp32 matrix
+// cores, whose rate is a sixteenth.
 // A first kernel writes K and V in this form, once per row (the rows that read
-// them split nothing): [head][token][hi, lo][D], and 2^a per row.
+// them split nothing): [head][token][hi, lo][D], and 2^a per row (of K 2^(a - 23): the
+// sums are below 2^38, and large rows of K must not overflow where those of q are small).
 // The scale of K's rows multiplies the logits. That of V's rows goes into the
 // weights: w_j = p_j 2^a_j / ref with ref the running maximum of p_j 2^a_j, so that
 // hi and lo of w keep 22 bits of the largest products (and a row of V counts for as
@@ -457,15 +462,16 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 constexpr float kSlackF32 = 3.0f;      // as kSlack
 constexpr float kMostWeight = 8.0f;    // the same for w ...
 constexpr float kWeightOne = 2048.0f;  // ... so that w times this stays below 2^14
+constexpr int kKeyShift = 23, kMostQuery = 100;  // a row of q's a above this is made up for apart
 
-// 2^a of a row whose largest finite magnitude is big, and its reciprocal
-__device__ inline void row_scale(float big, float &scale, float &inv)
+// a of a row whose largest finite magnitude is big; 2^a and 2^-a are normal, and so are
+// the smallest weights that count relative to it
+__device__ inline int row_exponent(float big)
 {
-    int a = (int)(__float_as_uint(big) >> 23) - 127 - 14;
-    a = a < -100 ? -100 : a;
-    scale = __uint_as_float((uint32_t)(a + 127) << 23);
-    inv = __uint_as_float((uint32_t)(127 - a) << 23);
+    const int a = (int)(__float_as_uint(big) >> 23) - 127 - 14;
+    return a < -112 ? -112 : a;
 }
+__device__ inline float power_of_two(int a) { return __uint_as_float((uint32_t)(a + 127) << 23); }
 __device__ inline float finite_abs(float v) { return fabsf(v) <= 3.402823466e38f ? fabsf(v) : 0.0f; }
 __device__ inline void split_f16(float v, _Float16 &hi, _Float16 &lo)
 {
@@ -498,8 +504,8 @@ __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a
     float big = fmaxf(fmaxf(finite_abs(x.x), finite_abs(x.y)), fmaxf(finite_abs(x.z), finite_abs(x.w)));
 #pragma unroll
     for (int d = 1; d < L; d <<= 1) big = fmaxf(big, __shfl_xor(big, d));
-    float scale, inv;
-    row_scale(big, scale, inv);
+    const int exponent = row_exponent(big);
+    const float inv = power_of_two(-exponent);
     _Float16 hi[4], lo[4];
     bool bad = false;
 #pragma unroll
@@ -514,7 +520,8 @@ __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a
     char *dst = planes + (is_v * rows + at) * (D * 4) + lane * 8;
     *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(hi);
     *reinterpret_cast<uint2 *>(dst + D * 2) = *reinterpret_cast<const uint2 *>(lo);
-    if (lane == 0) scales[is_v * rows + at] = any ? -scale : scale;
+    const float scale = power_of_two(exponent);
+    if (lane == 0) scales[is_v * rows + at] = !is_v ? scale * power_of_two(-kKeyShift) : any ? -scale : scale;
 }
 
 // The loop of attention_bf16_kernel (as it is there with KS = 1) with the four 16-bit
@@ -582,7 +589,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
     request(0);
 
     int tok;
-    float c;
+    float c, large_q;  // what c is not made up of
     v8h qh[C], ql[C];
     {
         int r = r_wave + col;
@@ -599,9 +606,10 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
             for (int e = 0; e < 8; ++e) big = fmaxf(big, finite_abs(x[i][e]));
         }
         both_halves(big, lo, up);
-        float scale, inv;
-        row_scale(fmaxf(lo, up), scale, inv);
-        c = fmaxf(fabsf(a.scale) * kLog2e * scale, 1e-37f);
+        const int exponent = row_exponent(fmaxf(lo, up)), most = exponent < kMostQuery ? exponent : kMostQuery;
+        large_q = power_of_two(exponent - most);
+        c = logit_factor(a.scale * power_of_two(kKeyShift) * power_of_two(most));
+        float inv = power_of_two(-exponent);
         if (a.scale < 0.0f) inv = -inv;
 #pragma unroll
         for (int i = 0; i < C; ++i)
@@ -635,6 +643,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = v16f{};
 
+    const int cut = __any(large_q != 1.0f) ? 0 : wave_masked;
     int aside = 0;  // negative: a tile of V held values that are not finite
     for (int tile = 0; tile < tiles; ++tile) {
         ring_barrier<0>();
@@ -672,11 +681,11 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
                 gv[4 * g + i] = fabsf((&v4.x)[i]);
             }
         }
-        if (tile >= wave_masked) {
+        if (tile >= cut) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const bool seen = tile * KEYS + 32 * b0 + 8 * (i >> 2) + 4 * h + (i & 3) <= tok;
-                s[i] = seen ? s[i] : kNegInf;
+                s[i] = seen ? s[i] * large_q : kNegInf;
                 gv[i] = seen ? gv[i] : 0.0f;
             }
         }

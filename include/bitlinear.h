@@ -349,8 +349,9 @@ size_t bitlinear_attention_workspace_size(bl_dtype dtype, int64_t m, int64_t q_h
  * BL_BF16: products of the bf16 inputs summed in fp32, softmax in fp32, p
  * rounded to bf16 for its product with v. BL_F32: sums and softmax in fp32, the
  * factors of the two products held to 2^-22 of their value, but elements of q, k
- * and v no closer than 2^-39 of the largest of their row (one token and head), and
- * the weights no closer than 2^-36 of the row's largest p_ij max |v_j|.
+ * and v no closer than 2^-39 of the largest of their row (one token and head), nor
+ * than 2^-137, and the weights no closer than 2^-36 of the row's largest
+ * p_ij max |v_j|.
  * A row depends on rows 0..i of its own sequence only: infinities and NaN in
  * later rows or in other sequences do not reach it. Those that a row sees count as
  * the formula has them: a logit of -inf gives its key no weight; one of +inf or NaN
