@@ -244,6 +244,11 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
             w = make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
             qf[i] = __builtin_bit_cast(v8bf, w);
         }
+        if (a.scale == 0.0f)  // every logit 0, also where q . k overflows
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) qf[i][e] = (__bf16)((float)qf[i][e] * 0.0f);
     }
     const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
     const int tiles = last_row / group / KEYS + 1;
@@ -610,7 +615,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void attention_f32_kernel(Att
         large_q = power_of_two(exponent - most);
         c = logit_factor(a.scale * power_of_two(kKeyShift) * power_of_two(most));
         float inv = power_of_two(-exponent);
-        if (a.scale < 0.0f) inv = -inv;
+        if (!(a.scale > 0.0f)) inv = a.scale == 0.0f ? 0.0f : -inv;  // 0: every logit 0, also where q . k overflows
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
