@@ -1,7 +1,8 @@
 """Compile the gfx950 HIP sources into bit_ternary_weight_bitlinear_amd/libbitlinear.so
 (the product library) and libbitlinear_bench.so (the benchmark's plain read
 kernels, loaded by bench.py only), and the host-only module _binding.so, which
-marshals torch tensors to the library's attention calls.
+marshals torch tensors to the library's attention calls. The library needs hipcc
+alone and is linked first; where torch is not installed the module is left out.
 
 Flags: correctly rounded fp32 division, no FMA contraction, no fast-math, no
 denormal flushing (the quantizers decide integers in fp32 and must match the
@@ -38,9 +39,14 @@ FLAGS = [
 EXTRA_FLAGS = {"attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
-def build_binding(verbose: bool = False) -> str:
-    """The CPython module of the attention calls (csrc/binding.cpp, host code only)."""
-    import torch
+def build_binding(verbose: bool = False) -> str | None:
+    """The CPython module of the attention calls (csrc/binding.cpp, host code only); None without torch,
+    whose tensors it takes."""
+    try:
+        import torch
+    except ImportError as e:
+        print(f"{BINDING} is not built ({e}); the C library does not need it", file=sys.stderr)
+        return None
     base = os.path.dirname(torch.__file__)
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -76,13 +82,13 @@ def build(verbose: bool = False, out_dir: str | None = None) -> str:
     with ThreadPoolExecutor(max_workers=min(len(all_src), os.cpu_count() or 1)) as ex:
         binding = ex.submit(build_binding, verbose)
         objs = dict(zip(all_src, ex.map(compile_one, all_src)))
-    binding.result()
     for lib, srcs in ((LIB, SOURCES), (BENCH_LIB, BENCH_SOURCES)):
         cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *[objs[s] for s in srcs], "-o", lib + ".tmp"]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(lib + ".tmp", lib)
+    binding.result()  # raises what the module's compiler reported
     return LIB
 
 
