@@ -449,7 +449,7 @@ def attention_workspace_size(dtype: torch.dtype, m: int, q_heads: int, kv_heads:
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
               scale: float | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Causal attention over packed prompts. q [m][q_heads][head_dim], k and v [m][kv_heads][head_dim]
-    (fp32 or bf16, possibly slices of one projection's rows), cu_seqlens int32 [seqs + 1]
+    (fp32 or bf16, possibly slices of one projection's rows), cu_seqlens int32 [seqs + 1], not decreasing,
     -> [m][q_heads * head_dim] of q's type. Rows outside the sequences are not written."""
     return (_native or _attention_calls()).attention(q, k, v, cu_seqlens, scale, out, workspace)
 

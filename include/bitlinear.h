@@ -331,8 +331,10 @@ bl_status bitlinear_gemm_i32(const int8_t *q, int64_t m, int64_t k,
  * Packed sequences: `cu_seqlens` int32 [seqs + 1] on the device, sequence s is
  * rows cu_seqlens[s] .. cu_seqlens[s+1]-1 (empty ones are allowed). Offsets are
  * read by the kernels, so a call can be captured and replayed with others;
- * values outside 0..m are taken as the nearest of the two, and a sequence that
- * ends before it begins is empty. Rows before the first and behind the last
+ * values outside 0..m are taken as the nearest of the two. Offsets do not decrease:
+ * where they do, a sequence that ends before it begins is empty, and what a call
+ * leaves in the rows (and the cache's pages) that its sequences name is unspecified,
+ * but nothing else is read or written. Rows before the first and behind the last
  * sequence are not written and enter nothing.
  */
 #define BL_MAX_HEADS ((int64_t)1 << 12)
