@@ -6,8 +6,9 @@
 // kc, vc are int8 codes and ks, vs one scale per page of 64 tokens. Both products
 // run on v_mfma_i32_16x16x64_i8 with the codes as they lie in memory: q and p
 // become three signed base-256 digits (23 bits and a sign, relative to the
-// largest of the row of q, and to the page's largest p), so the codes need no
-// conversion, the sums are exact integers, and the result is as good as fp32.
+// largest of the row of q, and to the page's largest p: off by less than 2^-22 and
+// 2^-23 of it), so the codes need no conversion, the sums are exact integers, and
+// the result is as good as fp32.
 // The 16 rows of the first operand hold 4 query rows x (3 digits + a zero row):
 // row 4j+i is digit i of query row j. The result's row 4j+i lies in register i of
 // the lanes with lane / 16 = j, so a lane joins the digits of its own query row
@@ -28,7 +29,9 @@ constexpr float kDigitMax = 8355711.0f;  // 0x7F7F7F: every digit within -128..1
 // Signed base-256 digits: with 0x80 added to each, the bytes of n + 0x808080. For
 // |x * scale| <= kDigitMax the fp32 sum x * scale + 0x808080 is at least 2^23, where
 // fp32 holds integers only, or (for x * scale < -32896) is cut to one by the
-// conversion: one fma and one conversion per value, off by less than 1.
+// conversion: one fma and one conversion per value, off by less than 1 where x * scale
+// is below -32896 and by at most a half elsewhere. For q the factor to its largest rounds
+// by up to 0.5 and the product with it by 0.25 besides: less than 1.75 of 8355711.
 __device__ inline uint32_t biased_digits(float x, float scale)
 {
     return (uint32_t)__builtin_fmaf(x, scale, 8421504.0f);

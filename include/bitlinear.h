@@ -360,7 +360,9 @@ size_t bitlinear_attention_workspace_size(bl_dtype dtype, int64_t m, int64_t q_h
  * makes the row NaN, as -inf in all of them does. An element of v_j that is not
  * finite reaches every row that sees it, whatever its weight: as NaN where the row
  * sees a NaN or infinities of both signs in that dim, otherwise as the infinity
- * (but a row of NaN weights is NaN throughout).
+ * (but a row of NaN weights is NaN throughout). Finite values of v beside which
+ * 2^8 sum_j |v_j| passes fp32's range may give results that are not (BL_BF16), and so
+ * may logits that do.
  * BL_ERR_SHAPE also where m * q_heads / kv_heads, or its 64th part (plus seqs)
  * times kv_heads, passes 2^31 - 1024.
  *   workspace  >= bitlinear_attention_workspace_size() bytes
@@ -398,9 +400,10 @@ bl_status bitlinear_attention(const void *q, int64_t q_stride, const void *k, in
  *   new codes      rint(x * (127 / s'))
  *   earlier codes  rint(c * (s / s')) if the scale grew
  * in fp32, ties to even. Codes of later slots stay as they are. NaN counts as 0
- * and infinities as the largest finite number, so a token spoils its block's
- * precision at most. `lens` is not changed: the caller adds the new tokens once
- * every layer has appended. Two sequences may share pages that no call writes.
+ * and infinities as the largest finite number, beside which the block's other
+ * codes become 0 (and c * (scale / 127) may round to an infinity again). `lens` is
+ * not changed: the caller adds the new tokens once every layer has appended. Two
+ * sequences may share pages that no call writes.
  */
 bl_status bitlinear_cache_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                  bl_dtype dtype, int64_t m, int64_t kv_heads, int64_t head_dim,
@@ -433,10 +436,12 @@ size_t bitlinear_attention_cached_workspace_size(int64_t m, int64_t q_heads, int
  *   weights   optional fp32 [seqs][max_blocks] (input and output): the attention
  *             weight that each block received, summed over the call's rows and
  *             query heads, is added to it; blocks without one are left alone
- * The codes enter exactly; q and the softmax weights are held to 2^-23 of their
- * row's (and block's) largest, sums are exact int32 within a block and fp32
- * across blocks, for either dtype. A row of q that is not finite gives NaN and
- * adds nothing to the weights. Results do not depend on the order of execution.
+ * The codes enter exactly; q is held to 2^-22 of its row's largest (or of 1e-30,
+ * where that is larger), the softmax weights to 2^-23 of their block's largest, sums
+ * are exact int32 within a block and fp32 across blocks, for either dtype. Logits
+ * or sums that pass fp32's range give a row that is not finite. A row of q that is
+ * not finite gives NaN and adds nothing to the weights. Results do not depend on
+ * the order of execution.
  *   workspace  >= bitlinear_attention_cached_workspace_size() bytes
  */
 bl_status bitlinear_attention_cached(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m,
