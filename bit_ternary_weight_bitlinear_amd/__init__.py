@@ -490,5 +490,5 @@ def cache_evict(block_table: torch.Tensor, lens: torch.Tensor, weights: torch.Te
                 recent: int = 1):
     """Chooses the blocks every sequence keeps: its first `first`, its last `recent` and, up to `keep`
     in all, those of the largest weight -> (block_table, lens, weights) of the kept blocks, and
-    (evicted, evicted_count): the pages that are free now, -1 behind them."""
+    (evicted, evicted_count): the pages of the others (free now, unless sequences share them), -1 behind them."""
     return (_native or _attention_calls()).cache_evict(block_table, lens, weights, keep, first, recent)

@@ -722,7 +722,7 @@ bl_status bitlinear_attention_cached(const void *q, int64_t q_stride, bl_dtype d
     p.head_dim = head_dim; p.cu = cu_seqlens; p.lens = lens; p.table = block_table; p.seqs = seqs;
     p.max_blocks = max_blocks; p.k_codes = k_codes; p.v_codes = v_codes; p.k_scale = k_scale; p.v_scale = v_scale;
     p.pages = pages; p.scale = scale; p.out = out; p.weights = weights;
-    p.packed = cu_seqlens != nullptr; p.want_weights = weights != nullptr;
+    p.want_weights = weights != nullptr;
     return hip_status(launch_attention_cached(p, workspace, static_cast<hipStream_t>(stream)));
 }
 

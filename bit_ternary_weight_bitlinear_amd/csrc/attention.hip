@@ -810,15 +810,12 @@ hipError_t launch_attention(const AttentionProblem &p, void *ws, hipStream_t st)
             });
         in_launches((p.m * group / rows_each + p.seqs) * p.kv_heads, [&](int first, unsigned n) {
             if (p.bf16) hipLaunchKernelGGL((attention_bf16_kernel<D, KS>), dim3(n), dim3(256), 0, st, p, group, first);
-            else if constexpr (KS < 4) hipLaunchKernelGGL((attention_f32_kernel<D, KS>), dim3(n), dim3(256), 0, st, p, group, first,
-                                                          (const char *)planes, (const float *)scales);
+            else hipLaunchKernelGGL((attention_f32_kernel<D, KS>), dim3(n), dim3(256), 0, st, p, group, first, (const char *)planes,
+                                    (const float *)scales);
         });
     };
     auto go_width = [&](auto width) {
-        switch (key_splits(p)) {
-        case 1: return go(width, Width<1>{});
-        default: return go(width, Width<2>{});
-        }
+        key_splits(p) == 1 ? go(width, Width<1>{}) : go(width, Width<2>{});
     };
     if (p.head_dim == 128) go_width(Width<128>{});
     else go_width(Width<64>{});

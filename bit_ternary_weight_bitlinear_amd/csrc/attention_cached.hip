@@ -541,7 +541,7 @@ static int64_t units_of(const CachedProblem &p, int rt) { return p.seqs * ceil_d
 static int64_t query_tiles(const CachedProblem &p, int rt)
 {
     const int64_t group = p.q_heads / p.kv_heads, r = 4 * rt;
-    return p.packed ? p.m * group / r + p.seqs : p.seqs * ceil_div(group, r);
+    return p.cu ? p.m * group / r + p.seqs : p.seqs * ceil_div(group, r);
 }
 
 // Row tiles per workgroup: 4 * rt query rows share a page's loads, but a wave works on

@@ -43,7 +43,7 @@ __device__ inline bool find_block(const int32_t *cu, const int32_t *lens, int se
     return true;
 }
 
-// 16 codes of which [0, used) are rescaled, [used, end) replaced, the rest kept
+// an earlier token's code under a scale that has grown by 1 / ratio
 __device__ inline int rescale_code(int c, float ratio) { return (int)rintf((float)c * ratio); }
 
 // One workgroup per (touched block, kv head), K and V together: the new rows are
@@ -189,7 +189,8 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const T *__restrict__
         for (int d = 0; d < 4; ++d)
             *reinterpret_cast<uint4 *>(vp + v_code_at(first, 4 * piece + d)) = make_uint4(o[d][0], o[d][1], o[d][2], o[d][3]);
     }
-    // the others, at most one before and one behind unless the scale grew: a dim per thread
+    // the others, at most one before and one behind unless the scale grew: a dim per thread,
+    // of whose 16 codes those of [0, used) are rescaled, of [used, end) replaced, the rest kept
     const int g0 = grow_v ? 0 : used / 16, ng = (end + 15) / 16 - g0;
     for (int it = tid; it < ng * D; it += 256) {
         const int g = g0 + it / D, dim = it % D, first = 16 * g;

@@ -195,7 +195,6 @@ struct CachedProblem {
     float scale;
     void *out;
     float *weights;     // optional [seqs][max_blocks], added to
-    bool packed;        // cu given
     bool want_weights;  // the layout of the workspace depends on it and the sizes
 };
 int64_t attention_cached_workspace(const CachedProblem &p);

@@ -463,6 +463,9 @@ bl_status bitlinear_attention_cached(const void *q, int64_t q_stride, bl_dtype d
  *   lens_out     int32 [seqs]: lens minus 64 per evicted block (unused slots as is)
  *   evicted      int32 [seqs][max_blocks]: pages of the evicted blocks, then -1
  *   evicted_count  int32 [seqs]
+ * The outputs lie apart from the inputs. Table entries are passed on as they are: one
+ * that names no page may be among the evicted, and a page that other sequences share
+ * is theirs still.
  */
 bl_status bitlinear_cache_evict(const int32_t *block_table, const int32_t *lens, const float *weights,
                                 int64_t seqs, int64_t max_blocks, int64_t keep, int64_t first, int64_t recent,
