@@ -547,9 +547,9 @@ __global__ __launch_bounds__(256) void attention_split_kernel(AttentionProblem a
 
 // The loop of attention_bf16_kernel (as it is there with KS = 1) with the four 16-bit
 // planes of a tile of 32 * KS keys, 32 keys per wave. Bound by the matrix cores: 8192
-// tokens, 32/8 heads of 128: 1.54 ms, 357 TFLOP/s of fp32 (three times that in
+// tokens, 32/8 heads of 128: 1.49 ms, 369 TFLOP/s of fp32 (three times that in
 // fp16 products; the fp32 matrix cores reach 153 in a plain product). With KS = 2, 2500
-// tokens of 6/2 heads: 82.5 us; 97.5 with matrix results in accumulation registers
+// tokens of 6/2 heads: 82.7 us; 97.5 with matrix results in accumulation registers
 // (build.py), 84.2 with V's operands read as they are used, 88.2 with the next tile's
 // logits formed beside the softmax (too many registers). Two accumulators for the
 // logits' main and cross terms instead of one measured the same.

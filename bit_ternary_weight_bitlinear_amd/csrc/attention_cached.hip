@@ -17,9 +17,11 @@
 // A page is one step of a wave: 8 KB of K, 8 KB of V (head_dim 128), each lane
 // 16 bytes per load, every load of a wave contiguous. ~200 VALU operations and 16
 // matrix instructions per 16 KB and four query rows (0.5 us of a SIMD): bound by HBM
-// with four rows a page (64 tokens over 7900, 32/8 heads: 168 us, 6.1 TB/s), by the
-// VALU from eight on. Not kept: the next page's V too ahead of its use (registers
-// spill).
+// with four rows a page (64 tokens over 7900, 32/8 heads: 168 us, 5.8 TB/s), by the
+// latency of a wave's pages with eight (16 x 4 tokens over 2500, 32/8 heads: 18.5 us,
+// the VALU busy 34 % of the cycles; 12 x 4 over 1 to 4000: 13 %), by the VALU with
+// sixteen (32 x 8 tokens over 2500: 47 us, VALU 59 %, matrix cores 18 %). Not kept: the
+// next page's V too ahead of its use (registers spill).
 #include "attention.hpp"
 
 namespace bl {
@@ -547,12 +549,12 @@ static int64_t query_tiles(const CachedProblem &p, int rt)
 // Row tiles per workgroup: 4 * rt query rows share a page's loads, but a wave works on
 // them one after the other (0.5 us per page and tile of rows, 16 rows 2.3). Where four
 // rows give no more workgroups than CUs and there is little to read, that spreads the
-// work (4 tokens of 20/5 heads over 1000: 6.9 us with 4 rows, 8.6 with 8, 12.5 with
+// work (4 tokens of 20/5 heads over 1000: 6.8 us with 4 rows, 8.8 with 8, 12.3 with
 // 16); where there is much, the pages are read less often (32 x 8 tokens of 32/8 heads
-// over 2500: 195, 104, 62 us). In between it is 8 rows (16 x 4 tokens of 32/8 heads over
-// 2500: 53.5, 30.6, 40.7 us). Pages counted for every tile, as of 128-wide heads; 482
-// shapes take 1.04 times their best on average by this rule (16 rows wherever a sequence
-// has more than 8: 1.42).
+// over 2500: 74, 56, 47 us). In between it is 8 rows (16 x 4 tokens of 32/8 heads over
+// 2500: 20.0, 18.5, 28.1 us). Pages counted for every tile, as of 128-wide heads. When
+// the rule was fitted 482 shapes took 1.04 times their best on average by it (16 rows
+// wherever a sequence has more than 8: 1.42).
 static int row_tiles(const CachedProblem &p)
 {
     const int64_t rows = rows_each(p), pages = p.max_blocks * p.head_dim / 64;  // twice them
