@@ -105,13 +105,22 @@ __device__ inline bool set_aside(char *tile, int *flags)
     return true;
 }
 
+// four adjacent elements
+template <typename T>
+struct Adjacent {
+    typedef v4f type;
+};
+template <>
+struct Adjacent<bf16_t> {
+    typedef uint2 type;
+};
+
 // bit e (+inf or NaN) and 4 + e (-inf or NaN) of what four adjacent elements are
 template <typename T>
-__device__ inline int odd_kinds(const T *p)
+__device__ inline int odd_kinds(typename Adjacent<T>::type four)
 {
     T w[4];
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(p);
-    else *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(p);
+    __builtin_memcpy(w, &four, sizeof(w));
     int kinds = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -135,23 +144,29 @@ __device__ inline void settle(T *dst, const T *v, int64_t stride, int keys, int 
     const int col = threadIdx.x & 31, common = __builtin_amdgcn_readfirstlane(keys);  // rows ascend
     for (int i = first; i < first + n; ++i) {
         const int at = 32 * (i >> 2) + 8 * (i & 3);
-        bool odd = wanted && aside;
-        if (wanted && !aside)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) odd = odd || !(fabsf(to_f32(dst[at + e])) <= 3.402823466e38f);
+        // read and written as the type that it was stored as
+        using Four = typename Adjacent<T>::type;
+        Four *four = reinterpret_cast<Four *>(dst + at), was = {};
+        if (wanted) was = *four;
+        const bool odd = wanted && (aside || odd_kinds<T>(was));
         if (!__any(odd)) continue;
+        auto at_key = [&](int j) { return *reinterpret_cast<const Four *>(v + j * stride + at); };
         int kinds = 0;
 #pragma unroll 4
-        for (int j = col; j < common && kinds != 0xFF; j += 32) kinds |= odd_kinds(v + j * stride + at);
+        for (int j = col; j < common && kinds != 0xFF; j += 32) kinds |= odd_kinds<T>(at_key(j));
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) kinds |= __shfl_xor(kinds, d);
-        for (int j = common; j < keys; ++j) kinds |= odd_kinds(v + j * stride + at);
+        for (int j = common; j < keys; ++j) kinds |= odd_kinds<T>(at_key(j));
         if (!odd) continue;
+        T now[4];
+        __builtin_memcpy(now, &was, sizeof(now));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const bool plus = kinds >> e & 1, minus = kinds >> (4 + e) & 1;
-            if (plus || minus) store_out(dst + at + e, plus && minus ? __builtin_nanf("") : plus ? -kNegInf : kNegInf);
+            if (plus || minus) store_out(&now[e], plus && minus ? __builtin_nanf("") : plus ? -kNegInf : kNegInf);
         }
+        __builtin_memcpy(&was, now, sizeof(now));
+        *four = was;
     }
 }
 
