@@ -274,11 +274,6 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
             w = make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
             qf[i] = __builtin_bit_cast(v8bf, w);
         }
-        if (a.scale == 0.0f)  // every logit 0, also where q . k overflows
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) qf[i][e] = (__bf16)((float)qf[i][e] * 0.0f);
     }
     const int last_row = t.tile * ROWS + ROWS < rows ? t.tile * ROWS + ROWS - 1 : rows - 1;
     const int tiles = last_row / group / KEYS + 1;
@@ -354,6 +349,12 @@ __global__ __launch_bounds__(256, 2) void attention_bf16_kernel(AttentionProblem
     auto k_read = [&](int n) { return kf[n]; };
 
     request_k(0);
+    // every logit 0, also where q . k overflows (behind the request: q's rows are waited for here)
+    if (a.scale == 0.0f)
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) qf[i][e] = (__bf16)((float)qf[i][e] * 0.0f);
     if constexpr (AHEAD) {
         ring_barrier<0>();
         request_v(0);
