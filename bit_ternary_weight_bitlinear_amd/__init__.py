@@ -26,12 +26,19 @@ Functions mirror the C entry points:
   cache_read(cache, block_table, begin, cu_seqlens, m) -> (k, v) [m][kv_heads][head_dim]
   attention_cached(q, cache, block_table, lens, cu_seqlens=None, weights=None) -> out of new tokens over the cache
   cache_evict(block_table, lens, weights, keep) -> (block_table, lens, weights, evicted, evicted_count)
+  rotary_frequencies(rotary_dim, base)  -> fp32 [rotary_dim / 2] angles per position, scaled for long contexts if asked
+  rotate(q, k, inv_freq, begin, cu_seqlens=None) -> (q, k) rotated by their tokens' positions, each head normed before if asked
+  attention_shared(q, cache, prefix_table, prefix_len, block_table, lens) -> attention_cached behind a prefix all sequences share
+  bounds_alloc(cache), cache_bounds(cache, bounds, block_table, lens, cu_seqlens, m)   the extremes of every block's keys
+  block_select(q, bounds, k_scale, block_table, lens, keep) -> selected int32 [m][kv_heads][keep] by an upper bound of the scores
+  attention_selected(q, cache, block_table, lens, selected) -> attention_cached over the selected blocks
 Activations may be float32 or bfloat16 CUDA (HIP) tensors, contiguous, [m][k]; q, k and v are
 [m][heads][head_dim] and may be slices of a fused projection's rows (any stride between tokens).
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import NamedTuple
 
@@ -42,7 +49,9 @@ __all__ = ["pack_weights", "pack_weights_threshold", "quant_act", "quant_act_nor
            "OP_GEMM_I32", "OP_PACK_THRESHOLD", "OP_FORWARD_NORM", "OP_FFN_SPARSE", "OP_FORWARD_A4",
            "pack_kmajor", "ffn_sparse", "quant_act_a4", "forward_a4",
            "attention", "attention_cached", "KVCache", "cache_alloc", "cache_append", "cache_read", "cache_evict",
-           "attention_workspace_size", "attention_cached_workspace_size", "CACHE_BLOCK"]
+           "attention_workspace_size", "attention_cached_workspace_size", "CACHE_BLOCK",
+           "rotary_frequencies", "rotate", "attention_shared", "attention_shared_workspace_size", "bounds_alloc", "cache_bounds",
+           "block_select", "block_select_workspace_size", "attention_selected", "attention_selected_workspace_size"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbitlinear.so")
@@ -90,6 +99,20 @@ _SIGNATURES = {
                                             _c_p, _c_size, _c_p]),
     "bitlinear_cache_evict": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p,
                                        _c_p, _c_p, _c_p]),
+    "bitlinear_rotate": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p,
+                                  _c_i64, _c_int, ctypes.c_float, _c_p, _c_p, ctypes.c_float, _c_p, _c_i64, _c_p, _c_i64, _c_p]),
+    "bitlinear_attention_shared_workspace_size": (_c_size, [_c_i64] * 7),
+    "bitlinear_attention_shared": (_c_int, [_c_p, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p,
+                                            _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, ctypes.c_float, _c_p, _c_p,
+                                            _c_size, _c_p]),
+    "bitlinear_cache_bounds": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p]),
+    "bitlinear_block_select_workspace_size": (_c_size, [_c_i64] * 3),
+    "bitlinear_block_select": (_c_int, [_c_p, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p, _c_i64,
+                                        _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_size, _c_p]),
+    "bitlinear_attention_selected_workspace_size": (_c_size, [_c_i64] * 5),
+    "bitlinear_attention_selected": (_c_int, [_c_p, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p, _c_i64,
+                                              _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, ctypes.c_float, _c_p, _c_p, _c_size,
+                                              _c_p]),
 }
 
 _lib = None
@@ -492,3 +515,97 @@ def cache_evict(block_table: torch.Tensor, lens: torch.Tensor, weights: torch.Te
     in all, those of the largest weight -> (block_table, lens, weights) of the kept blocks, and
     (evicted, evicted_count): the pages of the others (free now, unless sequences share them), -1 behind them."""
     return (_native or _attention_calls()).cache_evict(block_table, lens, weights, keep, first, recent)
+
+
+# ---------------------------------------------------------------- positions, a shared prefix, chosen blocks
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                       length: int | None = None, low: float = 1.0, high: float = 32.0, device="cuda") -> torch.Tensor:
+    """Angles per position of a head's rotated pairs, base^(-2 i / rotary_dim), fp32 [rotary_dim / 2] (computed in 64
+    bits). For a context `factor` times the one a model was trained on (`length` tokens), scaling is
+      "positions"  every angle divided by factor;
+      "base"       the base raised to base * factor^(n / (n - 2)), n = rotary_dim: the slowest pair's angle divided by
+                   factor, the fastest one's kept;
+      "parts"      pairs that turn more than `high` times within `length` kept, those that turn less than `low` times
+                   divided by factor, between the two linear in the number of turns. The attention's logits often
+                   grow with it: rotate()'s magnitude, say 0.1 * log(factor) + 1."""
+    if not (16 <= rotary_dim and rotary_dim % 16 == 0):
+        raise BitLinearError(f"rotary_dim must be a multiple of 16, got {rotary_dim}")
+    if not (math.isfinite(base) and base > 0 and math.isfinite(factor) and factor > 0):
+        raise BitLinearError("base and factor must be finite and positive")
+    if scaling not in (None, "positions", "base", "parts"):
+        raise BitLinearError(f'scaling must be None, "positions", "base" or "parts", got {scaling!r}')
+    if scaling == "base":
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    freq = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    if scaling == "positions":
+        freq = freq / factor
+    if scaling == "parts":
+        if length is None or length < 1 or not 0 <= low < high:
+            raise BitLinearError('scaling "parts" needs length >= 1 and 0 <= low < high')
+        kept = ((length * freq / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        freq = freq * (kept + (1 - kept) / factor)
+    return freq.to(torch.float32).to(device)
+
+
+def rotate(q: torch.Tensor, k: torch.Tensor, inv_freq: torch.Tensor, begin: torch.Tensor, cu_seqlens: torch.Tensor | None = None, *,
+           interleaved: bool = False, q_gain: torch.Tensor | None = None, k_gain: torch.Tensor | None = None, eps: float = 1e-5,
+           magnitude: float = 1.0, out: tuple[torch.Tensor, torch.Tensor] | None = None):
+    """Rotates queries and keys by their tokens' positions, row i of sequence s standing at begin[s] + i (int32 [seqs];
+    negative: an unused slot; without cu_seqlens one row per sequence), on the first 2 * len(inv_freq) elements of every
+    head: pairs (i, i + len(inv_freq)), or (2i, 2i + 1) if interleaved. With a gain (fp32 [head_dim]) the head's RMS norm
+    comes before. -> (q, k) dense, or `out`, which may be (q, k) themselves."""
+    return (_native or _attention_calls()).rotate(q, k, inv_freq, begin, cu_seqlens, interleaved, q_gain, k_gain, eps, magnitude, out)
+
+
+def attention_shared_workspace_size(m: int, q_heads: int, kv_heads: int, head_dim: int, seqs: int, max_blocks: int, prefix_blocks: int) -> int:
+    return int(load_library().bitlinear_attention_shared_workspace_size(m, q_heads, kv_heads, head_dim, seqs, max_blocks, prefix_blocks))
+
+
+def attention_shared(q: torch.Tensor, cache: KVCache, prefix_table: torch.Tensor, prefix_len: torch.Tensor, block_table: torch.Tensor,
+                     lens: torch.Tensor, cu_seqlens: torch.Tensor | None = None, *, scale: float | None = None,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """attention_cached of a batch whose sequences share a prefix: every row sees the prefix's tokens (pages
+    prefix_table int32 [prefix_blocks], prefix_len int32 [1] of them) and its own sequence's up to itself. lens and
+    block_table count and hold the sequences' own tokens only."""
+    return (_native or _attention_calls()).attention_shared(q, cache, prefix_table, prefix_len, block_table, lens, cu_seqlens, scale,
+                                                            out, workspace)
+
+
+def bounds_alloc(cache: KVCache) -> torch.Tensor:
+    """Bounds for every page of a cache: int8 [pages][kv_heads][2][head_dim]."""
+    pages, heads, codes = cache.k.shape
+    return torch.zeros((pages, heads, 2, codes // CACHE_BLOCK), dtype=torch.int8, device=cache.k.device)
+
+
+def cache_bounds(cache: KVCache, bounds: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, cu_seqlens: torch.Tensor | None,
+                 m: int) -> None:
+    """The largest and the smallest K code of every dim, for the blocks that the m rows of a cache_append with the same
+    tables reached (called after it, lens still as they were)."""
+    (_native or _attention_calls()).cache_bounds(cache, bounds, block_table, lens, cu_seqlens, m)
+
+
+def block_select_workspace_size(m: int, kv_heads: int, max_blocks: int) -> int:
+    return int(load_library().bitlinear_block_select_workspace_size(m, kv_heads, max_blocks))
+
+
+def block_select(q: torch.Tensor, bounds: torch.Tensor, k_scale: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, keep: int,
+                 cu_seqlens: torch.Tensor | None = None, *, first: int = 0, recent: int = 1, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None):
+    """Chooses the blocks of its sequence that every row and kv head attends to: the first `first`, the last `recent` (its
+    own among them) and, up to `keep` in all, those whose keys may have the largest product with its queries by their
+    bounds (k_scale: the cache's) -> int32 [m][kv_heads][keep], ascending, -1 behind them."""
+    return (_native or _attention_calls()).block_select(q, bounds, k_scale, block_table, lens, keep, cu_seqlens, first, recent, out,
+                                                        workspace)
+
+
+def attention_selected_workspace_size(m: int, q_heads: int, kv_heads: int, head_dim: int, keep: int) -> int:
+    return int(load_library().bitlinear_attention_selected_workspace_size(m, q_heads, kv_heads, head_dim, keep))
+
+
+def attention_selected(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lens: torch.Tensor, selected: torch.Tensor,
+                       cu_seqlens: torch.Tensor | None = None, *, scale: float | None = None, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None):
+    """attention_cached over the blocks that selected int32 [m][kv_heads][keep] lists for each row and kv head (entries
+    that name no block are passed over, a block counts as often as it is listed)."""
+    return (_native or _attention_calls()).attention_selected(q, cache, block_table, lens, selected, cu_seqlens, scale, out, workspace)

@@ -21,7 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbitlinear.so")
 BENCH_LIB = os.path.join(HERE, "libbitlinear_bench.so")
 SOURCES = ["api.hip", "pack.hip", "act_quant.hip", "gemv.hip", "bgemv.hip", "gemm.hip", "skinny.hip",
-           "sparse_down.hip", "bmma.hip", "attention.hip", "attention_cached.hip", "cache.hip"]
+           "sparse_down.hip", "bmma.hip", "attention.hip", "attention_cached.hip", "cache.hip",
+           "attention_selected.hip", "attention_shared.hip", "rotate.hip", "blocks.hip"]
 BENCH_SOURCES = ["bench_read.hip"]
 BINDING = os.path.join(HERE, "_binding.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

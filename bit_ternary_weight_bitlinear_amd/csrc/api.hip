@@ -206,6 +206,8 @@ bool prompt_ok(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t seqs)
     const int64_t rows = m * (q_heads / kv_heads);
     return rows <= INT32_MAX - 1024 && (rows / 64 + seqs) * kv_heads <= INT32_MAX;
 }
+// rows of all query heads of a kv head, counted in 32 bits on the device
+bool grouped_rows_ok(int64_t m, int64_t q_heads, int64_t kv_heads) { return m * (q_heads / kv_heads) <= INT32_MAX - 1024; }
 bool seqs_ok(int64_t seqs) { return seqs >= 1 && seqs <= BL_MAX_TOKENS; }
 bool cache_ok(int64_t max_blocks, int64_t pages)
 {
@@ -228,6 +230,19 @@ bool tables_aligned(const int32_t *cu, const int32_t *lens, const int32_t *table
 bool cache_aligned(const int8_t *k, const int8_t *v, const float *ks, const float *vs)
 {
     return aligned16(k) && aligned16(v) && aligned(ks, 4) && aligned(vs, 4);
+}
+
+CachedProblem cached_problem(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m, int64_t q_heads, int64_t kv_heads,
+                             int64_t head_dim, const int32_t *cu, const int32_t *lens, int64_t seqs, const int32_t *table,
+                             int64_t max_blocks, const int8_t *k_codes, const int8_t *v_codes, const float *k_scale,
+                             const float *v_scale, int64_t pages, float scale, void *out)
+{
+    CachedProblem p{};
+    p.q = q; p.q_stride = q_stride; p.bf16 = dtype == BL_BF16; p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads;
+    p.head_dim = head_dim; p.cu = cu; p.lens = lens; p.table = table; p.seqs = seqs; p.max_blocks = max_blocks;
+    p.k_codes = k_codes; p.v_codes = v_codes; p.k_scale = k_scale; p.v_scale = v_scale; p.pages = pages; p.scale = scale;
+    p.out = out;
+    return p;
 }
 
 int64_t cached_workspace(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
@@ -717,11 +732,9 @@ bl_status bitlinear_attention_cached(const void *q, int64_t q_stride, bl_dtype d
         return BL_ERR_ALIGN;
     const int64_t need = cached_workspace(m, q_heads, kv_heads, head_dim, seqs, max_blocks, weights != nullptr);
     if (const bl_status w = check_ws(workspace, workspace_bytes, need)) return w;
-    CachedProblem p{};
-    p.q = q; p.q_stride = q_stride; p.bf16 = dtype == BL_BF16; p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads;
-    p.head_dim = head_dim; p.cu = cu_seqlens; p.lens = lens; p.table = block_table; p.seqs = seqs;
-    p.max_blocks = max_blocks; p.k_codes = k_codes; p.v_codes = v_codes; p.k_scale = k_scale; p.v_scale = v_scale;
-    p.pages = pages; p.scale = scale; p.out = out; p.weights = weights;
+    CachedProblem p = cached_problem(q, q_stride, dtype, m, q_heads, kv_heads, head_dim, cu_seqlens, lens, seqs, block_table,
+                                     max_blocks, k_codes, v_codes, k_scale, v_scale, pages, scale, out);
+    p.weights = weights;
     p.want_weights = weights != nullptr;
     return hip_status(launch_attention_cached(p, workspace, static_cast<hipStream_t>(stream)));
 }
@@ -742,6 +755,152 @@ bl_status bitlinear_cache_evict(const int32_t *block_table, const int32_t *lens,
     return hip_status(launch_cache_evict(block_table, lens, weights, seqs, max_blocks, keep, first, recent, table_out,
                                          lens_out, weights_out, evicted, evicted_count,
                                          static_cast<hipStream_t>(stream)));
+}
+
+// ---- rotation, a shared prefix, chosen blocks
+bl_status bitlinear_rotate(const void *q, int64_t q_stride, const void *k, int64_t k_stride, bl_dtype dtype, int64_t m,
+                           int64_t q_heads, int64_t kv_heads, int64_t head_dim, const int32_t *cu_seqlens,
+                           const int32_t *begin, int64_t seqs, const float *inv_freq, int64_t rotary_dim, int interleaved,
+                           float magnitude, const float *q_gain, const float *k_gain, float eps, void *q_out,
+                           int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream)
+{
+    if (!q || !k || !begin || !inv_freq || !q_out || !k_out) return BL_ERR_NULL;
+    if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !seqs_ok(seqs) || (!cu_seqlens && m != seqs) || rotary_dim < 16 ||
+        rotary_dim > head_dim || rotary_dim % 16 != 0)
+        return BL_ERR_SHAPE;
+    if ((interleaved != 0 && interleaved != 1) || !finite(magnitude) || !finite(eps) || eps < 0.0f) return BL_ERR_VALUE;
+    if (const bl_status s = rows_ok(q, q_stride, q_heads * head_dim, dtype)) return s;
+    if (const bl_status s = rows_ok(k, k_stride, kv_heads * head_dim, dtype)) return s;
+    if (const bl_status s = rows_ok(q_out, q_out_stride, q_heads * head_dim, dtype)) return s;
+    if (const bl_status s = rows_ok(k_out, k_out_stride, kv_heads * head_dim, dtype)) return s;
+    if (!tables_aligned(cu_seqlens, begin, begin) || !aligned(inv_freq, 4) || (q_gain && !aligned16(q_gain)) ||
+        (k_gain && !aligned16(k_gain)))
+        return BL_ERR_ALIGN;
+    RotateProblem p{};
+    p.q = q; p.k = k; p.q_stride = q_stride; p.k_stride = k_stride; p.bf16 = dtype == BL_BF16; p.m = m; p.q_heads = q_heads;
+    p.kv_heads = kv_heads; p.head_dim = head_dim; p.cu = cu_seqlens; p.begin = begin; p.seqs = seqs; p.inv_freq = inv_freq;
+    p.rotary_dim = rotary_dim; p.interleaved = interleaved != 0; p.magnitude = magnitude; p.q_gain = q_gain; p.k_gain = k_gain;
+    p.eps = eps; p.q_out = q_out; p.k_out = k_out; p.q_out_stride = q_out_stride; p.k_out_stride = k_out_stride;
+    return hip_status(launch_rotate(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t bitlinear_attention_shared_workspace_size(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                                 int64_t seqs, int64_t max_blocks, int64_t prefix_blocks)
+{
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !grouped_rows_ok(m, q_heads, kv_heads) || !seqs_ok(seqs) ||
+        !cache_ok(max_blocks, 1) || !cache_ok(prefix_blocks, 1))
+        return 0;
+    SharedProblem p{};
+    p.c.m = m; p.c.q_heads = q_heads; p.c.kv_heads = kv_heads; p.c.head_dim = head_dim; p.c.seqs = seqs;
+    p.c.max_blocks = max_blocks; p.prefix_blocks = prefix_blocks;
+    return (size_t)attention_shared_workspace(p);
+}
+
+bl_status bitlinear_attention_shared(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m, int64_t q_heads,
+                                     int64_t kv_heads, int64_t head_dim, const int32_t *prefix_table, int64_t prefix_blocks,
+                                     const int32_t *prefix_len, const int32_t *cu_seqlens, const int32_t *lens,
+                                     int64_t seqs, const int32_t *block_table, int64_t max_blocks, const int8_t *k_codes,
+                                     const int8_t *v_codes, const float *k_scale, const float *v_scale, int64_t pages,
+                                     float scale, void *out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!q || !prefix_table || !prefix_len || !lens || !block_table || !k_codes || !v_codes || !k_scale || !v_scale || !out)
+        return BL_ERR_NULL;
+    if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !grouped_rows_ok(m, q_heads, kv_heads) || !seqs_ok(seqs) ||
+        !cache_ok(max_blocks, pages) || !cache_ok(prefix_blocks, pages) || (!cu_seqlens && m != seqs))
+        return BL_ERR_SHAPE;
+    if (!finite(scale)) return BL_ERR_VALUE;
+    if (const bl_status s = rows_ok(q, q_stride, q_heads * head_dim, dtype)) return s;
+    if (!tables_aligned(cu_seqlens, lens, block_table) || !tables_aligned(nullptr, prefix_len, prefix_table) ||
+        !cache_aligned(k_codes, v_codes, k_scale, v_scale) || !aligned16(out))
+        return BL_ERR_ALIGN;
+    SharedProblem p{};
+    p.c = cached_problem(q, q_stride, dtype, m, q_heads, kv_heads, head_dim, cu_seqlens, lens, seqs, block_table, max_blocks,
+                         k_codes, v_codes, k_scale, v_scale, pages, scale, out);
+    p.prefix_table = prefix_table; p.prefix_len = prefix_len; p.prefix_blocks = prefix_blocks;
+    if (const bl_status w = check_ws(workspace, workspace_bytes, attention_shared_workspace(p))) return w;
+    return hip_status(launch_attention_shared(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+bl_status bitlinear_cache_bounds(const int8_t *k_codes, int64_t pages, int64_t kv_heads, int64_t head_dim, int64_t m,
+                                 const int32_t *cu_seqlens, const int32_t *lens, int64_t seqs, const int32_t *block_table,
+                                 int64_t max_blocks, int8_t *bounds, void *stream)
+{
+    if (!k_codes || !lens || !block_table || !bounds) return BL_ERR_NULL;
+    if (!heads_ok(m, kv_heads, kv_heads, head_dim) || !seqs_ok(seqs) || !cache_ok(max_blocks, pages) ||
+        (!cu_seqlens && m != seqs))
+        return BL_ERR_SHAPE;
+    if (!tables_aligned(cu_seqlens, lens, block_table) || !aligned16(k_codes) || !aligned16(bounds)) return BL_ERR_ALIGN;
+    CacheBounds p{};
+    p.k_codes = k_codes; p.bounds = bounds; p.pages = pages; p.kv_heads = kv_heads; p.head_dim = head_dim; p.m = m;
+    p.cu = cu_seqlens; p.lens = lens; p.table = block_table; p.seqs = seqs; p.max_blocks = max_blocks;
+    return hip_status(launch_cache_bounds(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t bitlinear_block_select_workspace_size(int64_t m, int64_t kv_heads, int64_t max_blocks)
+{
+    if (!heads_ok(m, kv_heads, kv_heads, 64) || !cache_ok(max_blocks, 1)) return 0;
+    return (size_t)block_select_workspace(m, kv_heads, max_blocks);
+}
+
+bl_status bitlinear_block_select(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m, int64_t q_heads,
+                                 int64_t kv_heads, int64_t head_dim, const int32_t *cu_seqlens, const int32_t *lens,
+                                 int64_t seqs, const int32_t *block_table, int64_t max_blocks, const int8_t *bounds,
+                                 const float *k_scale, int64_t pages, int64_t keep, int64_t first, int64_t recent,
+                                 int32_t *selected, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!q || !lens || !block_table || !bounds || !k_scale || !selected) return BL_ERR_NULL;
+    if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || q_heads / kv_heads > 128 || !seqs_ok(seqs) || !cache_ok(max_blocks, pages) ||
+        (!cu_seqlens && m != seqs))
+        return BL_ERR_SHAPE;
+    if (first < 0 || recent < 1 || first > BL_MAX_DIM || recent > BL_MAX_DIM || keep < first + recent || keep > BL_MAX_DIM)
+        return BL_ERR_VALUE;
+    if (const bl_status s = rows_ok(q, q_stride, q_heads * head_dim, dtype)) return s;
+    if (!tables_aligned(cu_seqlens, lens, block_table) || !aligned16(bounds) || !aligned(k_scale, 4) || !aligned(selected, 4))
+        return BL_ERR_ALIGN;
+    if (const bl_status w = check_ws(workspace, workspace_bytes, block_select_workspace(m, kv_heads, max_blocks))) return w;
+    SelectProblem p{};
+    p.q = q; p.q_stride = q_stride; p.bf16 = dtype == BL_BF16; p.m = m; p.q_heads = q_heads; p.kv_heads = kv_heads;
+    p.head_dim = head_dim; p.cu = cu_seqlens; p.lens = lens; p.table = block_table; p.seqs = seqs; p.max_blocks = max_blocks;
+    p.pages = pages; p.bounds = bounds; p.k_scale = k_scale; p.keep = keep; p.first = first; p.recent = recent;
+    p.selected = selected;
+    return hip_status(launch_block_select(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t bitlinear_attention_selected_workspace_size(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                                   int64_t keep)
+{
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !grouped_rows_ok(m, q_heads, kv_heads) || !cache_ok(keep, 1)) return 0;
+    SelectedProblem p{};
+    p.c.m = m; p.c.q_heads = q_heads; p.c.kv_heads = kv_heads; p.c.head_dim = head_dim; p.keep = keep;
+    return (size_t)attention_selected_workspace(p);
+}
+
+bl_status bitlinear_attention_selected(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m, int64_t q_heads,
+                                       int64_t kv_heads, int64_t head_dim, const int32_t *cu_seqlens, const int32_t *lens,
+                                       int64_t seqs, const int32_t *block_table, int64_t max_blocks,
+                                       const int32_t *selected, int64_t keep, const int8_t *k_codes,
+                                       const int8_t *v_codes, const float *k_scale, const float *v_scale, int64_t pages,
+                                       float scale, void *out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!q || !lens || !block_table || !selected || !k_codes || !v_codes || !k_scale || !v_scale || !out) return BL_ERR_NULL;
+    if (dtype != BL_F32 && dtype != BL_BF16) return BL_ERR_DTYPE;
+    if (!heads_ok(m, q_heads, kv_heads, head_dim) || !grouped_rows_ok(m, q_heads, kv_heads) || !seqs_ok(seqs) ||
+        !cache_ok(max_blocks, pages) || !cache_ok(keep, 1) || (!cu_seqlens && m != seqs))
+        return BL_ERR_SHAPE;
+    if (!finite(scale)) return BL_ERR_VALUE;
+    if (const bl_status s = rows_ok(q, q_stride, q_heads * head_dim, dtype)) return s;
+    if (!tables_aligned(cu_seqlens, lens, block_table) || !aligned(selected, 4) ||
+        !cache_aligned(k_codes, v_codes, k_scale, v_scale) || !aligned16(out))
+        return BL_ERR_ALIGN;
+    SelectedProblem p{};
+    p.c = cached_problem(q, q_stride, dtype, m, q_heads, kv_heads, head_dim, cu_seqlens, lens, seqs, block_table, max_blocks,
+                         k_codes, v_codes, k_scale, v_scale, pages, scale, out);
+    p.selected = selected; p.keep = keep;
+    if (const bl_status w = check_ws(workspace, workspace_bytes, attention_selected_workspace(p))) return w;
+    return hip_status(launch_attention_selected(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -78,6 +78,32 @@ __device__ inline bool find_tile(const int32_t *cu, int seqs, int64_t m, int idx
     return false;
 }
 
+// The sequence that a row of a packed batch lies in, and its place there: the last one that
+// begins at or before it, of 64 probes a round. False: it is in none. Wave-uniform.
+__device__ inline bool find_row(const int32_t *cu, int seqs, int64_t m, int64_t row, int &seq, int &place)
+{
+    if (!cu) {
+        seq = (int)row;
+        place = 0;
+        return row < seqs;
+    }
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = seqs;
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const bool before = lane * step < n && cu[lo + lane * step] <= row;
+        const int last = 63 - __builtin_clzll(__ballot(before) | 1);
+        lo += last * step;
+        n = n - last * step < step ? n - last * step : step;
+    }
+    int64_t begin;
+    int rows;
+    seq_rows(cu, lo, m, begin, rows);
+    seq = lo;
+    place = (int)(row - begin);
+    return row >= begin && row < begin + rows;
+}
+
 __device__ inline void store_out(float *p, float v) { *p = v; }
 __device__ inline void store_out(bf16_t *p, float v)
 {
@@ -107,6 +133,46 @@ __device__ inline float row16_sum(float v)
 }
 
 constexpr int kBlock = 64;  // tokens per cache page
+
+// Blocks of sequence s that rows lens .. lens+n-1 reach; first: the first one.
+__device__ inline int blocks_reached(const int32_t *lens, int s, int n, int64_t max_blocks, int64_t &first)
+{
+    const int64_t have = lens[s];
+    first = have / kBlock;
+    if (have < 0 || n <= 0) return 0;
+    const int64_t last = (have + n - 1) / kBlock;
+    const int64_t cnt = (last < max_blocks ? last : max_blocks - 1) - first + 1;
+    return cnt > 0 ? (int)cnt : 0;
+}
+
+__device__ inline bool find_block(const int32_t *cu, const int32_t *lens, int seqs, int64_t m, int64_t max_blocks,
+                                  int idx, SeqTile &t, int64_t &block)
+{
+    int64_t first;
+    if (!cu) {
+        if (idx >= seqs) return false;
+        t.seq = idx;
+        t.tile = 0;
+        t.begin = idx;
+        t.n = 1;
+        if (blocks_reached(lens, idx, 1, max_blocks, first) == 0) return false;
+        block = first;
+        return true;
+    }
+    if (!find_tile(cu, seqs, m, idx, [&](int s, int n) { int64_t f; return blocks_reached(lens, s, n, max_blocks, f); }, t))
+        return false;
+    blocks_reached(lens, t.seq, t.n, max_blocks, first);
+    block = first + t.tile;
+    return true;
+}
+
+// order of the weights as unsigned integers: -0 as +0, NaN as +inf
+__device__ inline uint32_t weight_key(float w)
+{
+    if (w != w) w = __builtin_inff();
+    const uint32_t b = __float_as_uint(w + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
 
 // A launch holds fewer than 2^32 threads in x: longer grids go in several launches,
 // each with the index of its first workgroup.

@@ -1,0 +1,52 @@
+// attention_selected.hip -- attention of new tokens over the blocks of the 8-bit cache
+// that a list names for each of them and each kv head.
+//
+// The mathematics, the digits and a wave's work on a page are those of
+// attention_cached.hip; a page is found through the list and the sequence's table, and
+// the rows of a workgroup are one token's query heads of one kv head.
+#include "attention_cached.hpp"
+
+namespace bl {
+
+// For the launch rules a token and its list are a sequence and its table
+static CachedProblem by_rows(const SelectedProblem &p)
+{
+    CachedProblem r = p.c;
+    r.seqs = p.c.m;
+    r.max_blocks = p.keep;
+    r.cu = nullptr;
+    return r;
+}
+
+struct SelectedLayout {
+    int64_t part_ml, bytes;
+};
+static SelectedLayout selected_layout(const CachedProblem &r)
+{
+    const int64_t splits = launch_shape(r, row_tiles(r)).splits, rows = r.m * r.q_heads;
+    SelectedLayout L{};
+    if (splits == 1) return L;
+    L.part_ml = round_up(splits * rows * r.head_dim * 4, 256);
+    L.bytes = L.part_ml + round_up(splits * rows * 8, 256);
+    return L;
+}
+
+int64_t attention_selected_workspace(const SelectedProblem &p) { return selected_layout(by_rows(p)).bytes; }
+
+hipError_t launch_attention_selected(const SelectedProblem &p, void *ws, hipStream_t st)
+{
+    const CachedProblem r = by_rows(p);
+    const int rt = row_tiles(r);
+    const Shape shape = launch_shape(r, rt);
+    CachedArgs a = cached_args(p.c, shape, rt);
+    a.selected = p.selected;
+    a.keep = p.keep;
+    if (a.splits > 1) {
+        a.part_o = static_cast<float *>(ws);
+        a.part_ml = reinterpret_cast<float *>(static_cast<char *>(ws) + selected_layout(r).part_ml);
+    }
+    launch_tiles<kSelected>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, a.splits, st);
+    return hipGetLastError();
+}
+
+}  // namespace bl

@@ -33,6 +33,14 @@ struct Library {
     decltype(&bitlinear_attention_cached_workspace_size) attention_cached_workspace_size;
     decltype(&bitlinear_attention_cached) attention_cached;
     decltype(&bitlinear_cache_evict) cache_evict;
+    decltype(&bitlinear_rotate) rotate;
+    decltype(&bitlinear_attention_shared_workspace_size) attention_shared_workspace_size;
+    decltype(&bitlinear_attention_shared) attention_shared;
+    decltype(&bitlinear_cache_bounds) cache_bounds;
+    decltype(&bitlinear_block_select_workspace_size) block_select_workspace_size;
+    decltype(&bitlinear_block_select) block_select;
+    decltype(&bitlinear_attention_selected_workspace_size) attention_selected_workspace_size;
+    decltype(&bitlinear_attention_selected) attention_selected;
 } g_lib;
 
 struct Refused {
@@ -376,6 +384,219 @@ PyObject *cache_evict(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// an optional gain of every head's norm
+const float *gain_of(PyObject *o, const char *name, int64_t d, at::Device device)
+{
+    if (o == Py_None) return nullptr;
+    const int64_t per[1] = {d};
+    return static_cast<const float *>(dense(tensor(o, name), name, at::kFloat, per, device));
+}
+
+float float_of(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) refuse("");
+    return (float)v;
+}
+
+// (q, k, inv_freq, begin, cu_seqlens, interleaved, q_gain, k_gain, eps, magnitude, out)
+PyObject *rotate(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 11, [&]() -> PyObject * {
+        const at::Tensor &tq = first_tensor(a[0], "q"), &tk = tensor(a[1], "k");
+        const at::Device device = tq.device();
+        const at::ScalarType type = tq.scalar_type();
+        const Rows q = heads(tq, "q", type, device), k = heads(tk, "k", type, device);
+        const bl_dtype dtype = act_dtype(type);
+        if (k.m != q.m || k.d != q.d)
+            refuse("k must be [" + std::to_string(q.m) + "][kv_heads][" + std::to_string(q.d) + "], got " + shape_text(tk.sizes()));
+        const at::Tensor &freq = tensor(a[2], "inv_freq");
+        const auto *fp = static_cast<const float *>(dense(freq, "inv_freq", at::kFloat, freq.sizes(), device));
+        if (freq.dim() != 1) refuse("inv_freq must be fp32 [rotary_dim / 2]");
+        int64_t seqs = q.m;
+        const int32_t *cu = a[4] == Py_None ? nullptr : starts(a[4], device, seqs);
+        const int64_t per[1] = {seqs};
+        const auto *begin = static_cast<const int32_t *>(dense(tensor(a[3], "begin"), "begin", at::kInt, per, device));
+        const int interleaved = PyObject_IsTrue(a[5]);
+        if (interleaved < 0) refuse("");
+        const float *gq = gain_of(a[6], "q_gain", q.d, device), *gk = gain_of(a[7], "k_gain", q.d, device);
+        const float eps = float_of(a[8]), magnitude = float_of(a[9]);
+        at::Tensor oq, ok;
+        Rows q2 = q, k2 = k;
+        if (a[10] != Py_None) {
+            if (!PyTuple_Check(a[10]) || PyTuple_GET_SIZE(a[10]) != 2) refuse("out must be two tensors");
+            oq = tensor(PyTuple_GET_ITEM(a[10], 0), "out[0]");
+            ok = tensor(PyTuple_GET_ITEM(a[10], 1), "out[1]");
+            q2 = heads(oq, "out[0]", type, device);
+            k2 = heads(ok, "out[1]", type, device);
+            if (oq.sizes() != tq.sizes() || ok.sizes() != tk.sizes())
+                refuse("out must have the shapes of q and k, got " + shape_text(oq.sizes()) + " and " + shape_text(ok.sizes()));
+        }
+        {
+            WithoutGil free;
+            const c10::DeviceGuard guard(device);
+            if (!oq.defined()) {
+                oq = at::empty(tq.sizes(), tq.options());
+                ok = at::empty(tk.sizes(), tk.options());
+                q2 = {oq.data_ptr(), q.heads * q.d, q.m, q.heads, q.d};
+                k2 = {ok.data_ptr(), k.heads * k.d, k.m, k.heads, k.d};
+            }
+            done(g_lib.rotate(q.p, q.stride, k.p, k.stride, dtype, q.m, q.heads, k.heads, q.d, cu, begin, seqs, fp, 2 * freq.size(0),
+                              interleaved, magnitude, gq, gk, eps, const_cast<void *>(q2.p), q2.stride, const_cast<void *>(k2.p),
+                              k2.stride, stream_of(device)),
+                 "bitlinear_rotate");
+        }
+        return Py_BuildValue("NN", THPVariable_Wrap(oq), THPVariable_Wrap(ok));
+    });
+}
+
+// (q, cache, prefix_table, prefix_len, block_table, lens, cu_seqlens, scale, out, workspace)
+PyObject *attention_shared(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 10, [&]() -> PyObject * {
+        const at::Tensor &tq = first_tensor(a[0], "q");
+        const at::Device device = tq.device();
+        const at::ScalarType type = tq.scalar_type();
+        const Rows q = heads(tq, "q", type, device);
+        const bl_dtype dtype = act_dtype(type);
+        const Cache c = cache_args(a[1], -1, q.d, device);
+        const at::Tensor &pt = tensor(a[2], "prefix_table");
+        if (pt.dim() != 1) refuse("prefix_table must be int32 [prefix_blocks]");
+        const auto *pages = static_cast<const int32_t *>(dense(pt, "prefix_table", at::kInt, pt.sizes(), device));
+        const int64_t one[1] = {1};
+        const auto *length = static_cast<const int32_t *>(dense(tensor(a[3], "prefix_len"), "prefix_len", at::kInt, one, device));
+        const Table t = table_args(a[4], a[5], a[6], q.m, device, "lens");
+        const float scale = scale_of(a[7], q.d);
+        const int64_t shape[2] = {q.m, q.heads * q.d};
+        at::Tensor out, ws = given_workspace(a[9]);
+        if (a[8] != Py_None) {
+            out = tensor(a[8], "out");
+            dense(out, "out", type, shape, device);
+        }
+        {
+            WithoutGil free;
+            const c10::DeviceGuard guard(device);
+            if (!out.defined()) out = at::empty(shape, tq.options());
+            const size_t bytes = g_lib.attention_shared_workspace_size(q.m, q.heads, c.heads, q.d, t.seqs, t.wide, pt.size(0));
+            void *const space = scratch(bytes, ws, device);
+            done(g_lib.attention_shared(q.p, q.stride, dtype, q.m, q.heads, c.heads, q.d, pages, pt.size(0), length, t.cu, t.lens,
+                                        t.seqs, t.table, t.wide, c.k, c.v, c.ks, c.vs, c.pages, scale, out.data_ptr(), space, bytes,
+                                        stream_of(device)),
+                 "bitlinear_attention_shared");
+        }
+        return THPVariable_Wrap(out);
+    });
+}
+
+struct Bounds {
+    int8_t *p;
+    int64_t pages, heads, d;
+};
+Bounds bounds_of(PyObject *o, at::Device device)
+{
+    const at::Tensor &t = tensor(o, "bounds");
+    if (t.dim() != 4 || t.size(2) != 2) refuse("bounds must be int8 [pages][kv_heads][2][head_dim]");
+    return {static_cast<int8_t *>(dense(t, "bounds", at::kChar, t.sizes(), device)), t.size(0), t.size(1), t.size(3)};
+}
+
+// (cache, bounds, block_table, lens, cu_seqlens, m)
+PyObject *cache_bounds(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 6, [&]() -> PyObject * {
+        if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != 4) refuse("cache must be a KVCache");
+        const at::Device device = first_tensor(PyTuple_GET_ITEM(a[0], 0), "cache.k").device();
+        const Cache c = cache_args(a[0], -1, -1, device);
+        const Bounds b = bounds_of(a[1], device);
+        if (b.pages != c.pages || b.heads != c.heads || b.d != c.d)
+            refuse("bounds must be [" + std::to_string(c.pages) + "][" + std::to_string(c.heads) + "][2][" + std::to_string(c.d) +
+                   "], got " + shape_text(THPVariable_Unpack(a[1]).sizes()));
+        const int64_t m = int_of(a[5]);
+        const Table t = table_args(a[2], a[3], a[4], m, device, "lens");
+        {
+            WithoutGil free;
+            const c10::DeviceGuard guard(device);
+            done(g_lib.cache_bounds(c.k, c.pages, c.heads, c.d, m, t.cu, t.lens, t.seqs, t.table, t.wide, b.p, stream_of(device)),
+                 "bitlinear_cache_bounds");
+        }
+        Py_RETURN_NONE;
+    });
+}
+
+// (q, bounds, k_scale, block_table, lens, keep, cu_seqlens, first, recent, out, workspace)
+PyObject *block_select(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 11, [&]() -> PyObject * {
+        const at::Tensor &tq = first_tensor(a[0], "q");
+        const at::Device device = tq.device();
+        const at::ScalarType type = tq.scalar_type();
+        const Rows q = heads(tq, "q", type, device);
+        const bl_dtype dtype = act_dtype(type);
+        const Bounds b = bounds_of(a[1], device);
+        if (b.d != q.d) refuse("bounds are of heads of " + std::to_string(b.d) + ", q of " + std::to_string(q.d));
+        const int64_t per[2] = {b.pages, b.heads};
+        const auto *ks = static_cast<const float *>(dense(tensor(a[2], "k_scale"), "k_scale", at::kFloat, per, device));
+        const Table t = table_args(a[3], a[4], a[6], q.m, device, "lens");
+        const int64_t keep = int_of(a[5]), first = int_of(a[7]), recent = int_of(a[8]);
+        // before there is an output of that size
+        if (keep < 1 || keep > BL_MAX_DIM) done(BL_ERR_VALUE, "bitlinear_block_select");
+        const int64_t shape[3] = {q.m, b.heads, keep};
+        at::Tensor out, ws = given_workspace(a[10]);
+        if (a[9] != Py_None) {
+            out = tensor(a[9], "out");
+            dense(out, "out", at::kInt, shape, device);
+        }
+        {
+            WithoutGil free;
+            const c10::DeviceGuard guard(device);
+            if (!out.defined()) out = at::empty(shape, at::TensorOptions(at::kInt).device(device));
+            const size_t bytes = g_lib.block_select_workspace_size(q.m, b.heads, t.wide);
+            void *const space = scratch(bytes, ws, device);
+            done(g_lib.block_select(q.p, q.stride, dtype, q.m, q.heads, b.heads, q.d, t.cu, t.lens, t.seqs, t.table, t.wide, b.p, ks,
+                                    b.pages, keep, first, recent, static_cast<int32_t *>(out.data_ptr()), space, bytes,
+                                    stream_of(device)),
+                 "bitlinear_block_select");
+        }
+        return THPVariable_Wrap(out);
+    });
+}
+
+// (q, cache, block_table, lens, selected, cu_seqlens, scale, out, workspace)
+PyObject *attention_selected(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 9, [&]() -> PyObject * {
+        const at::Tensor &tq = first_tensor(a[0], "q");
+        const at::Device device = tq.device();
+        const at::ScalarType type = tq.scalar_type();
+        const Rows q = heads(tq, "q", type, device);
+        const bl_dtype dtype = act_dtype(type);
+        const Cache c = cache_args(a[1], -1, q.d, device);
+        const Table t = table_args(a[2], a[3], a[5], q.m, device, "lens");
+        const at::Tensor &sel = tensor(a[4], "selected");
+        if (sel.dim() != 3) refuse("selected must be int32 [m][kv_heads][keep]");
+        const int64_t each[3] = {q.m, c.heads, sel.size(2)};
+        const auto *chosen = static_cast<const int32_t *>(dense(sel, "selected", at::kInt, each, device));
+        const float scale = scale_of(a[6], q.d);
+        const int64_t shape[2] = {q.m, q.heads * q.d};
+        at::Tensor out, ws = given_workspace(a[8]);
+        if (a[7] != Py_None) {
+            out = tensor(a[7], "out");
+            dense(out, "out", type, shape, device);
+        }
+        {
+            WithoutGil free;
+            const c10::DeviceGuard guard(device);
+            if (!out.defined()) out = at::empty(shape, tq.options());
+            const size_t bytes = g_lib.attention_selected_workspace_size(q.m, q.heads, c.heads, q.d, each[2]);
+            void *const space = scratch(bytes, ws, device);
+            done(g_lib.attention_selected(q.p, q.stride, dtype, q.m, q.heads, c.heads, q.d, t.cu, t.lens, t.seqs, t.table, t.wide, chosen,
+                                          each[2], c.k, c.v, c.ks, c.vs, c.pages, scale, out.data_ptr(), space, bytes,
+                                          stream_of(device)),
+                 "bitlinear_attention_selected");
+        }
+        return THPVariable_Wrap(out);
+    });
+}
+
 template <typename F>
 bool find(void *lib, const char *name, F &f)
 {
@@ -396,7 +617,14 @@ PyObject *bind(PyObject *, PyObject *args)
         !find(lib, "bitlinear_attention", l.attention) || !find(lib, "bitlinear_cache_append", l.cache_append) ||
         !find(lib, "bitlinear_cache_read", l.cache_read) ||
         !find(lib, "bitlinear_attention_cached_workspace_size", l.attention_cached_workspace_size) ||
-        !find(lib, "bitlinear_attention_cached", l.attention_cached) || !find(lib, "bitlinear_cache_evict", l.cache_evict)) {
+        !find(lib, "bitlinear_attention_cached", l.attention_cached) || !find(lib, "bitlinear_cache_evict", l.cache_evict) ||
+        !find(lib, "bitlinear_rotate", l.rotate) ||
+        !find(lib, "bitlinear_attention_shared_workspace_size", l.attention_shared_workspace_size) ||
+        !find(lib, "bitlinear_attention_shared", l.attention_shared) || !find(lib, "bitlinear_cache_bounds", l.cache_bounds) ||
+        !find(lib, "bitlinear_block_select_workspace_size", l.block_select_workspace_size) ||
+        !find(lib, "bitlinear_block_select", l.block_select) ||
+        !find(lib, "bitlinear_attention_selected_workspace_size", l.attention_selected_workspace_size) ||
+        !find(lib, "bitlinear_attention_selected", l.attention_selected)) {
         PyErr_Format(error, "%s does not hold the attention calls: %s", path, lib ? "a symbol is missing" : dlerror());
         return nullptr;
     }
@@ -409,7 +637,8 @@ PyObject *bind(PyObject *, PyObject *args)
 
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr}, FAST(attention), FAST(cache_append), FAST(cache_read),
-                         FAST(attention_cached), FAST(cache_evict), {nullptr, nullptr, 0, nullptr}};
+                         FAST(attention_cached), FAST(cache_evict), FAST(rotate), FAST(attention_shared), FAST(cache_bounds),
+                         FAST(block_select), FAST(attention_selected), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

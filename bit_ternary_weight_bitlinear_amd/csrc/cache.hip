@@ -11,38 +11,6 @@ namespace bl {
 
 constexpr float kSmallestScale = 1e-30f;  // keeps 127 / s finite
 
-// Blocks of sequence s that rows lens .. lens+n-1 reach; first: the first one.
-__device__ inline int blocks_reached(const int32_t *lens, int s, int n, int64_t max_blocks, int64_t &first)
-{
-    const int64_t have = lens[s];
-    first = have / kBlock;
-    if (have < 0 || n <= 0) return 0;
-    const int64_t last = (have + n - 1) / kBlock;
-    const int64_t cnt = (last < max_blocks ? last : max_blocks - 1) - first + 1;
-    return cnt > 0 ? (int)cnt : 0;
-}
-
-__device__ inline bool find_block(const int32_t *cu, const int32_t *lens, int seqs, int64_t m, int64_t max_blocks,
-                                  int idx, SeqTile &t, int64_t &block)
-{
-    int64_t first;
-    if (!cu) {
-        if (idx >= seqs) return false;
-        t.seq = idx;
-        t.tile = 0;
-        t.begin = idx;
-        t.n = 1;
-        if (blocks_reached(lens, idx, 1, max_blocks, first) == 0) return false;
-        block = first;
-        return true;
-    }
-    if (!find_tile(cu, seqs, m, idx, [&](int s, int n) { int64_t f; return blocks_reached(lens, s, n, max_blocks, f); }, t))
-        return false;
-    blocks_reached(lens, t.seq, t.n, max_blocks, first);
-    block = first + t.tile;
-    return true;
-}
-
 // an earlier token's code under a scale that has grown by 1 / ratio
 __device__ inline int rescale_code(int c, float ratio) { return (int)rintf((float)c * ratio); }
 
@@ -270,14 +238,6 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const int8_t *__restric
 
 // ---------------------------------------------------------------- eviction
 constexpr int kEvictThreads = 1024;
-
-// order of the weights as unsigned integers: -0 as +0, NaN as +inf
-__device__ inline uint32_t weight_key(float w)
-{
-    if (w != w) w = __builtin_inff();
-    const uint32_t b = __float_as_uint(w + 0.0f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
 
 // One workgroup per sequence. The weight that the last kept block has is found by
 // its digits from the top, 11, 11 and 10 bits (counts in LDS, integers, so the

@@ -200,4 +200,65 @@ struct CachedProblem {
 int64_t attention_cached_workspace(const CachedProblem &p);
 hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t st);
 
+// the same over the blocks that `selected` [m][kv_heads][keep] lists (attention_selected.hip)
+struct SelectedProblem {
+    CachedProblem c;
+    const int32_t *selected;
+    int64_t keep;
+};
+int64_t attention_selected_workspace(const SelectedProblem &p);
+hipError_t launch_attention_selected(const SelectedProblem &p, void *ws, hipStream_t st);
+
+// the same behind a prefix that every sequence shares (attention_shared.hip)
+struct SharedProblem {
+    CachedProblem c;
+    const int32_t *prefix_table, *prefix_len;
+    int64_t prefix_blocks;
+};
+int64_t attention_shared_workspace(const SharedProblem &p);
+hipError_t launch_attention_shared(const SharedProblem &p, void *ws, hipStream_t st);
+
+// ---- rotation of queries and keys (rotate.hip)
+struct RotateProblem {
+    const void *q, *k;
+    int64_t q_stride, k_stride;
+    bool bf16;
+    int64_t m, q_heads, kv_heads, head_dim;
+    const int32_t *cu, *begin;
+    int64_t seqs;
+    const float *inv_freq;
+    int64_t rotary_dim;
+    bool interleaved;
+    float magnitude;
+    const float *q_gain, *k_gain;
+    float eps;
+    void *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+};
+hipError_t launch_rotate(const RotateProblem &p, hipStream_t st);
+
+// ---- bounds of the cache's blocks and the choice by them (blocks.hip)
+struct CacheBounds {
+    const int8_t *k_codes;
+    int8_t *bounds;
+    int64_t pages, kv_heads, head_dim, m;
+    const int32_t *cu, *lens, *table;
+    int64_t seqs, max_blocks;
+};
+hipError_t launch_cache_bounds(const CacheBounds &p, hipStream_t st);
+struct SelectProblem {
+    const void *q;
+    int64_t q_stride;
+    bool bf16;
+    int64_t m, q_heads, kv_heads, head_dim;
+    const int32_t *cu, *lens, *table;
+    int64_t seqs, max_blocks, pages;
+    const int8_t *bounds;
+    const float *k_scale;
+    int64_t keep, first, recent;
+    int32_t *selected;
+};
+int64_t block_select_workspace(int64_t m, int64_t kv_heads, int64_t max_blocks);
+hipError_t launch_block_select(const SelectProblem &p, void *ws, hipStream_t st);
+
 }  // namespace bl

@@ -1,0 +1,179 @@
+// rotate.hip -- rotation of queries and keys by their tokens' positions, with an RMS
+// norm of every head before it.
+//
+//   x^ = (x * r) * gain,  r = 1 / sqrt(mean_d x^2 + eps)          (where a gain is given)
+//   (a, b) -> magnitude * (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
+//
+// for the pairs i of the head's first rotary_dim elements; the others pass. Bound by HBM
+// with many tokens (every element read once and written once), by one token's latency with
+// few. A wave works on one token: its 64 lanes compute the token's angles once, for all of
+// its heads, and exchange the cosines and sines through LDS; a lane then holds the same two
+// 16-byte pieces of every head that it gets, both elements of each pair among them, so a
+// norm is one reduction over 4 to 16 neighbouring lanes and a rotation none.
+//
+// The angle in 64 bits: the product of a position and an fp32 frequency by its rounded value
+// and the remainder, less the multiple of pi / 2 next to it (two constants, 106 bits of
+// pi / 2), so positions up to 2^31 cost no digits; its cosine and sine are rounded to fp32.
+#include "attention.hpp"
+
+namespace bl {
+
+struct RotateArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride, m;
+    int q_heads, kv_heads, seqs, pairs;  // pairs: rotary_dim / 2
+    const int32_t *cu, *begin;
+    const float *inv_freq, *q_gain, *k_gain;
+    float eps, magnitude;
+    int parts;  // waves per token
+};
+
+// Cosine and sine of position * freq: Taylor's series to r^15 on |r| <= pi / 4 (off by
+// less than 1e-16 of 1), rounded to fp32 once.
+__device__ inline float2 turn(int64_t position, float freq)
+{
+    const double p = (double)position, f = freq, t = p * f, rest = __builtin_fma(p, f, -t);
+    const double n = __builtin_rint(t * 0.6366197723675814);  // 2 / pi
+    double r = __builtin_fma(n, -1.5707963267948966, t);
+    r = __builtin_fma(n, -6.123233995736766e-17, r) + rest;
+    const double z = r * r;
+    double s = -1.0 / 1307674368000.0, c = -1.0 / 87178291200.0;
+    s = __builtin_fma(s, z, 1.0 / 6227020800.0);
+    c = __builtin_fma(c, z, 1.0 / 479001600.0);
+    s = __builtin_fma(s, z, -1.0 / 39916800.0);
+    c = __builtin_fma(c, z, -1.0 / 3628800.0);
+    s = __builtin_fma(s, z, 1.0 / 362880.0);
+    c = __builtin_fma(c, z, 1.0 / 40320.0);
+    s = __builtin_fma(s, z, -1.0 / 5040.0);
+    c = __builtin_fma(c, z, -1.0 / 720.0);
+    s = __builtin_fma(s, z, 1.0 / 120.0);
+    c = __builtin_fma(c, z, 1.0 / 24.0);
+    s = __builtin_fma(s, z, -1.0 / 6.0);
+    c = __builtin_fma(c, z, -0.5);
+    const float sine = (float)__builtin_fma(s * z, r, r), cosine = (float)__builtin_fma(c, z, 1.0);
+    const int quarter = (int)(long long)n & 3;
+    const float a = quarter & 1 ? sine : cosine, b = quarter & 1 ? cosine : sine;
+    return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter >= 2 ? -b : b);
+}
+
+template <typename T, int D, bool INTERLEAVED>
+__global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int first)
+{
+    constexpr int E = 16 / sizeof(T);  // elements of a piece
+    constexpr int LANES = D / (2 * E);  // of a head
+    constexpr int HEADS = 64 / LANES;   // of a wave at once
+    __shared__ __align__(16) float2 turns[4][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t item = ((int64_t)first + blockIdx.x) * 4 + wave;
+    const int64_t row = item / a.parts;
+    const int part = (int)(item - row * a.parts);
+    if (row >= a.m) return;
+    int seq, place;
+    if (!find_row(a.cu, a.seqs, a.m, row, seq, place)) return;
+    const int begin = a.begin[seq];
+    if (begin < 0) return;  // an unused slot
+    const int slot = lane % LANES, heads = a.q_heads + a.kv_heads;
+    const bool rotary = slot * E < a.pairs;
+    // elements of a lane: `lo` .. lo+E-1 and `hi` .. hi+E-1 of the head
+    const int lo = INTERLEAVED ? 2 * E * slot : rotary ? E * slot : 2 * E * slot;
+    const int hi = INTERLEAVED ? lo + E : rotary ? a.pairs + lo : lo + E;
+
+    float gq[2 * E], gk[2 * E];
+    auto gains = [&](const float *g, float (&out)[2 * E]) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            const v4f u = g ? *reinterpret_cast<const v4f *>(g + lo + i) : v4f{1.0f, 1.0f, 1.0f, 1.0f};
+            const v4f v = g ? *reinterpret_cast<const v4f *>(g + hi + i) : v4f{1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                out[i + j] = u[j];
+                out[E + i + j] = v[j];
+            }
+        }
+    };
+    gains(a.q_gain, gq);
+    gains(a.k_gain, gk);
+
+    if (lane < a.pairs) {
+        const float2 t = turn((int64_t)begin + place, a.inv_freq[lane]);
+        turns[wave][lane] = make_float2(t.x * a.magnitude, t.y * a.magnitude);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    float co[E], si[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const float2 t = rotary ? turns[wave][slot * E + i] : make_float2(1.0f, 0.0f);
+        co[i] = t.x;
+        si[i] = t.y;
+    }
+
+    for (int h0 = part * HEADS; h0 < heads; h0 += a.parts * HEADS) {
+        const int h = h0 + lane / LANES;
+        const bool there = h < heads, is_q = h < a.q_heads;
+        const int at = is_q ? h : h - a.q_heads;
+        T x[2 * E];
+        const T *src = static_cast<const T *>(is_q ? a.q : a.k) + row * (is_q ? a.q_stride : a.k_stride) + (int64_t)at * D;
+        if (there) {
+            *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(src + lo);
+            *reinterpret_cast<uint4 *>(x + E) = *reinterpret_cast<const uint4 *>(src + hi);
+        }
+        float f[2 * E];
+#pragma unroll
+        for (int i = 0; i < 2 * E; ++i) f[i] = there ? to_f32(x[i]) : 0.0f;
+        if ((is_q ? a.q_gain : a.k_gain) != nullptr) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * E; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
+            ss += __int_as_float(dpp_mov<kDppQuadXor1>(__float_as_int(ss)));
+            ss += __int_as_float(dpp_mov<kDppQuadXor2>(__float_as_int(ss)));
+            if constexpr (LANES >= 8) ss += __int_as_float(dpp_mov<kDppRowHalfMirror>(__float_as_int(ss)));
+            if constexpr (LANES >= 16) ss += __int_as_float(dpp_mov<kDppRowMirror>(__float_as_int(ss)));
+            const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+            for (int i = 0; i < 2 * E; ++i) f[i] = (f[i] * r) * (is_q ? gq[i] : gk[i]);
+        }
+        if (rotary) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                float &u = f[INTERLEAVED ? 2 * i : i], &v = f[INTERLEAVED ? 2 * i + 1 : E + i];
+                const float a0 = u, b0 = v;
+                u = __builtin_fmaf(a0, co[i], -(b0 * si[i]));
+                v = __builtin_fmaf(b0, co[i], a0 * si[i]);
+            }
+        }
+        if (!there) continue;
+#pragma unroll
+        for (int i = 0; i < 2 * E; ++i) store_out(&x[i], f[i]);
+        T *dst = static_cast<T *>(is_q ? a.q_out : a.k_out) + row * (is_q ? a.q_out_stride : a.k_out_stride) + (int64_t)at * D;
+        *reinterpret_cast<uint4 *>(dst + lo) = *reinterpret_cast<const uint4 *>(x);
+        *reinterpret_cast<uint4 *>(dst + hi) = *reinterpret_cast<const uint4 *>(x + E);
+    }
+}
+
+hipError_t launch_rotate(const RotateProblem &p, hipStream_t st)
+{
+    RotateArgs a{};
+    a.q = p.q; a.k = p.k; a.q_out = p.q_out; a.k_out = p.k_out;
+    a.q_stride = p.q_stride; a.k_stride = p.k_stride; a.q_out_stride = p.q_out_stride; a.k_out_stride = p.k_out_stride;
+    a.m = p.m; a.q_heads = (int)p.q_heads; a.kv_heads = (int)p.kv_heads; a.seqs = (int)p.seqs; a.pairs = (int)p.rotary_dim / 2;
+    a.cu = p.cu; a.begin = p.begin; a.inv_freq = p.inv_freq; a.q_gain = p.q_gain; a.k_gain = p.k_gain;
+    a.eps = p.eps; a.magnitude = p.magnitude;
+    // few tokens: a wave for every 64 lanes' worth of heads
+    const int64_t rounds = ceil_div((p.q_heads + p.kv_heads) * p.head_dim * (p.bf16 ? 2 : 4), 64 * 32);
+    a.parts = p.m * rounds <= 2048 ? (int)rounds : 1;
+    in_launches(ceil_div(p.m * a.parts, 4), [&](int first, unsigned n) {
+        auto go = [&](auto type, auto width) {
+            using T = decltype(type);
+            constexpr int D = decltype(width)::value;
+            if (p.interleaved) hipLaunchKernelGGL((rotate_kernel<T, D, true>), dim3(n), dim3(256), 0, st, a, first);
+            else hipLaunchKernelGGL((rotate_kernel<T, D, false>), dim3(n), dim3(256), 0, st, a, first);
+        };
+        if (p.bf16) p.head_dim == 128 ? go(bf16_t{}, Width<128>{}) : go(bf16_t{}, Width<64>{});
+        else p.head_dim == 128 ? go(float{}, Width<128>{}) : go(float{}, Width<64>{});
+    });
+    return hipGetLastError();
+}
+
+}  // namespace bl

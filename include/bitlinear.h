@@ -472,6 +472,126 @@ bl_status bitlinear_cache_evict(const int32_t *block_table, const int32_t *lens,
                                 int32_t *table_out, int32_t *lens_out, float *weights_out, int32_t *evicted,
                                 int32_t *evicted_count, void *stream);
 
+/*
+ * Rotation of queries and keys by their tokens' positions, between the QKV projection
+ * and the attention or the cache, with an optional RMS norm of every head before it.
+ * Row i of sequence s is position begin[s] + i (begin as `lens` of the cache calls: for
+ * a prompt 0, for new tokens the tokens before them, evicted ones included; a negative
+ * entry marks an unused slot). Per row and head x, y = x without a gain and otherwise
+ *   y = (x * r) * gain[d],  r = 1 / sqrt(mean_d x^2 + eps)
+ * in fp32, and for the pairs i < rotary_dim / 2 of y, t = position * inv_freq[i],
+ *   (a, b) -> (a * cs - b * sn, b * cs + a * sn),  cs = magnitude * cos t, sn = magnitude * sin t
+ * with (a, b) = (y[2i], y[2i + 1]) if `interleaved`, (y[i], y[i + rotary_dim / 2]) if not;
+ * elements from rotary_dim on stay y. One rounding to `dtype` at the end. Angles are
+ * exact up to rounding of cs and sn to fp32, whatever the position.
+ *   q, k            as in bitlinear_attention
+ *   inv_freq        fp32 [rotary_dim / 2], 4-byte aligned
+ *   rotary_dim      16 .. head_dim, a multiple of 16 (BL_ERR_SHAPE otherwise)
+ *   interleaved     0 or 1 (BL_ERR_VALUE otherwise)
+ *   magnitude       finite, eps finite and >= 0 (BL_ERR_VALUE otherwise)
+ *   q_gain, k_gain  optional fp32 [head_dim], 16-byte aligned; NULL = no norm
+ *   q_out, k_out    rows like q's and k's (output), `*_stride` elements apart. In place is
+ *                   allowed: q_out = q with the same stride, k_out = k likewise. Rows of
+ *                   unused slots and outside the sequences are not written.
+ */
+bl_status bitlinear_rotate(const void *q, int64_t q_stride, const void *k, int64_t k_stride, bl_dtype dtype, int64_t m,
+                           int64_t q_heads, int64_t kv_heads, int64_t head_dim, const int32_t *cu_seqlens,
+                           const int32_t *begin, int64_t seqs, const float *inv_freq, int64_t rotary_dim, int interleaved,
+                           float magnitude, const float *q_gain, const float *k_gain, float eps, void *q_out,
+                           int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+
+/* Bytes of workspace of bitlinear_attention_shared (0 for invalid shapes) */
+size_t bitlinear_attention_shared_workspace_size(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                                 int64_t seqs, int64_t max_blocks, int64_t prefix_blocks);
+
+/*
+ * Attention of new tokens over the cache of a batch whose sequences share a prefix: a
+ * row sees the prefix's tokens 0 .. prefix_len - 1 that have a page, and its own
+ * sequence's as in bitlinear_attention_cached (lens does not count the prefix). The
+ * prefix is read once for all rows.
+ *   prefix_table  int32 [prefix_blocks] on the device: the prefix's pages, in the caches
+ *                 of the sequences' own. Entries that name no page hold no tokens.
+ *   prefix_len    int32 [1] on the device; below 1: no prefix, and at most
+ *                 64 * prefix_blocks count
+ * Over the prefix q is held to 2^-22 of itself (fp32; elements below 2^-17 of their
+ * row's largest, or of 1e-30, to 2^-39 of that) or exactly (bf16, to 2^-39 of the
+ * largest), and the softmax weights to 2^-22 (fp32) or 2^-11 (bf16) of themselves, or 2^-39
+ * of the largest of their block and row; sums are fp32. The rest is as in
+ * bitlinear_attention_cached: rows that see nothing, rows of q that are not finite, unused
+ * slots and rows outside the sequences among it. Results do not depend on the order of
+ * execution.
+ * BL_ERR_SHAPE also where m * q_heads / kv_heads passes 2^31 - 1024.
+ *   workspace  >= bitlinear_attention_shared_workspace_size() bytes
+ */
+bl_status bitlinear_attention_shared(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m, int64_t q_heads,
+                                     int64_t kv_heads, int64_t head_dim, const int32_t *prefix_table, int64_t prefix_blocks,
+                                     const int32_t *prefix_len, const int32_t *cu_seqlens, const int32_t *lens,
+                                     int64_t seqs, const int32_t *block_table, int64_t max_blocks, const int8_t *k_codes,
+                                     const int8_t *v_codes, const float *k_scale, const float *v_scale, int64_t pages,
+                                     float scale, void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Bounds of the cache's blocks: per page and kv head the largest and the smallest code of
+ * K of every dim, over the tokens that the block holds.
+ *   bounds  int8 [pages][kv_heads][2][head_dim], 16-byte aligned (output): [0] the largest,
+ *           [1] the smallest. Blocks that rows lens[s] .. of a sequence reach are written
+ *           (called after bitlinear_cache_append with the same rows: the blocks that
+ *           changed), others left as they are.
+ * Other arguments as in bitlinear_cache_append; m counts the rows.
+ */
+bl_status bitlinear_cache_bounds(const int8_t *k_codes, int64_t pages, int64_t kv_heads, int64_t head_dim, int64_t m,
+                                 const int32_t *cu_seqlens, const int32_t *lens, int64_t seqs, const int32_t *block_table,
+                                 int64_t max_blocks, int8_t *bounds, void *stream);
+
+/* Bytes of workspace of bitlinear_block_select (0 if none, or for invalid shapes) */
+size_t bitlinear_block_select_workspace_size(int64_t m, int64_t kv_heads, int64_t max_blocks);
+
+/*
+ * Chooses the blocks that a new token attends to, for every row and kv head, by an upper
+ * bound of the products of its query heads (summed over the group) with a block's keys. The
+ * queries of a row's kv head become integers as activations do,
+ *   c = rint(x * (127 / s)),  s = max(max |x| over the group's heads and dims, 1e-30)
+ * in fp32, ties to even (NaN counts as 0, infinities as the largest finite number), and
+ *   T = sum_d high_d * sum_h max(c_hd, 0) + low_d * sum_h min(c_hd, 0)    (exact)
+ *   score = fp32(T) * k_scale of the page
+ * Row i of sequence s is token lens[s] + i, already appended and in the bounds, and has
+ * (lens[s] + i) / 64 + 1 blocks (at most max_blocks). The first `first`, the last `recent`
+ * of these and, up to `keep` in all, the ones of the largest score stay; of equal scores the
+ * lower block, NaN counts as +inf, and a block without a page has -inf. The last `recent`
+ * blocks' bounds are not needed: with recent >= 1, those of a block that is still filling.
+ *   keep      first + recent .. 2^20, first >= 0, recent >= 1 (BL_ERR_VALUE otherwise)
+ *   selected  int32 [m][kv_heads][keep] (output): blocks of the sequence, ascending, then
+ *             -1; rows of unused slots and outside the sequences are not written
+ *   q_heads / kv_heads <= 128 (BL_ERR_SHAPE otherwise)
+ *   workspace >= bitlinear_block_select_workspace_size() bytes
+ */
+bl_status bitlinear_block_select(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m, int64_t q_heads,
+                                 int64_t kv_heads, int64_t head_dim, const int32_t *cu_seqlens, const int32_t *lens,
+                                 int64_t seqs, const int32_t *block_table, int64_t max_blocks, const int8_t *bounds,
+                                 const float *k_scale, int64_t pages, int64_t keep, int64_t first, int64_t recent,
+                                 int32_t *selected, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of bitlinear_attention_selected (0 if none, or for invalid shapes) */
+size_t bitlinear_attention_selected_workspace_size(int64_t m, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                                   int64_t keep);
+
+/*
+ * Attention of new tokens over chosen blocks of the cache: bitlinear_attention_cached, but
+ * a row and kv head sees the tokens 0 .. lens[s] + i of the blocks that
+ *   selected  int32 [m][kv_heads][keep], keep 1 .. 2^20
+ * lists for it. Entries outside 0 .. max_blocks - 1 name no block, wherever they stand; a
+ * block counts as often as it is listed. Precision, rows that see nothing (0) or are not
+ * finite, unused slots: as there.
+ * BL_ERR_SHAPE also where m * q_heads / kv_heads passes 2^31 - 1024.
+ *   workspace  >= bitlinear_attention_selected_workspace_size() bytes
+ */
+bl_status bitlinear_attention_selected(const void *q, int64_t q_stride, bl_dtype dtype, int64_t m, int64_t q_heads,
+                                       int64_t kv_heads, int64_t head_dim, const int32_t *cu_seqlens, const int32_t *lens,
+                                       int64_t seqs, const int32_t *block_table, int64_t max_blocks,
+                                       const int32_t *selected, int64_t keep, const int8_t *k_codes,
+                                       const int8_t *v_codes, const float *k_scale, const float *v_scale, int64_t pages,
+                                       float scale, void *out, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *bitlinear_status_string(bl_status status);
 
