@@ -37,7 +37,8 @@ FLAGS = [
 # Where LDS lets one workgroup of four waves onto a CU, a wave may have more than 256
 # registers and the compiler puts matrix results into the accumulation half of them,
 # which vector instructions reach by copies only: this keeps them in the other.
-EXTRA_FLAGS = {"attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+EXTRA_FLAGS = {"attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+               "attention_shared.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def build_binding(verbose: bool = False) -> str | None:

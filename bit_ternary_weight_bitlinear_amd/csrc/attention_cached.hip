@@ -69,7 +69,7 @@ hipError_t launch_attention_cached(const CachedProblem &p, void *ws, hipStream_t
         if (a.splits == 1) a.final_ml = reinterpret_cast<float *>(base + L.final_ml);
     }
 
-    launch_tiles<kWhole>(p, a, shape, rt, query_tiles(p, rt), a.splits, st);
+    launch_tiles<kWhole>(p, a, shape, rt, query_tiles(p, rt), st);
     if (p.weights && a.splits == 1) {
         const int64_t blocks64 = ceil_div(p.max_blocks, 64);
         in_launches(p.seqs, [&](int first, unsigned n) {

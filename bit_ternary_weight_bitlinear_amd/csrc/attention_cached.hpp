@@ -74,7 +74,7 @@ struct CachedArgs {
     const float *prefix_o, *prefix_ml;
     const int32_t *prefix_len;
     int64_t prefix_blocks;
-    int prefix_splits, prefix_waves;
+    int prefix_splits;
 };
 
 __device__ inline int parts_of(int npages, int splits, int waves)
@@ -83,12 +83,18 @@ __device__ inline int parts_of(int npages, int splits, int waves)
     return npages <= chunk ? 1 : (npages + chunk - 1) / chunk;
 }
 
-// a prefix's pages, and the parts that its results come in (none for an empty one)
+// A prefix's pages, those of a workgroup (whole rounds of its waves: a part less to write and
+// to join costs no time), and the parts that its results come in (none for an empty one)
+constexpr int kPrefixWaves = 4;
+__device__ inline int prefix_chunk(int npages, int splits)
+{
+    return (pages_per_split(npages, splits, kPrefixWaves) + kPrefixWaves - 1) / kPrefixWaves * kPrefixWaves;
+}
 __device__ inline int prefix_pages(const int32_t *len, int64_t blocks) { return *len <= 0 ? 0 : pages_of(*len, 0, blocks); }
 __device__ inline int prefix_parts(const CachedArgs &a)
 {
-    const int np = prefix_pages(a.prefix_len, a.prefix_blocks);
-    return np == 0 ? 0 : parts_of(np, a.prefix_splits, a.prefix_waves);
+    const int np = prefix_pages(a.prefix_len, a.prefix_blocks), chunk = prefix_chunk(np, a.prefix_splits);
+    return (np + chunk - 1) / chunk;
 }
 
 // tiles of 4*RT query rows: row r of a sequence is token r / group, head r % group.
@@ -121,26 +127,30 @@ __device__ inline bool find_rows(const CachedArgs &a, int idx, SeqTile &t, int &
 // what a row adds to the blocks' weights: nothing if it sees nothing or is not finite
 __device__ inline float2 final_of(float top, float l) { return make_float2(top, l > 0.0f ? 1.0f / l : 0.0f); }
 
-template <typename T, int D, int RT, int W, bool STAT, CachedMode MODE = kWhole>
-__global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kernel(CachedArgs a, int first_tile)
+// words of LDS that a workgroup of attention_cached_tile needs: digits of q in operand
+// order, [row tile][step][lane][16 bytes]; per wave the digits of p, [16 rows][16 dwords of
+// 4 tokens]; at the end the waves' results
+template <int D, int RT, int W>
+struct CachedLds {
+    static constexpr int query = RT * (D / 64) * 256, digits = W * 256, join = W * 4 * RT * (D + 2);
+    static constexpr int words = query + digits > join ? query + digits : join;
+};
+
+// One workgroup's work: split `split` of tile idx of kv head `head`. row_scale: 4 * RT floats of LDS
+template <typename T, int D, int RT, int W, bool STAT, CachedMode MODE>
+__device__ inline void attention_cached_tile(const CachedArgs &a, int idx, int head, int split, uint32_t *lds, float *row_scale)
 {
     constexpr int H = D / 64;   // matrix steps over the head width
     constexpr int N = D / 16;   // 16-dim tiles of the output
     constexpr int R = 4 * RT;   // query rows
     constexpr int E = D / 16;   // elements of a query row per thread
-    // digits of q in operand order, [row tile][step][lane][16 bytes]; per wave the
-    // digits of p, [16 rows][16 dwords of 4 tokens]; at the end the waves' results
-    constexpr int kQueryWords = RT * H * 256, kDigitWords = W * 256, kJoinWords = W * R * (D + 2);
-    constexpr int kWords = kQueryWords + kDigitWords;
-    __shared__ __align__(16) uint32_t lds[kWords > kJoinWords ? kWords : kJoinWords];
-    __shared__ float row_scale[R];
+    constexpr int kQueryWords = CachedLds<D, RT, W>::query;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane >> 4, c = lane & 15;
     SeqTile t;
     int at_tok;
-    if (!find_rows<RT, MODE>(a, first_tile + (int)blockIdx.z, t, at_tok)) return;
-    const int head = blockIdx.y, split = blockIdx.x;
+    if (!find_rows<RT, MODE>(a, idx, t, at_tok)) return;
     const int32_t *table = a.table + (int64_t)t.seq * a.max_blocks;
     const int32_t *chosen = MODE == kSelected ? a.selected + (t.begin * a.kv_heads + head) * a.keep : nullptr;
     // one split: the wave's pages do not depend on the length, which is on its way
@@ -370,7 +380,6 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
     }
     __syncthreads();
     const int64_t total_rows = a.m * a.q_heads;
-    const int parts = MODE == kBehindPrefix ? prefix_parts(a) : 0;
     for (int it = tid; it < R * D; it += 64 * W) {
         const int r = it / D, dim = it % D;
         if (r >= rows) break;
@@ -388,23 +397,7 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
         int tok, hq;
         place(r, tok, hq);
         const int64_t row = (t.begin + tok) * a.q_heads + hq;
-        if (MODE == kBehindPrefix && a.splits == 1) {
-            const float2 *ml = reinterpret_cast<const float2 *>(a.prefix_ml) + row;
-            const float *src = a.prefix_o + row * D + dim;
-            const float mine = top;
-            for (int s = 0; s < parts; ++s) top = fmaxf(top, ml[s * total_rows].x);
-            const float ref = top == kNegInf ? 0.0f : top, f = __builtin_amdgcn_exp2f(mine - ref);
-            o *= f;
-            l *= f;
-#pragma unroll 4
-            for (int s = 0; s < parts; ++s) {
-                const float2 v = ml[s * total_rows];
-                const float g = __builtin_amdgcn_exp2f(v.x - ref);
-                o = __builtin_fmaf(g, src[s * total_rows * D], o);
-                l = __builtin_fmaf(g, v.y, l);
-            }
-        }
-        if (a.splits > 1) {
+        if (a.splits > 1 || MODE == kBehindPrefix) {
             a.part_o[((int64_t)split * total_rows + row) * D + dim] = o;
             if (dim == 0) reinterpret_cast<float2 *>(a.part_ml)[(int64_t)split * total_rows + row] = make_float2(top, l);
         } else {
@@ -412,6 +405,14 @@ __global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kern
             if (STAT && dim == 0) reinterpret_cast<float2 *>(a.final_ml)[row] = final_of(top, l);
         }
     }
+}
+
+template <typename T, int D, int RT, int W, bool STAT, CachedMode MODE = kWhole>
+__global__ __launch_bounds__(64 * W, RT == 1 ? 4 : 2) void attention_cached_kernel(CachedArgs a, int first_tile)
+{
+    __shared__ __align__(16) uint32_t lds[CachedLds<D, RT, W>::words];
+    __shared__ float row_scale[4 * RT];
+    attention_cached_tile<T, D, RT, W, STAT, MODE>(a, first_tile + (int)blockIdx.z, blockIdx.y, blockIdx.x, lds, row_scale);
 }
 
 // Adds the attention weight of 64 blocks of a sequence, a block per lane and the
@@ -662,13 +663,23 @@ inline CachedArgs cached_args(const CachedProblem &p, const Shape &shape, int rt
     return a;
 }
 
-// The kernel over `tiles_in_all` tiles per head, and the joining launch where there are splits;
-// most_parts: a bound of the results that it joins
-template <CachedMode MODE>
-inline void launch_tiles(const CachedProblem &p, const CachedArgs &a, const Shape &shape, int rt, int64_t tiles_in_all, int64_t most_parts,
-                         hipStream_t st)
+// The joining launch; most_parts: a bound of the results that it joins
+template <CachedMode MODE, typename T, int D>
+inline void launch_join(const CachedProblem &p, const CachedArgs &a, int64_t most_parts, hipStream_t st)
 {
-    const int64_t blocks64 = ceil_div(p.max_blocks, 64);
+    const int64_t rows = p.m * p.q_heads, blocks64 = ceil_div(p.max_blocks, 64), extra = p.weights ? p.seqs * blocks64 : 0;
+    if (most_parts <= kFewSplits)
+        hipLaunchKernelGGL((attention_join_kernel<T, D, true, MODE>), dim3((unsigned)(ceil_div(rows, 512 / D) + extra)), dim3(512), 0, st, a,
+                           p.weights, (int)blocks64);
+    else
+        hipLaunchKernelGGL((attention_join_kernel<T, D, false, MODE>), dim3((unsigned)(rows + extra)), dim3(512), 0, st, a, p.weights,
+                           (int)blocks64);
+}
+
+// The kernel over `tiles_in_all` tiles per head, and the joining launch where there are splits
+template <CachedMode MODE>
+inline void launch_tiles(const CachedProblem &p, const CachedArgs &a, const Shape &shape, int rt, int64_t tiles_in_all, hipStream_t st)
+{
     auto go_waves = [&](auto type, auto width, auto tiles, auto waves) {
         using T = decltype(type);
         constexpr int D = decltype(width)::value, RT = decltype(tiles)::value, W = decltype(waves)::value;
@@ -682,14 +693,7 @@ inline void launch_tiles(const CachedProblem &p, const CachedArgs &a, const Shap
             }
             hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, false, MODE>), grid, dim3(64 * W), 0, st, a, first);
         }, kMostInZ);
-        if (a.splits == 1) return;
-        const int64_t rows = p.m * p.q_heads, extra = p.weights ? p.seqs * blocks64 : 0;
-        if (most_parts <= kFewSplits)
-            hipLaunchKernelGGL((attention_join_kernel<T, D, true, MODE>), dim3((unsigned)(ceil_div(rows, 512 / D) + extra)), dim3(512), 0, st,
-                               a, p.weights, (int)blocks64);
-        else
-            hipLaunchKernelGGL((attention_join_kernel<T, D, false, MODE>), dim3((unsigned)(rows + extra)), dim3(512), 0, st, a, p.weights,
-                               (int)blocks64);
+        if (a.splits > 1) launch_join<MODE, T, D>(p, a, a.splits, st);
     };
     auto go = [&](auto type, auto width, auto tiles) {
         constexpr int RT = decltype(tiles)::value;

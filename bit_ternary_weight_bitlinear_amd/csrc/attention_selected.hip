@@ -45,7 +45,7 @@ hipError_t launch_attention_selected(const SelectedProblem &p, void *ws, hipStre
         a.part_o = static_cast<float *>(ws);
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(ws) + selected_layout(r).part_ml);
     }
-    launch_tiles<kSelected>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, a.splits, st);
+    launch_tiles<kSelected>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, st);
     return hipGetLastError();
 }
 

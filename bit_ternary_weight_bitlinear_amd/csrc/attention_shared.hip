@@ -30,7 +30,7 @@ namespace bl {
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
-constexpr int kPrefixRows = 32, kPrefixWaves = 4;
+constexpr int kPrefixRows = 32;
 
 struct PrefixArgs {
     const void *q;
@@ -44,7 +44,10 @@ struct PrefixArgs {
     float *part_o, *part_ml;
 };
 
-// eight codes as fp16: 1024 + (code + 128) is the bits 0x6400 with the biased code in the low byte
+// Eight codes as fp16. EXACT: 1024 + (code + 128) is the bits 0x6400 with the biased code in
+// the low byte. Otherwise those alone, (code + 128) 2^-24: two instructions of five fewer for
+// four codes, and a product with them is 2^-24 (sum + 128 * the sum of the other factor).
+template <bool EXACT>
 __device__ inline v8h codes_f16(uint32_t lo, uint32_t hi)
 {
     union {
@@ -52,91 +55,150 @@ __device__ inline v8h codes_f16(uint32_t lo, uint32_t hi)
         v2h h[4];
         v8h v;
     } u;
+    constexpr uint32_t kTop = EXACT ? 0x64646464u : 0u;
     lo ^= 0x80808080u;
     hi ^= 0x80808080u;
-    u.w[0] = __builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u);
-    u.w[1] = __builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u);
-    u.w[2] = __builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u);
-    u.w[3] = __builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u);
+    u.w[0] = __builtin_amdgcn_perm(kTop, lo, 0x04010400u);
+    u.w[1] = __builtin_amdgcn_perm(kTop, lo, 0x04030402u);
+    u.w[2] = __builtin_amdgcn_perm(kTop, hi, 0x04010400u);
+    u.w[3] = __builtin_amdgcn_perm(kTop, hi, 0x04030402u);
     const v2h bias = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+    if constexpr (EXACT)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u.h[i] += bias;
+        for (int i = 0; i < 4; ++i) u.h[i] += bias;
     return u.v;
 }
 
+// the weights of a page's 64 tokens, register r of tile t being token 32 t + 16 half + r
+template <int PARTS>
+struct Weights {
+    v8h hi[2][2], lo[2][2];
+};
+
+// Weights from sums s of products (times f, less `off`: the logits, in powers of two) of the
+// `left` tokens that the page holds (none without a page, of whose stand-in nothing may enter).
+// Returns their reference exponent.
+template <int PARTS>
+__device__ inline float page_weights(v16f (&s)[2], float f, float off, int left, int half, Weights<PARTS> &w)
+{
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[t][r] = PARTS == 2 ? s[t][r] * f : __builtin_fmaf(s[t][r], f, off);
+    if (left < kBlock)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[t][r] = 32 * t + 16 * half + r < left ? s[t][r] : kNegInf;
+    float big = kNegInf;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) big = fmaxf(big, s[t][r]);
+    big = fmaxf(big, __shfl_xor(big, 32));
+    // raised by more than the rounding of its difference to 15, so that no weight passes 2^15
+    const float ref = left > 0 ? ceilf(__builtin_fmaf(fabsf(big), 0x1p-22f, big)) : kNegInf;
+    const float shift = left > 0 ? 15.0f - ref : 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float e = __builtin_amdgcn_exp2f(s[t][r] + shift);
+            const _Float16 e16 = (_Float16)e;
+            w.hi[t][r >> 3][r & 7] = e16;
+            if constexpr (PARTS == 2) w.lo[t][r >> 3][r & 7] = (_Float16)(e - (float)e16);
+        }
+    return ref;
+}
+
+// A query row as fp16, row r of an operand of 32: an eighth of it by thread c of eight. Returns
+// the row's factor (NaN where it is not finite) and the sum of its elements.
+template <typename T, int D, int PARTS>
+__device__ inline float2 query_row(const PrefixArgs &a, int64_t row, int head, int r, int c, _Float16 *qh)
+{
+    constexpr int E = D / 8, U = D / 32;
+    const bool there = row < a.rows;
+    const int64_t at = there ? row : 0, tok = at / a.group;
+    const int hq = head * a.group + (int)(at - tok * a.group);
+    const T *src = static_cast<const T *>(a.q) + tok * a.q_stride + (int64_t)hq * D + E * c;
+    T raw[E];
+#pragma unroll
+    for (int i = 0; i < (int)(E * sizeof(T) / 16); ++i) reinterpret_cast<uint4 *>(raw)[i] = reinterpret_cast<const uint4 *>(src)[i];
+    float x[E], big = 0.0f, bad = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        x[i] = there ? to_f32(raw[i]) : 0.0f;
+        if (!(fabsf(x[i]) <= 3.402823466e38f)) {
+            bad = 1.0f;
+            x[i] = 0.0f;
+        }
+        big = fmaxf(big, fabsf(x[i]));
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) {
+        big = fmaxf(big, __shfl_xor(big, d));
+        bad = fmaxf(bad, __shfl_xor(bad, d));
+    }
+    const int e = 14 - ((int)(__float_as_uint(fmaxf(big, 1e-30f)) >> 23) - 127);
+    float total = 0.0f;
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
+#pragma unroll
+    for (int g = 0; g < E / 8; ++g) {
+        const int piece = c * (E / 8) + g;  // of 8 dims: 32 * pair + 16 * half + 8 * s
+        _Float16 *dst = qh + (((piece >> 2) * 2 + (piece & 1)) * 64 + (piece >> 1 & 1) * 32 + r) * 8;
+        v8h hi, lo;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = x[8 * g + i] * up;
+            hi[i] = (_Float16)v;
+            lo[i] = (_Float16)(v - (float)hi[i]);
+            total += (float)hi[i];
+        }
+        *reinterpret_cast<v8h *>(dst) = hi;
+        if constexpr (PARTS == 2) *reinterpret_cast<v8h *>(dst + U * 2 * 64 * 8) = lo;
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) total += __shfl_xor(total, d);
+    return make_float2(bad > 0.0f ? __builtin_nanf("") : __uint_as_float((uint32_t)(127 - e) << 23) * fabsf(a.scale), total);
+}
+
+// A workgroup has 32 query rows of a kv head and part of the prefix, whose pages go to its
+// waves in turn.
+template <int D, int PARTS>
+struct PrefixLds {
+    static constexpr int stride = D + 4;                   // of a row in the join
+    static constexpr int query = PARTS * (D / 32) * 2 * 64;  // 16-byte pieces of the rows' operands
+    static constexpr int join = kPrefixWaves * kPrefixRows * stride * 4;
+    static constexpr int bytes = query * 16 > join ? query * 16 : join;
+};
+
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kPrefixWaves) void attention_prefix_kernel(PrefixArgs a, int first_tile)
+__device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, int head, int split, char *lds, float2 *row_scale,
+                                             float2 (*jm)[kPrefixRows])
 {
     constexpr int W = kPrefixWaves, R = kPrefixRows;
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
-    constexpr int U = D / 32;      // pairs of 16-dim pieces of K; 32-dim tiles of the output
-    constexpr int E = D / 8;       // elements of a query row per thread
-    constexpr int kStride = D + 4;  // of a row in the join
-    constexpr int kQueryHalfs = PARTS * U * 2 * 64 * 8, kJoinFloats = W * R * kStride;
-    __shared__ __align__(16) char lds[kQueryHalfs * 2 > kJoinFloats * 4 ? kQueryHalfs * 2 : kJoinFloats * 4];
-    __shared__ float row_scale[R];
-    __shared__ float2 jm[W][R];
-    _Float16 *qh = reinterpret_cast<_Float16 *>(lds);  // [part][2 * pair + s][lane][8], in operand order
+    constexpr bool EXACT = PARTS == 2;
+    constexpr int U = D / 32;  // pairs of 16-dim pieces of K; 32-dim tiles of the output
+    constexpr int kStride = PrefixLds<D, PARTS>::stride;
+    v8h *qh = reinterpret_cast<v8h *>(lds);  // [part][2 * pair + s][lane], in operand order
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, col = lane & 31;
-    const int head = blockIdx.y, split = blockIdx.x;
-    const int64_t row0 = ((int64_t)first_tile + blockIdx.z) * R;
+    const int64_t row0 = tile * R;
     const int len = *a.len, npages = prefix_pages(a.len, a.blocks);
-    const int chunk = pages_per_split(npages, a.splits, W);
+    const int chunk = prefix_chunk(npages, a.splits);
     const int p0 = split * chunk, p1 = p0 + chunk < npages ? p0 + chunk : npages;
     if (p0 >= npages) return;  // the join knows
 
-    // ---- query rows as fp16, eight threads a row
     {
-        const int r = tid >> 3, c = tid & 7;
-        const bool there = row0 + r < a.rows;
-        const int64_t row = there ? row0 + r : 0;
-        const int64_t tok = row / a.group;
-        const int hq = head * a.group + (int)(row - tok * a.group);
-        const T *src = static_cast<const T *>(a.q) + tok * a.q_stride + (int64_t)hq * D + E * c;
-        T raw[E];
-#pragma unroll
-        for (int i = 0; i < (int)(E * sizeof(T) / 16); ++i) reinterpret_cast<uint4 *>(raw)[i] = reinterpret_cast<const uint4 *>(src)[i];
-        float x[E], big = 0.0f, bad = 0.0f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            x[i] = there ? to_f32(raw[i]) : 0.0f;
-            if (!(fabsf(x[i]) <= 3.402823466e38f)) {
-                bad = 1.0f;
-                x[i] = 0.0f;
-            }
-            big = fmaxf(big, fabsf(x[i]));
-        }
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) {
-            big = fmaxf(big, __shfl_xor(big, d));
-            bad = fmaxf(bad, __shfl_xor(bad, d));
-        }
-        const int e = 14 - ((int)(__float_as_uint(fmaxf(big, 1e-30f)) >> 23) - 127);
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
-#pragma unroll
-        for (int g = 0; g < E / 8; ++g) {
-            const int piece = c * (E / 8) + g;  // of 8 dims: 32 * pair + 16 * half + 8 * s
-            _Float16 *dst = qh + (((piece >> 2) * 2 + (piece & 1)) * 64 + (piece >> 1 & 1) * 32 + r) * 8;
-            v8h hi, lo;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = x[8 * g + i] * up;
-                hi[i] = (_Float16)v;
-                lo[i] = (_Float16)(v - (float)hi[i]);
-            }
-            *reinterpret_cast<v8h *>(dst) = hi;
-            if constexpr (PARTS == 2) *reinterpret_cast<v8h *>(dst + U * 2 * 64 * 8) = lo;
-        }
-        if (c == 0) row_scale[r] = bad > 0.0f ? __builtin_nanf("") : __uint_as_float((uint32_t)(127 - e) << 23) * fabsf(a.scale);
+        const float2 f = query_row<T, D, PARTS>(a, row0 + (tid >> 3), head, tid >> 3, tid & 7, reinterpret_cast<_Float16 *>(qh));
+        if ((tid & 7) == 0) row_scale[tid >> 3] = f;
     }
     __syncthreads();
-    const float qs_raw = row_scale[col];
-    const bool poor = !(qs_raw == qs_raw);
-    const float qs = poor ? 0.0f : qs_raw;
-
-    float top = kNegInf, sum = 0.0f;
+    const bool poor = !(row_scale[col].x == row_scale[col].x);
+    const float qs = poor ? 0.0f : row_scale[col].x, qsum = row_scale[col].y;
+    float top = kNegInf, sum = 0.0f, bias = 0.0f;  // bias: what the biased codes of V added to acc
     v16f acc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -147,29 +209,40 @@ __global__ __launch_bounds__(64 * kPrefixWaves) void attention_prefix_kernel(Pre
     const int token = 16 * (col >> 2 & 1) + 8 * (col >> 4) + 4 * (col >> 3 & 1) + (col & 3);
     const int k_at = k_code_at<D>(token, 16 * half);
     const int v_at = v_code_at(16 * half, col);
+    v8h ones;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ones[i] = (_Float16)1.0f;
 
+    uint4 kf[2][U];
     for (int base = p0 + wave; base < p1; base += 64 * W) {
         const int mine = base + W * lane;
         const int ids = mine < p1 ? a.table[mine] : -1;
         const bool ok = ids >= 0 && ids < a.pages;
-        const int64_t my_at = ok ? (int64_t)ids * a.kv_heads + head : 0;
-        const float my_ks = ok ? a.k_scale[my_at] : 0.0f, my_vs = ok ? a.v_scale[my_at] : 0.0f;
-        for (int p = base, i = 0; p < p1 && i < 64; p += W, ++i) {
-            const int id = __builtin_amdgcn_readlane(ids, i);
-            if (id < 0 || id >= a.pages) continue;  // a block without a page holds no tokens
-            const int64_t at = ((int64_t)id * a.kv_heads + head) * (kBlock * D);
-            const int8_t *kp = a.k_codes + at + k_at, *vp = a.v_codes + at + v_at;
-            uint4 kf[2][U], vf[U][2];
+        const int page = ok ? ids : 0;  // a block without a page reads page 0
+        const int64_t my_at = (int64_t)page * a.kv_heads + head;
+        const float my_ks = ok ? a.k_scale[my_at] / 127.0f : 0.0f, my_vs = ok ? a.v_scale[my_at] / 127.0f : 0.0f;
+        auto load_k = [&](int i) {
+            const int id = __builtin_amdgcn_readlane(page, i);
+            const int8_t *kp = a.k_codes + ((int64_t)id * a.kv_heads + head) * (kBlock * D) + k_at;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int u = 0; u < U; ++u) kf[t][u] = *reinterpret_cast<const uint4 *>(kp + t * 8 * 16 + u * 2 * 256);
+        };
+        // K of a page is asked for when the one before has met the queries, V of a page before its K does
+        load_k(0);
+        for (int p = base, i = 0; p < p1 && i < 64; p += W, ++i) {
+            const int id = __builtin_amdgcn_readlane(page, i);
+            const int8_t *vp = a.v_codes + ((int64_t)id * a.kv_heads + head) * (kBlock * D) + v_at;
+            uint4 vf[U][2];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) vf[u][t] = *reinterpret_cast<const uint4 *>(vp + (u * 2 * 4 + t * 2) * 256);
-            const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_ks), i)) / 127.0f;
-            const float vs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_vs), i)) / 127.0f;
+            const bool there = __builtin_amdgcn_readlane((int)ok, i) != 0;
+            const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_ks), i));
+            const float vs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_vs), i));
+            const int left = there ? len - p * kBlock : 0;
 
             v16f s[2];
 #pragma unroll
@@ -177,59 +250,50 @@ __global__ __launch_bounds__(64 * kPrefixWaves) void attention_prefix_kernel(Pre
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U * 2; ++u) {
+                const v8h q0 = qh[u * 64 + lane];
+                v8h q1;
+                if constexpr (PARTS == 2) q1 = qh[(U * 2 + u) * 64 + lane];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const v8h q0 = *reinterpret_cast<const v8h *>(qh + ((u * 2 + b) * 64 + lane) * 8);
-                    v8h q1;
-                    if constexpr (PARTS == 2) q1 = *reinterpret_cast<const v8h *>(qh + ((U * 2 + u * 2 + b) * 64 + lane) * 8);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const v8h k8 = b ? codes_f16(kf[t][u].z, kf[t][u].w) : codes_f16(kf[t][u].x, kf[t][u].y);
-                        if constexpr (PARTS == 2) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q1, s[t], 0, 0, 0);
-                        s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q0, s[t], 0, 0, 0);
-                    }
+                for (int t = 0; t < 2; ++t) {
+                    const uint4 c = kf[t][u >> 1];
+                    const v8h k8 = u & 1 ? codes_f16<EXACT>(c.z, c.w) : codes_f16<EXACT>(c.x, c.y);
+                    if constexpr (PARTS == 2) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q1, s[t], 0, 0, 0);
+                    s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q0, s[t], 0, 0, 0);
                 }
-
-            // register r of tile t is token 32 t + 16 half + r
-            const float f = qs * ks;  // not negative: the sign of the scale is in q
-            const int left = len - p * kBlock;
-            float big = kNegInf;
-            if (left >= kBlock) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) big = fmaxf(big, s[t][r]);
-            } else {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (32 * t + 16 * half + r < left) big = fmaxf(big, s[t][r]);
             }
-            big = fmaxf(big, __shfl_xor(big, 32));
-            // raised by more than the rounding of its difference to 15, so that no weight passes 2^15
-            const float ref = ceilf(__builtin_fmaf(fabsf(big * f), 0x1p-22f, big * f)), shift = 15.0f - ref;
-            float total = 0.0f;
-            v8h ph[2][2], pl[2][2];
+            if (p + W < p1 && i < 63) load_k(i + 1);
+
+            Weights<PARTS> w;
+            const float f = qs * ks;
+            const float ref = page_weights<PARTS>(s, EXACT ? f : f * 0x1p24f, -128.0f * qsum * f, left, half, w);
+            const float now = fmaxf(top, ref), to = now == kNegInf ? 0.0f : now;
+            const float add = __builtin_amdgcn_exp2f(ref - to) * 0x1p-15f, g = add * vs;  // of the page's weights and sums
+            if (__any(now != top)) {
+                asm volatile("");  // a branch, not 64 products and a choice
+                const float keep = __builtin_amdgcn_exp2f(top - to);
+                sum *= keep;
+                bias *= keep;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[u][r] *= keep;
+            }
+            top = now;
+            auto product = [&](const v8h &c, int t, int b, v16f o) {
+                if constexpr (PARTS == 2) o = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, w.lo[t][b], o, 0, 0, 0);
+                return __builtin_amdgcn_mfma_f32_32x32x16_f16(c, w.hi[t][b], o, 0, 0, 0);
+            };
+            // the weights' sum as they are after rounding: every register the same
+            v16f all;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) all[r] = 0.0f;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], f, shift));
-                    if (left < kBlock && 32 * t + 16 * half + r >= left) w = 0.0f;
-                    total += w;
-                    const _Float16 w16 = (_Float16)w;
-                    ph[t][r >> 3][r & 7] = w16;
-                    if constexpr (PARTS == 2) pl[t][r >> 3][r & 7] = (_Float16)(w - (float)w16);
-                }
-            total += __shfl_xor(total, 32);
-            const float now = fmaxf(top, ref);
-            const float keep = __builtin_amdgcn_exp2f(top - now), add = __builtin_amdgcn_exp2f(ref - now) * 0x1p-15f;
-            top = now;
-            sum = __builtin_fmaf(sum, keep, total * add);
-            const float g = add * vs;
-            const bool same = !__any(keep != 1.0f);
+                for (int b = 0; b < 2; ++b) all = product(ones, t, b, all);
+            sum = __builtin_fmaf(all[0], add, sum);
+            if (!EXACT) bias = __builtin_fmaf(all[0], g, bias);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 v16f o;
@@ -238,18 +302,10 @@ __global__ __launch_bounds__(64 * kPrefixWaves) void attention_prefix_kernel(Pre
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const v8h v8 = b ? codes_f16(vf[u][t].z, vf[u][t].w) : codes_f16(vf[u][t].x, vf[u][t].y);
-                        if constexpr (PARTS == 2) o = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, pl[t][b], o, 0, 0, 0);
-                        o = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, ph[t][b], o, 0, 0, 0);
-                    }
-                if (same) {
+                    for (int b = 0; b < 2; ++b)
+                        o = product(b ? codes_f16<EXACT>(vf[u][t].z, vf[u][t].w) : codes_f16<EXACT>(vf[u][t].x, vf[u][t].y), t, b, o);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[u][r] = __builtin_fmaf(o[r], g, acc[u][r]);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[u][r] = __builtin_fmaf(o[r], g, acc[u][r] * keep);
-                }
+                for (int r = 0; r < 16; ++r) acc[u][r] = __builtin_fmaf(o[r], g, acc[u][r]);
             }
         }
     }
@@ -257,12 +313,16 @@ __global__ __launch_bounds__(64 * kPrefixWaves) void attention_prefix_kernel(Pre
     // ---- join the waves, in wave order
     __syncthreads();
     float *jo = reinterpret_cast<float *>(lds);  // [wave][row][kStride]
+    const float less = 128.0f * bias;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-            *reinterpret_cast<v4f *>(jo + (wave * R + col) * kStride + 32 * u + 2 * r + 4 * half) =
-                v4f{acc[u][r], acc[u][r + 1], acc[u][r + 2], acc[u][r + 3]};
+        for (int r = 0; r < 16; r += 4) {
+            v4f o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = EXACT ? acc[u][r + i] : __builtin_fmaf(acc[u][r + i], 0x1p24f, -less);
+            *reinterpret_cast<v4f *>(jo + (wave * R + col) * kStride + 32 * u + 2 * r + 4 * half) = o;
+        }
     if (half == 0) jm[wave][col] = make_float2(top, poor ? __builtin_nanf("") : sum);
     __syncthreads();
     for (int it = tid; it < R * (D / 4); it += 64 * W) {
@@ -289,16 +349,44 @@ __global__ __launch_bounds__(64 * kPrefixWaves) void attention_prefix_kernel(Pre
     }
 }
 
+// The prefix's workgroups first, which take longest, then the sequences' own pages: the one
+// waits for arithmetic, the other for memory.
+template <typename T, int D, int RT>
+__global__ __launch_bounds__(64 * kPrefixWaves, 2) void attention_shared_kernel(PrefixArgs f, CachedArgs a, int64_t prefix_groups, int64_t first)
+{
+    constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
+    constexpr int kOwnBytes = CachedLds<D, RT, kPrefixWaves>::words * 4, kPrefixBytes = PrefixLds<D, PARTS>::bytes;
+    __shared__ __align__(16) char lds[kPrefixBytes > kOwnBytes ? kPrefixBytes : kOwnBytes];
+    __shared__ float2 row_scale[kPrefixRows], jm[kPrefixWaves][kPrefixRows];
+    int64_t group = first + blockIdx.x;
+    if (group < prefix_groups) {
+        const int64_t unit = group / f.splits;
+        attention_prefix_tile<T, D>(f, unit / f.kv_heads, (int)(unit % f.kv_heads), (int)(group - unit * f.splits), lds, row_scale, jm);
+        return;
+    }
+    group -= prefix_groups;
+    const int64_t unit = group / a.splits;
+    attention_cached_tile<T, D, RT, kPrefixWaves, false, kBehindPrefix>(a, (int)(unit / a.kv_heads), (int)(unit % a.kv_heads),
+                                                                       (int)(group - unit * a.splits), reinterpret_cast<uint32_t *>(lds),
+                                                                       reinterpret_cast<float *>(row_scale));
+}
+
 // ---------------------------------------------------------------- launcher
 
-// Workgroups per tile of 32 rows and kv head: two per CU in all, but at least a page per wave
+// Workgroups per unit, a tile of rows and a kv head: of the prefix, and of the sequences' own
+// pages, each about one per CU in all and with a page per wave at least
+static int64_t splits_of(int64_t units, int64_t blocks, int64_t target)
+{
+    const int64_t most = ceil_div(blocks, kPrefixWaves), s = target / units < most ? target / units : most;
+    return s < 1 ? 1 : s > 256 ? 256 : s;
+}
 static int64_t prefix_splits(const SharedProblem &p)
 {
-    const int64_t units = ceil_div(p.c.m * (p.c.q_heads / p.c.kv_heads), kPrefixRows) * p.c.kv_heads;
-    const int64_t most = ceil_div(p.prefix_blocks, kPrefixWaves);
-    int64_t s = 512 / units;
-    s = s > most ? most : s;
-    return s < 1 ? 1 : s > 256 ? 256 : s;
+    return splits_of(ceil_div(p.c.m * (p.c.q_heads / p.c.kv_heads), kPrefixRows) * p.c.kv_heads, p.prefix_blocks, 256);
+}
+static int64_t own_splits(const CachedProblem &c)
+{
+    return splits_of(units_of(c, row_tiles(c)), c.max_blocks, 512);
 }
 
 struct SharedLayout {
@@ -306,12 +394,12 @@ struct SharedLayout {
 };
 static SharedLayout shared_layout(const SharedProblem &p)
 {
-    const int64_t splits = launch_shape(p.c, row_tiles(p.c)).splits, before = prefix_splits(p), rows = p.c.m * p.c.q_heads;
+    const int64_t rows = p.c.m * p.c.q_heads, before = prefix_splits(p) * rows, own = own_splits(p.c) * rows;
     SharedLayout L{};
-    L.part_ml = round_up(before * rows * p.c.head_dim * 4, 256);
-    L.own_o = L.part_ml + round_up(before * rows * 8, 256);
-    L.own_ml = L.own_o + (splits > 1 ? round_up(splits * rows * p.c.head_dim * 4, 256) : 0);
-    L.bytes = L.own_ml + (splits > 1 ? round_up(splits * rows * 8, 256) : 0);
+    L.part_ml = round_up(before * p.c.head_dim * 4, 256);
+    L.own_o = L.part_ml + round_up(before * 8, 256);
+    L.own_ml = L.own_o + round_up(own * p.c.head_dim * 4, 256);
+    L.bytes = L.own_ml + round_up(own * 8, 256);
     return L;
 }
 
@@ -321,7 +409,6 @@ hipError_t launch_attention_shared(const SharedProblem &p, void *ws, hipStream_t
 {
     const CachedProblem &c = p.c;
     const int rt = row_tiles(c);
-    const Shape shape = launch_shape(c, rt);
     const SharedLayout L = shared_layout(p);
     char *base = static_cast<char *>(ws);
     PrefixArgs f{};
@@ -331,24 +418,26 @@ hipError_t launch_attention_shared(const SharedProblem &p, void *ws, hipStream_t
     f.k_codes = c.k_codes; f.v_codes = c.v_codes; f.k_scale = c.k_scale; f.v_scale = c.v_scale; f.scale = c.scale * kLog2e;
     f.part_o = reinterpret_cast<float *>(base);
     f.part_ml = reinterpret_cast<float *>(base + L.part_ml);
-    in_launches(ceil_div(f.rows, kPrefixRows), [&](int first, unsigned n) {
-        const dim3 grid((unsigned)f.splits, (unsigned)c.kv_heads, n), threads(64 * kPrefixWaves);
-        auto go = [&](auto type) {
-            using T = decltype(type);
-            if (c.head_dim == 128) hipLaunchKernelGGL((attention_prefix_kernel<T, 128>), grid, threads, 0, st, f, first);
-            else hipLaunchKernelGGL((attention_prefix_kernel<T, 64>), grid, threads, 0, st, f, first);
-        };
-        c.bf16 ? go(bf16_t{}) : go(float{});
-    }, kMostInZ);
-
-    CachedArgs a = cached_args(c, shape, rt);
+    CachedArgs a = cached_args(c, Shape{kPrefixWaves, own_splits(c)}, rt);
     a.prefix_o = f.part_o; a.prefix_ml = f.part_ml; a.prefix_len = p.prefix_len; a.prefix_blocks = p.prefix_blocks;
-    a.prefix_splits = f.splits; a.prefix_waves = kPrefixWaves;
-    if (a.splits > 1) {
-        a.part_o = reinterpret_cast<float *>(base + L.own_o);
-        a.part_ml = reinterpret_cast<float *>(base + L.own_ml);
-    }
-    launch_tiles<kBehindPrefix>(c, a, shape, rt, query_tiles(c, rt), a.splits + f.splits, st);
+    a.prefix_splits = f.splits;
+    a.part_o = reinterpret_cast<float *>(base + L.own_o);
+    a.part_ml = reinterpret_cast<float *>(base + L.own_ml);
+    const int64_t prefix_groups = ceil_div(f.rows, kPrefixRows) * c.kv_heads * f.splits;
+    const int64_t groups = prefix_groups + query_tiles(c, rt) * c.kv_heads * a.splits;
+    auto go = [&](auto type, auto width) {
+        using T = decltype(type);
+        constexpr int D = decltype(width)::value;
+        for (int64_t first = 0; first < groups; first += kMostGroups) {
+            const dim3 grid((unsigned)(groups - first < kMostGroups ? groups - first : kMostGroups)), threads(64 * kPrefixWaves);
+            if (rt == 1) hipLaunchKernelGGL((attention_shared_kernel<T, D, 1>), grid, threads, 0, st, f, a, prefix_groups, first);
+            else if (rt == 2) hipLaunchKernelGGL((attention_shared_kernel<T, D, 2>), grid, threads, 0, st, f, a, prefix_groups, first);
+            else hipLaunchKernelGGL((attention_shared_kernel<T, D, 4>), grid, threads, 0, st, f, a, prefix_groups, first);
+        }
+        launch_join<kBehindPrefix, T, D>(c, a, a.splits + f.splits, st);
+    };
+    if (c.bf16) c.head_dim == 128 ? go(bf16_t{}, Width<128>{}) : go(bf16_t{}, Width<64>{});
+    else c.head_dim == 128 ? go(float{}, Width<128>{}) : go(float{}, Width<64>{});
     return hipGetLastError();
 }
 
