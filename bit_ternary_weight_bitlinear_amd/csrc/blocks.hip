@@ -102,7 +102,7 @@ struct SelectArgs {
     const void *q;
     int64_t q_stride, m;
     const int32_t *cu, *lens, *table;
-    int seqs, q_heads, kv_heads, group, splits;
+    int seqs, q_heads, kv_heads, group;
     int64_t max_blocks, pages, keep, first, recent;
     const int8_t *bounds;
     const float *k_scale;
@@ -110,214 +110,376 @@ struct SelectArgs {
     uint32_t *keys;  // [m][kv_heads][max_blocks], where a workgroup's LDS does not hold them
 };
 
-constexpr int kSelectThreads = 512;
 constexpr int kKeysInLds = 8192;
+constexpr float kLargest = 3.402823466e38f;
 
-// The sums of the group's positive and negative parts as a lane's digits of 7 bits: lanes
-// 0 .. D/16-1 of a 16-byte piece's 2 * D/16 lanes have P, the others -N. `lds`: D words.
-template <typename T, int D>
-__device__ inline void query_digits(const SelectArgs &a, int64_t row, int head, uint32_t *lds, float *red, v4i &lo, v4i &hi)
-{
-    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 63, n = a.group * D;
-    const T *src = static_cast<const T *>(a.q) + row * a.q_stride + (int64_t)head * n;  // a kv head's query heads are adjacent
-    constexpr float kMost = 3.402823466e38f;
-    auto value = [&](int i) {  // NaN counts as 0 and infinities as the largest finite number
-        const float v = to_f32(src[i]);
-        return v == v ? fminf(fmaxf(v, -kMost), kMost) : 0.0f;
-    };
-    float big = 0.0f;
-    for (int i = tid; i < n; i += threads) big = fmaxf(big, fabsf(value(i)));
-    big = wave_max(big);
-    if (lane == 0) red[tid >> 6] = big;
-    __syncthreads();
-    for (int w = 0; w < threads / 64; ++w) big = fmaxf(big, red[w]);
-    const float inv = 127.0f / fmaxf(big, 1e-30f);
-    for (int d = tid; d < D; d += threads) {
-        int p = 0, q = 0;
-        for (int h = 0; h < a.group; ++h) {
-            const int c = (int)rintf(value(h * D + d) * inv);
-            p += c > 0 ? c : 0;
-            q += c < 0 ? -c : 0;
-        }
-        lds[d] = (uint32_t)p | (uint32_t)q << 16;  // at most 127 * 128
-    }
-    __syncthreads();
-    const int at = lane % (D / 8), dim = at % (D / 16) * 16, down = at < D / 16 ? 0 : 16;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        uint32_t l = 0, h = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t v = lds[dim + 4 * w + i] >> down & 0xFFFFu;
-            l |= (v & 127u) << (8 * i);
-            h |= (v >> 7) << (8 * i);
-        }
-        lo[w] = (int)l;
-        hi[w] = (int)h;
-    }
-}
+// The sums of the group's positive and negative parts, as a lane's digits of 7 bits and a sign: of
+// the 2 * D / 16 lanes that have a block's bounds the first half has P, the other N. Every element
+// is looked at twice, for the largest and then for its integer, with the largest on the way
+// through LDS between. `sums`: D words, zero at the start; at most 127 * 128 in either half.
+template <typename T, int D, int THREADS>
+struct QueryDigits {
+    static constexpr int E = 16 / sizeof(T), KEEP = 2;  // elements of a piece; pieces kept in registers
+    T raw[KEEP][E];
+    const T *src;
+    int pieces;
 
-// Keys of blocks b0 .. b0+63 of a sequence, one per lane: their scores in order, as the
-// weights of an eviction are. D/8 lanes have a block's bounds, so a wave's load is 64 / (D/8)
-// blocks.
-template <int D>
-__device__ inline uint32_t block_keys(const SelectArgs &a, const int32_t *table, int head, int b0, int used, const v4i &lo, const v4i &hi)
-{
-    constexpr int L = D / 8, B = 64 / L;  // lanes of a block, blocks of a load
-    const int lane = threadIdx.x & 63, mine = b0 + lane;
-    const int id = mine < used ? table[mine] : -1;
-    const bool ok = id >= 0 && id < a.pages;
-    const int64_t my_at = ok ? (int64_t)id * a.kv_heads + head : 0;
-    const float scale = ok ? a.k_scale[my_at] : 0.0f;
-    const int page = ok ? id : 0;
-    int sum = 0;
-#pragma unroll 8
-    for (int i = 0; i < 64 / B; ++i) {
-        const int64_t at = (int64_t)__shfl(page, i * B + lane / L) * a.kv_heads + head;
-        const v4i c = *reinterpret_cast<const v4i *>(a.bounds + at * (2 * D) + lane % L * 16);
-        int l = 0, h = 0;
+    __device__ void load(const SelectArgs &a, int64_t row, int head)
+    {
+        pieces = a.group * D / E;
+        src = static_cast<const T *>(a.q) + row * a.q_stride + (int64_t)head * a.group * D;  // a kv head's query heads are adjacent
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if ((int)threadIdx.x + k * THREADS < pieces)
+                *reinterpret_cast<uint4 *>(raw[k]) = reinterpret_cast<const uint4 *>(src)[threadIdx.x + k * THREADS];
+    }
+    // f(piece, elements) for every piece of this thread
+    template <typename F>
+    __device__ void each(F f)
+    {
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if ((int)threadIdx.x + k * THREADS < pieces) f((int)threadIdx.x + k * THREADS, raw[k]);
+        for (int i = threadIdx.x + KEEP * THREADS; i < pieces; i += THREADS) {
+            T more[E];
+            *reinterpret_cast<uint4 *>(more) = reinterpret_cast<const uint4 *>(src)[i];
+            f(i, more);
+        }
+    }
+    // NaN counts as 0 and infinities as the largest finite number
+    static __device__ float value(T x)
+    {
+        const float v = to_f32(x);
+        return v == v ? fminf(fmaxf(v, -kLargest), kLargest) : 0.0f;
+    }
+    __device__ float largest()
+    {
+        float big = 0.0f;
+        each([&](int, const T *x) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(value(x[i])));
+        });
+        return wave_max(big);
+    }
+    __device__ void add(float big, uint32_t *sums)
+    {
+        const float inv = 127.0f / fmaxf(big, 1e-30f);
+        each([&](int piece, const T *x) {
+            const int dim = piece * E % D;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int c = (int)rintf(value(x[i]) * inv);
+                atomicAdd(&sums[dim + i], c < 0 ? (uint32_t)-c << 16 : (uint32_t)c);
+            }
+        });
+    }
+    static __device__ void digits(const uint32_t *sums, v4i &lo, v4i &hi)
+    {
+        const int at = (threadIdx.x & 63) % (D / 8), dim = at % (D / 16) * 16, down = at < D / 16 ? 0 : 16;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            l = __builtin_amdgcn_sdot4(c[w], lo[w], l, false);
-            h = __builtin_amdgcn_sdot4(c[w], hi[w], h, false);
-        }
-        int v = l + (h << 7);
-        if (lane % L >= L / 2) v = -v;  // low_d N_d, by -N
-        if constexpr (L == 16) v = row16_sum(v);
-        else v = group8_sum(v);
-        const int got = __shfl(v, lane % B * L);
-        if (lane / B == i) sum = got;
-    }
-    return ok ? weight_key((float)sum * scale) : weight_key(kNegInf);
-}
-
-// The blocks that stay of those at mid0 .. mid1-1, `want` of them: every key above `prefix`
-// (without its lowest `shift` bits) and the first `left` that equal it. By digits from the
-// top, until a digit's count is what is left to keep.
-struct Cut {
-    uint32_t prefix;
-    int shift, left;
-};
-template <int THREADS>
-__device__ inline Cut find_cut(const uint32_t *keys, int mid0, int mid1, int want, int *hist, int *wave_sums, int *pick)
-{
-    constexpr int W = THREADS / 64, kBins = 2048, PER = kBins / THREADS;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    Cut r{0, 32, want};
-    while (want > 0 && r.shift > 0) {
-        const int bits = r.shift > 10 ? 11 : 10, down = r.shift - bits;
+            const uint4 v = *reinterpret_cast<const uint4 *>(sums + dim + 4 * w);
+            const uint32_t x[4] = {v.x >> down & 0xFFFFu, v.y >> down & 0xFFFFu, v.z >> down & 0xFFFFu, v.w >> down & 0xFFFFu};
+            uint32_t l = 0, h = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) hist[tid + i * THREADS] = 0;
-        __syncthreads();
-        for (int b = mid0 + tid; b < mid1; b += THREADS) {
-            const uint32_t key = keys[b];
-            if (r.shift == 32 || key >> r.shift == r.prefix) atomicAdd(&hist[key >> down & ((1u << bits) - 1)], 1);
-        }
-        __syncthreads();
-        // thread i has the i-th largest PER digits; what lies above them
-        const int top = (1 << bits) - 1 - PER * tid;
-        int h[PER], mine = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            h[i] = top - i >= 0 ? hist[top - i] : 0;
-            mine += h[i];
-        }
-        int incl = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(incl, d);
-            if (lane >= d) incl += o;
-        }
-        if (lane == 63) wave_sums[wave] = incl;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-            if (w < wave) incl += wave_sums[w];
-        int above = incl - mine;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (above < r.left && above + h[i] >= r.left) {
-                pick[0] = top - i;
-                pick[1] = r.left - above;
-                pick[2] = h[i];
+            for (int i = 0; i < 4; ++i) {
+                const int v = at < D / 16 ? (int)x[i] : -(int)x[i];
+                l |= (uint32_t)(v % 128 & 0xFF) << (8 * i);
+                h |= (uint32_t)(v / 128 & 0xFF) << (8 * i);
             }
-            above += h[i];
+            lo[w] = (int)l;
+            hi[w] = (int)h;
         }
-        __syncthreads();
-        r.prefix = r.prefix << bits | (uint32_t)pick[0];
-        r.left = pick[1];
-        r.shift = down;
-        if (pick[2] == r.left) break;  // all of them stay
-        __syncthreads();
     }
-    return r;
+};
+
+// Bounds of 64 blocks of a sequence: D / 8 lanes have one block's, so a wave's load holds
+// B = 64 / (D / 8) blocks. After the products a lane has the sum of its block alone: in a
+// step of the reduction a lane keeps one of two loads' sums, by a bit of its number, and gets
+// the other lane's share of it. Its block is `place` of the 64.
+template <int D>
+struct BlockBounds {
+    static constexpr int L = D / 8, B = 64 / L;  // L loads
+    v4i c[L];
+    float scale;
+    bool ok;
+
+    // The steps' partners are mirrored rows, halves of rows and pairs in quads, in this order, so
+    // that a partner differs in bits that have not been used yet: bits 3 (or 2) to 0 of the
+    // lane, the first of them the lowest of its load's number
+    static constexpr __host__ __device__ int reversed(int i)
+    {
+        return L == 16 ? (i & 1) << 3 | (i & 2) << 1 | (i & 4) >> 1 | (i & 8) >> 3 : (i & 1) << 2 | (i & 2) | (i & 4) >> 2;
+    }
+    static __device__ int place() { return reversed((int)threadIdx.x & (L - 1)) * B + ((int)threadIdx.x & 63) / L; }
+
+    // id: of the lane's block
+    __device__ void load(const SelectArgs &a, int id, int head)
+    {
+        const int lane = threadIdx.x & 63;
+        ok = id >= 0 && id < a.pages;
+        const int page = ok ? id : 0;  // a block without a page reads page 0
+        const int8_t *src = a.bounds + lane % L * 16;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            // the lane whose block is i * B + lane / L
+            const int64_t at = (int64_t)__shfl(page, lane / L * L + reversed(i)) * a.kv_heads + head;
+            c[i] = *reinterpret_cast<const v4i *>(src + at * (2 * D));
+        }
+        scale = a.k_scale[(int64_t)page * a.kv_heads + head];
+    }
+    template <int CTRL, int N>
+    static __device__ void halve(int (&v)[L], int bit)
+    {
+        const bool odd = threadIdx.x >> bit & 1;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const int stays = odd ? v[2 * i + 1] : v[2 * i], goes = odd ? v[2 * i] : v[2 * i + 1];
+            v[i] = stays + dpp_mov<CTRL>(goes);
+        }
+    }
+    // the key of the lane's block: its score in order, as the weights of an eviction are
+    __device__ uint32_t key(const v4i &lo, const v4i &hi) const
+    {
+        int v[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            int l = 0, h = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                l = __builtin_amdgcn_sdot4(c[i][w], lo[w], l, false);
+                h = __builtin_amdgcn_sdot4(c[i][w], hi[w], h, false);
+            }
+            v[i] = l + (h << 7);
+        }
+        if constexpr (L == 16) halve<kDppRowMirror, 16>(v, 3);
+        halve<kDppRowHalfMirror, 8>(v, 2);
+        halve<kDppQuadXor2, 4>(v, 1);
+        halve<kDppQuadXor1, 2>(v, 0);
+        return ok ? weight_key((float)v[0] * scale) : weight_key(kNegInf);
+    }
+};
+
+// What a row and kv head choose from
+struct Choice {
+    int used, mid0, mid1, want;  // blocks; those that a score decides on, and how many of them stay
+
+    __device__ Choice(const SelectArgs &a, int64_t have, int place)
+    {
+        const int64_t blocks = (have + place) / kBlock + 1;
+        used = blocks < a.max_blocks ? (int)blocks : (int)a.max_blocks;
+        const bool all = used <= a.keep;
+        mid0 = all ? used : (int)a.first;
+        mid1 = all ? used : (int)(used - a.recent);
+        want = all ? 0 : (int)(a.keep - a.first - a.recent);
+    }
+};
+
+__device__ inline uint32_t wave_max_u32(uint32_t v)
+{
+    auto up = [&](int o) { v = (uint32_t)o > v ? (uint32_t)o : v; };
+    up(dpp_mov<kDppQuadXor1>((int)v));
+    up(dpp_mov<kDppQuadXor2>((int)v));
+    up(dpp_mov<kDppRowHalfMirror>((int)v));
+    up(dpp_mov<kDppRowMirror>((int)v));
+    up(__builtin_amdgcn_update_dpp((int)v, (int)v, kDppRowBcast15, 0xA, 0xF, false));
+    up(__builtin_amdgcn_update_dpp((int)v, (int)v, kDppRowBcast31, 0xC, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// One workgroup per (row, kv head): the keys of its blocks into LDS (or, of tables too
-// wide for it, into the workspace), the cut, and the list in block order.
-template <typename T, int D, bool LDS>
-__global__ __launch_bounds__(kSelectThreads) void block_select_kernel(SelectArgs a, int first_row)
+// LDS of choose(): three histograms, zero at the start
+template <int THREADS>
+struct ChooseLds {
+    __align__(16) int hist[3][kDigitBins];
+    uint32_t ends[2][THREADS / 64];
+    int sums[2][2][THREADS / 64];
+};
+
+// The list of a row and kv head, in block order, from its blocks' keys: the `want` largest of
+// those at mid0 .. mid1-1, of equals the lower blocks, and everything outside. The least that
+// stays is found by digits of 11 bits from the highest in which the keys differ (their sign,
+// exponent and first bits are mostly the same, and counts of one digit stand in line), until
+// a digit's count is what is left to keep. low, high: the wave's least and largest key of
+// the middle. The keys, and the histograms' zeros, are behind the caller's writes, not yet behind a barrier.
+template <int THREADS>
+__device__ inline void choose(const SelectArgs &a, const Choice &ch, const uint32_t *keys, uint32_t low, uint32_t high, int32_t *out,
+                              ChooseLds<THREADS> &lds)
 {
-    constexpr int THREADS = kSelectThreads, W = THREADS / 64;
-    __shared__ uint32_t held[LDS ? kKeysInLds : 1];
-    __shared__ int hist[2048];
-    __shared__ uint32_t digits[D];
+    constexpr int W = THREADS / 64;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // keys without their lowest `shift` bits: above `prefix` they stay, and `left` of those that equal it
+    uint32_t prefix = 0;
+    int shift = 0, left = ch.want;
+    if (ch.want > 0) {
+        high = wave_max_u32(high);
+        low = ~wave_max_u32(~low);
+        if (lane == 0) {
+            lds.ends[0][wave] = low;
+            lds.ends[1][wave] = high;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            low = lds.ends[0][w] < low ? lds.ends[0][w] : low;
+            high = lds.ends[1][w] > high ? lds.ends[1][w] : high;
+        }
+        shift = low == high ? 0 : 32 - __builtin_clz(low ^ high);
+        prefix = shift < 32 ? high >> shift : 0;
+        for (int round = 0; round < 3 && shift > 0; ++round) {
+            int *hist = lds.hist[round];
+            const int down = shift > kDigitBits ? shift - kDigitBits : 0, bits = shift - down;
+            for (int b = ch.mid0 + tid; b < ch.mid1; b += THREADS) {
+                const uint32_t key = keys[b];
+                if (shift == 32 || key >> shift == prefix) atomicAdd(&hist[key >> down & ((1u << bits) - 1)], 1);
+            }
+            __syncthreads();
+            const uint32_t digit = pick_digit(hist, left);
+            prefix = prefix << bits | digit;
+            shift = down;
+            if (hist[digit] == left) break;  // all of them stay
+        }
+    }
+    int sure_at = 0, equal_at = 0;  // of the blocks before: those that stay anyway, and the cut's equals
+    for (int b0 = 0, buf = 0; b0 < ch.used; b0 += THREADS, buf ^= 1) {
+        const int b = b0 + tid;
+        const bool in = b < ch.used, mid = in && b >= ch.mid0 && b < ch.mid1;
+        const uint32_t key = ch.want > 0 && mid ? keys[b] >> shift : 0;
+        const bool equal = ch.want > 0 && mid && key == prefix, sure = in && (!mid || (ch.want > 0 && key > prefix));
+        const uint64_t equals = __ballot(equal), sures = __ballot(sure), below = lane ? ~0ull >> (64 - lane) : 0;
+        if (lane == 0) {
+            lds.sums[buf][0][wave] = __popcll(equals);
+            lds.sums[buf][1][wave] = __popcll(sures);
+        }
+        __syncthreads();
+        int eq = equal_at + __popcll(equals & below), at = sure_at + __popcll(sures & below);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (i < wave) {
+                eq += lds.sums[buf][0][i];
+                at += lds.sums[buf][1][i];
+            }
+            equal_at += lds.sums[buf][0][i];
+            sure_at += lds.sums[buf][1][i];
+        }
+        if (sure || (equal && eq < left)) out[at + (eq < left ? eq : left)] = b;
+    }
+    const int stayed = sure_at + (equal_at < left ? equal_at : left);
+    for (int64_t i = stayed + tid; i < a.keep; i += THREADS) out[i] = -1;
+}
+
+// least and largest key of the middle
+__device__ inline void widen(const Choice &ch, int b, uint32_t key, uint32_t &low, uint32_t &high)
+{
+    if (b < ch.mid0 || b >= ch.mid1) return;
+    low = key < low ? key : low;
+    high = key > high ? key : high;
+}
+
+// A workgroup per (row, kv head): the keys of its blocks into LDS, and the list. The queries
+// and the first bounds are asked for before either is needed.
+template <typename T, int D, int THREADS, int KEYS>
+__global__ __launch_bounds__(THREADS, 4) void block_select_kernel(SelectArgs a, int first_row)
+{
+    constexpr int W = THREADS / 64;
+    __shared__ uint32_t keys[KEYS];
+    __shared__ ChooseLds<THREADS> lds;
+    __shared__ __align__(16) uint32_t digits[D];
     __shared__ float red[W];
-    __shared__ int wave_sums[W], pick[3], sums[2][2][W];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, head = blockIdx.y;
     const int64_t row = (int64_t)first_row + blockIdx.x;
+    QueryDigits<T, D, THREADS> q;
+    q.load(a, row, head);
+    for (int i = tid; i < 3 * kDigitBins; i += THREADS) lds.hist[0][i] = 0;
+    for (int i = tid; i < D; i += THREADS) digits[i] = 0;
     int seq, place;
     if (!find_row(a.cu, a.seqs, a.m, row, seq, place)) return;
     const int64_t have = a.lens[seq];
     if (have < 0) return;
-    const int64_t blocks = (have + place) / kBlock + 1;
-    const int used = blocks < a.max_blocks ? (int)blocks : (int)a.max_blocks;
-    const bool all = used <= a.keep;
-    const int mid0 = all ? used : (int)a.first, mid1 = all ? used : (int)(used - a.recent);
-    const int want = all ? 0 : (int)(a.keep - a.first - a.recent);
+    const Choice ch(a, have, place);
     const int32_t *table = a.table + (int64_t)seq * a.max_blocks;
-    uint32_t *keys = LDS ? held : a.keys + (row * a.kv_heads + head) * a.max_blocks;
-    Cut cut{0, 32, 0};
-    if (want > 0) {
+    uint32_t low = ~0u, high = 0;
+    if (ch.want > 0) {
+        BlockBounds<D> bounds;
+        int b0 = wave * 64;
+        auto id_of = [&](int at) { return at + bounds.place() < ch.used ? table[at + bounds.place()] : -1; };
+        int id = id_of(b0);
+        if (b0 < ch.used) bounds.load(a, id, head);
+        id = id_of(b0 + THREADS);
+        float most = q.largest();
+        if (lane == 0) red[wave] = most;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) most = fmaxf(most, red[w]);
+        q.add(most, digits);
+        __syncthreads();
         v4i lo, hi;
-        query_digits<T, D>(a, row, head, digits, red, lo, hi);
-        for (int b0 = wave * 64; b0 < used; b0 += THREADS) {
-            const uint32_t key = block_keys<D>(a, table, head, b0, used, lo, hi);
-            if (b0 + lane < used) keys[b0 + lane] = key;
+        q.digits(digits, lo, hi);
+        for (; b0 < ch.used; b0 += THREADS) {
+            const uint32_t key = bounds.key(lo, hi);
+            if (b0 + THREADS < ch.used) {
+                bounds.load(a, id, head);
+                id = id_of(b0 + 2 * THREADS);
+            }
+            const int b = b0 + bounds.place();
+            if (b < ch.used) keys[b] = key;
+            widen(ch, b < ch.used ? b : -1, key, low, high);
         }
-        __syncthreads();
-        cut = find_cut<THREADS>(keys, mid0, mid1, want, hist, wave_sums, pick);
     }
-    int32_t *out = a.selected + (row * a.kv_heads + head) * a.keep;
-    int stay_at = 0, equal_at = 0;
-    for (int b0 = 0, buf = 0; b0 < used; b0 += THREADS, buf ^= 1) {
-        const int b = b0 + tid;
-        const bool in = b < used, mid = in && b >= mid0 && b < mid1;
-        const uint32_t key = want > 0 && mid ? keys[b] >> cut.shift : 0;
-        const bool equal = mid && want > 0 && key == cut.prefix;
-        const uint64_t below = lane ? ~0ull >> (64 - lane) : 0;
-        const uint64_t eq_mask = __ballot(equal);
-        if (lane == 0) sums[buf][0][wave] = __popcll(eq_mask);
-        __syncthreads();
-        int eq = equal_at + __popcll(eq_mask & below);
+    choose<THREADS>(a, ch, keys, low, high, a.selected + (row * a.kv_heads + head) * a.keep, lds);
+}
+
+// The same by two launches, for few rows and heads or tables too wide for LDS: the keys into
+// the workspace, four waves of 64 blocks per workgroup, and a workgroup per (row, kv head) that
+// chooses by them.
+template <typename T, int D>
+__global__ __launch_bounds__(256, 4) void block_score_kernel(SelectArgs a, int first_row)
+{
+    __shared__ __align__(16) uint32_t digits[D];
+    __shared__ float red[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, head = blockIdx.y;
+    const int64_t row = (int64_t)first_row + blockIdx.z;
+    QueryDigits<T, D, 256> q;
+    q.load(a, row, head);
+    for (int i = tid; i < D; i += 256) digits[i] = 0;
+    int seq, place;
+    if (!find_row(a.cu, a.seqs, a.m, row, seq, place)) return;
+    const int64_t have = a.lens[seq];
+    if (have < 0) return;
+    const Choice ch(a, have, place);
+    const int group0 = (int)blockIdx.x * 256, b = group0 + wave * 64 + BlockBounds<D>::place();
+    if (ch.want == 0 || group0 >= ch.used) return;
+    BlockBounds<D> bounds;
+    bounds.load(a, b < ch.used ? a.table[(int64_t)seq * a.max_blocks + b] : -1, head);
+    float most = q.largest();
+    if (lane == 0) red[wave] = most;
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (i < wave) eq += sums[buf][0][i];
-            equal_at += sums[buf][0][i];
-        }
-        const bool stay = in && (!mid || (want > 0 && (key > cut.prefix || (equal && eq < cut.left))));
-        const uint64_t stay_mask = __ballot(stay);
-        if (lane == 0) sums[buf][1][wave] = __popcll(stay_mask);
-        __syncthreads();
-        int at = stay_at + __popcll(stay_mask & below);
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (i < wave) at += sums[buf][1][i];
-            stay_at += sums[buf][1][i];
-        }
-        if (stay) out[at] = b;
-    }
-    for (int64_t i = stay_at + tid; i < a.keep; i += THREADS) out[i] = -1;
+    for (int w = 0; w < 4; ++w) most = fmaxf(most, red[w]);
+    q.add(most, digits);
+    __syncthreads();
+    v4i lo, hi;
+    q.digits(digits, lo, hi);
+    const uint32_t key = bounds.key(lo, hi);
+    if (b < ch.used) a.keys[(row * a.kv_heads + head) * a.max_blocks + b] = key;
+}
+
+__global__ __launch_bounds__(1024) void block_choose_kernel(SelectArgs a, int first_row)
+{
+    constexpr int THREADS = 1024;
+    __shared__ ChooseLds<THREADS> lds;
+    const int tid = threadIdx.x, head = blockIdx.y;
+    const int64_t row = (int64_t)first_row + blockIdx.x;
+    for (int i = tid; i < 3 * kDigitBins; i += THREADS) lds.hist[0][i] = 0;
+    int seq, place;
+    if (!find_row(a.cu, a.seqs, a.m, row, seq, place)) return;
+    const int64_t have = a.lens[seq];
+    if (have < 0) return;
+    const Choice ch(a, have, place);
+    const uint32_t *keys = a.keys + (row * a.kv_heads + head) * a.max_blocks;
+    uint32_t low = ~0u, high = 0;
+    if (ch.want > 0)
+        for (int b = tid; b < ch.used; b += THREADS) widen(ch, b, keys[b], low, high);
+    choose<THREADS>(a, ch, keys, low, high, a.selected + (row * a.kv_heads + head) * a.keep, lds);
 }
 
 // ---------------------------------------------------------------- launchers
@@ -335,9 +497,16 @@ hipError_t launch_cache_bounds(const CacheBounds &p, hipStream_t st)
     return hipGetLastError();
 }
 
+// One workgroup reads a head's bounds at 64 bytes a cycle and takes 6 us of arithmetic for
+// 2048 blocks: where rows and heads leave CUs idle, the scores are a launch of their own.
+static bool two_launches(int64_t m, int64_t kv_heads, int64_t max_blocks)
+{
+    return max_blocks > kKeysInLds || (max_blocks > 512 && m * kv_heads <= 64);
+}
+
 int64_t block_select_workspace(int64_t m, int64_t kv_heads, int64_t max_blocks)
 {
-    return max_blocks <= kKeysInLds ? 0 : m * kv_heads * max_blocks * 4;
+    return two_launches(m, kv_heads, max_blocks) ? m * kv_heads * max_blocks * 4 : 0;
 }
 
 hipError_t launch_block_select(const SelectProblem &p, void *ws, hipStream_t st)
@@ -347,17 +516,24 @@ hipError_t launch_block_select(const SelectProblem &p, void *ws, hipStream_t st)
     a.q_heads = (int)p.q_heads; a.kv_heads = (int)p.kv_heads; a.group = (int)(p.q_heads / p.kv_heads);
     a.max_blocks = p.max_blocks; a.pages = p.pages; a.keep = p.keep; a.first = p.first; a.recent = p.recent;
     a.bounds = p.bounds; a.k_scale = p.k_scale; a.selected = p.selected; a.keys = static_cast<uint32_t *>(ws);
-    in_launches(p.m, [&](int first, unsigned n) {
-        const dim3 grid(n, (unsigned)p.kv_heads), threads(kSelectThreads);
-        auto go = [&](auto type, auto width) {
-            using T = decltype(type);
-            constexpr int D = decltype(width)::value;
-            if (p.max_blocks <= kKeysInLds) hipLaunchKernelGGL((block_select_kernel<T, D, true>), grid, threads, 0, st, a, first);
-            else hipLaunchKernelGGL((block_select_kernel<T, D, false>), grid, threads, 0, st, a, first);
-        };
-        if (p.bf16) p.head_dim == 128 ? go(bf16_t{}, Width<128>{}) : go(bf16_t{}, Width<64>{});
-        else p.head_dim == 128 ? go(float{}, Width<128>{}) : go(float{}, Width<64>{});
-    });
+    auto go = [&](auto type, auto width) {
+        using T = decltype(type);
+        constexpr int D = decltype(width)::value;
+        const bool apart = two_launches(p.m, p.kv_heads, p.max_blocks);
+        if (apart)
+            in_launches(p.m, [&](int first, unsigned n) {
+                const dim3 grid((unsigned)ceil_div(p.max_blocks, 256), (unsigned)p.kv_heads, n);
+                hipLaunchKernelGGL((block_score_kernel<T, D>), grid, dim3(256), 0, st, a, first);
+            }, kMostInZ);
+        in_launches(p.m, [&](int first, unsigned n) {
+            const dim3 grid(n, (unsigned)p.kv_heads);
+            if (apart) hipLaunchKernelGGL(block_choose_kernel, grid, dim3(1024), 0, st, a, first);
+            else if (p.max_blocks <= 2048) hipLaunchKernelGGL((block_select_kernel<T, D, 256, 2048>), grid, dim3(256), 0, st, a, first);
+            else hipLaunchKernelGGL((block_select_kernel<T, D, 1024, kKeysInLds>), grid, dim3(1024), 0, st, a, first);
+        });
+    };
+    if (p.bf16) p.head_dim == 128 ? go(bf16_t{}, Width<128>{}) : go(bf16_t{}, Width<64>{});
+    else p.head_dim == 128 ? go(float{}, Width<128>{}) : go(float{}, Width<64>{});
     return hipGetLastError();
 }
 

@@ -87,7 +87,7 @@ def test_workspace_sizes(bl):  # noqa: F811
     assert bl.attention_shared_workspace_size(0, 8, 2, 128, 1, 4, 4) == 0 and bl.attention_shared_workspace_size(1, 8, 2, 128, 1, 4, 0) == 0
     assert bl.attention_shared_workspace_size(64, 32, 8, 128, 64, 32, 256) >= 64 * 32 * 130 * 4
     assert bl.attention_shared_workspace_size(1 << 18, 4096, 1, 128, 1 << 18, 1 << 20, 1 << 20) >= (1 << 30) * 130 * 4  # does not wrap
-    assert bl.block_select_workspace_size(7, 8, 2048) == 0 and bl.block_select_workspace_size(7, 8, 1 << 20) == 7 * 8 * 4 << 20
+    assert bl.block_select_workspace_size(64, 8, 2048) == 0 and bl.block_select_workspace_size(1, 8, 2048) == 8 * 4 * 2048 and bl.block_select_workspace_size(7, 8, 1 << 20) == 7 * 8 * 4 << 20
     assert bl.block_select_workspace_size(1, 0, 1 << 20) == 0
     assert bl.attention_selected_workspace_size(1, 32, 8, 128, 64) > 0 and bl.attention_selected_workspace_size(1024, 32, 8, 128, 64) == 0
     assert bl.attention_selected_workspace_size(1, 32, 8, 96, 64) == 0
