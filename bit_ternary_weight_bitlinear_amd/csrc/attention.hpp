@@ -78,30 +78,37 @@ __device__ inline bool find_tile(const int32_t *cu, int seqs, int64_t m, int idx
     return false;
 }
 
-// The sequence that a row of a packed batch lies in, and its place there: the last one that
-// begins at or before it, of 64 probes a round. False: it is in none. Wave-uniform.
-__device__ inline bool find_row(const int32_t *cu, int seqs, int64_t m, int64_t row, int &seq, int &place)
+// The sequence that a row of a packed batch lies in, its place there and the sequence's entry
+// of `per` (the tokens that it holds, or its first position): the last sequence that begins at
+// or before the row, of 64 probes a round, where the last round's lanes have the entry and the
+// next sequence's start at hand too. False: the row is in none. Wave-uniform.
+__device__ inline bool find_row(const int32_t *cu, const int32_t *per, int seqs, int64_t m, int64_t row, int &seq, int &place, int &entry)
 {
     if (!cu) {
         seq = (int)row;
         place = 0;
-        return row < seqs;
+        if (row >= seqs) return false;
+        entry = per[row];
+        return true;
     }
     const int lane = threadIdx.x & 63;
     int lo = 0, n = seqs;
-    while (n > 1) {
+    while (n > 64) {
         const int step = (n + 63) / 64;
         const bool before = lane * step < n && cu[lo + lane * step] <= row;
         const int last = 63 - __builtin_clzll(__ballot(before) | 1);
         lo += last * step;
         n = n - last * step < step ? n - last * step : step;
     }
-    int64_t begin;
-    int rows;
-    seq_rows(cu, lo, m, begin, rows);
-    seq = lo;
-    place = (int)(row - begin);
-    return row >= begin && row < begin + rows;
+    const int at = lane < n ? lo + lane : lo, begins = cu[at], ends = cu[at + 1], entries = per[at];
+    const int last = 63 - __builtin_clzll(__ballot(lane < n && begins <= row) | 1);
+    int64_t a = __builtin_amdgcn_readlane(begins, last), b = __builtin_amdgcn_readlane(ends, last);
+    a = a < 0 ? 0 : a > m ? m : a;
+    b = b < a ? a : b > m ? m : b;
+    seq = lo + last;
+    place = (int)(row - a);
+    entry = __builtin_amdgcn_readlane(entries, last);
+    return row >= a && row < b;
 }
 
 __device__ inline void store_out(float *p, float v) { *p = v; }

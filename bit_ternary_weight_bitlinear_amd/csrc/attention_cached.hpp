@@ -108,7 +108,8 @@ __device__ inline bool find_rows(const CachedArgs &a, int idx, SeqTile &t, int &
         t.begin = idx / a.tiles_per_seq;
         t.tile = idx % a.tiles_per_seq;
         t.n = 1;
-        return find_row(a.cu, a.seqs, a.m, t.begin, t.seq, tok) && a.lens[t.seq] >= 0;
+        int have;
+        return find_row(a.cu, a.lens, a.seqs, a.m, t.begin, t.seq, tok, have) && have >= 0;
     }
     if (!a.cu) {
         t.seq = idx / a.tiles_per_seq;

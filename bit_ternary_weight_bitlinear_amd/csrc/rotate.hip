@@ -69,10 +69,8 @@ __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int first)
     const int64_t row = item / a.parts;
     const int part = (int)(item - row * a.parts);
     if (row >= a.m) return;
-    int seq, place;
-    if (!find_row(a.cu, a.seqs, a.m, row, seq, place)) return;
-    const int begin = a.begin[seq];
-    if (begin < 0) return;  // an unused slot
+    int seq, place, begin;
+    if (!find_row(a.cu, a.begin, a.seqs, a.m, row, seq, place, begin) || begin < 0) return;  // negative: an unused slot
     const int slot = lane % LANES, heads = a.q_heads + a.kv_heads;
     const bool rotary = slot * E < a.pairs;
     // elements of a lane: `lo` .. lo+E-1 and `hi` .. hi+E-1 of the head
