@@ -34,7 +34,8 @@ constexpr int kPrefixRows = 32;
 
 struct PrefixArgs {
     const void *q;
-    int64_t q_stride, rows;  // rows of a kv head: m * group
+    int64_t q_stride;
+    uint32_t rows;  // of a kv head: m * group
     int q_heads, kv_heads, group, splits;
     const int32_t *table, *len;
     int64_t blocks, pages, total_rows;
@@ -114,12 +115,11 @@ __device__ inline float page_weights(v16f (&s)[2], float f, float off, int left,
 // A query row as fp16, row r of an operand of 32: an eighth of it by thread c of eight. Returns
 // the row's factor (NaN where it is not finite) and the sum of its elements.
 template <typename T, int D, int PARTS>
-__device__ inline float2 query_row(const PrefixArgs &a, int64_t row, int head, int r, int c, _Float16 *qh)
+__device__ inline float2 query_row(const PrefixArgs &a, uint32_t row, int head, int r, int c, _Float16 *qh)
 {
     constexpr int E = D / 8, U = D / 32;
     const bool there = row < a.rows;
-    const int64_t at = there ? row : 0, tok = at / a.group;
-    const int hq = head * a.group + (int)(at - tok * a.group);
+    const uint32_t at = there ? row : 0, tok = at / (uint32_t)a.group, hq = head * a.group + (at - tok * a.group);
     const T *src = static_cast<const T *>(a.q) + tok * a.q_stride + (int64_t)hq * D + E * c;
     T raw[E];
 #pragma unroll
@@ -134,11 +134,13 @@ __device__ inline float2 query_row(const PrefixArgs &a, int64_t row, int head, i
         }
         big = fmaxf(big, fabsf(x[i]));
     }
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) {
-        big = fmaxf(big, __shfl_xor(big, d));
-        bad = fmaxf(bad, __shfl_xor(bad, d));
-    }
+    auto of8 = [](float v, auto f) {
+        v = f(v, __int_as_float(dpp_mov<kDppQuadXor1>(__float_as_int(v))));
+        v = f(v, __int_as_float(dpp_mov<kDppQuadXor2>(__float_as_int(v))));
+        return f(v, __int_as_float(dpp_mov<kDppRowHalfMirror>(__float_as_int(v))));
+    };
+    big = of8(big, [](float x, float y) { return fmaxf(x, y); });
+    bad = of8(bad, [](float x, float y) { return fmaxf(x, y); });
     const int e = 14 - ((int)(__float_as_uint(fmaxf(big, 1e-30f)) >> 23) - 127);
     float total = 0.0f;
     const float up = __uint_as_float((uint32_t)(127 + e) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
@@ -157,8 +159,7 @@ __device__ inline float2 query_row(const PrefixArgs &a, int64_t row, int head, i
         *reinterpret_cast<v8h *>(dst) = hi;
         if constexpr (PARTS == 2) *reinterpret_cast<v8h *>(dst + U * 2 * 64 * 8) = lo;
     }
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) total += __shfl_xor(total, d);
+    total = of8(total, [](float x, float y) { return x + y; });
     return make_float2(bad > 0.0f ? __builtin_nanf("") : __uint_as_float((uint32_t)(127 - e) << 23) * fabsf(a.scale), total);
 }
 
@@ -185,11 +186,42 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, col = lane & 31;
-    const int64_t row0 = tile * R;
+    const uint32_t row0 = (uint32_t)tile * R;  // rows are counted in 31 bits
     const int len = *a.len, npages = prefix_pages(a.len, a.blocks);
     const int chunk = prefix_chunk(npages, a.splits);
     const int p0 = split * chunk, p1 = p0 + chunk < npages ? p0 + chunk : npages;
     if (p0 >= npages) return;  // the join knows
+
+    // place of this lane's K row in its 32 tokens, and of its pieces in a page and head
+    const int token = 16 * (col >> 2 & 1) + 8 * (col >> 4) + 4 * (col >> 3 & 1) + (col & 3);
+    const int k_at = k_code_at<D>(token, 16 * half);
+    const int v_at = v_code_at(16 * half, col);
+    // ids and scales of 64 of the wave's pages, one per lane
+    int page = 0, ok = 0;
+    float my_ks = 0.0f, my_vs = 0.0f;
+    auto fetch_ids = [&](int base) {
+        const int mine = base + W * lane, id = mine < p1 ? a.table[mine] : -1;
+        ok = id >= 0 && id < a.pages;
+        page = ok ? id : 0;  // a block without a page reads page 0
+        const int64_t at = (int64_t)page * a.kv_heads + head;
+        my_ks = a.k_scale[at];
+        my_vs = a.v_scale[at];
+    };
+    // K of a page is asked for when the one before has met the queries (the first while they are
+    // made ready), V of a page before its K does
+    uint4 kf[2][U];
+    auto load_k = [&](int i) {
+        const int id = __builtin_amdgcn_readlane(page, i);
+        const int8_t *kp = a.k_codes + ((int64_t)id * a.kv_heads + head) * (kBlock * D) + k_at;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int u = 0; u < U; ++u) kf[t][u] = *reinterpret_cast<const uint4 *>(kp + t * 8 * 16 + u * 2 * 256);
+    };
+    if (p0 + wave < p1) {
+        fetch_ids(p0 + wave);
+        load_k(0);
+    }
 
     {
         const float2 f = query_row<T, D, PARTS>(a, row0 + (tid >> 3), head, tid >> 3, tid & 7, reinterpret_cast<_Float16 *>(qh));
@@ -205,32 +237,17 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[u][i] = 0.0f;
 
-    // place of this lane's K row in its 32 tokens, and of its pieces in a page and head
-    const int token = 16 * (col >> 2 & 1) + 8 * (col >> 4) + 4 * (col >> 3 & 1) + (col & 3);
-    const int k_at = k_code_at<D>(token, 16 * half);
-    const int v_at = v_code_at(16 * half, col);
     v8h ones;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ones[i] = (_Float16)1.0f;
 
-    uint4 kf[2][U];
     for (int base = p0 + wave; base < p1; base += 64 * W) {
-        const int mine = base + W * lane;
-        const int ids = mine < p1 ? a.table[mine] : -1;
-        const bool ok = ids >= 0 && ids < a.pages;
-        const int page = ok ? ids : 0;  // a block without a page reads page 0
-        const int64_t my_at = (int64_t)page * a.kv_heads + head;
-        const float my_ks = ok ? a.k_scale[my_at] / 127.0f : 0.0f, my_vs = ok ? a.v_scale[my_at] / 127.0f : 0.0f;
-        auto load_k = [&](int i) {
-            const int id = __builtin_amdgcn_readlane(page, i);
-            const int8_t *kp = a.k_codes + ((int64_t)id * a.kv_heads + head) * (kBlock * D) + k_at;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int u = 0; u < U; ++u) kf[t][u] = *reinterpret_cast<const uint4 *>(kp + t * 8 * 16 + u * 2 * 256);
-        };
-        // K of a page is asked for when the one before has met the queries, V of a page before its K does
-        load_k(0);
+        if (base != p0 + wave) {
+            fetch_ids(base);
+            load_k(0);
+        }
+        my_ks = ok ? my_ks / 127.0f : 0.0f;  // nothing of page 0 may enter for a missing one
+        my_vs = ok ? my_vs / 127.0f : 0.0f;
         for (int p = base, i = 0; p < p1 && i < 64; p += W, ++i) {
             const int id = __builtin_amdgcn_readlane(page, i);
             const int8_t *vp = a.v_codes + ((int64_t)id * a.kv_heads + head) * (kBlock * D) + v_at;
@@ -239,7 +256,7 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) vf[u][t] = *reinterpret_cast<const uint4 *>(vp + (u * 2 * 4 + t * 2) * 256);
-            const bool there = __builtin_amdgcn_readlane((int)ok, i) != 0;
+            const bool there = __builtin_amdgcn_readlane(ok, i) != 0;
             const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_ks), i));
             const float vs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_vs), i));
             const int left = there ? len - p * kBlock : 0;
@@ -342,12 +359,15 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
             for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(f, v[i], o[i]);
             l = __builtin_fmaf(f, jm[w][r].y, l);
         }
-        const int64_t tok = (row0 + r) / a.group;
-        const int64_t row = tok * a.q_heads + head * a.group + (row0 + r - tok * a.group);
+        const uint32_t tok = (row0 + r) / (uint32_t)a.group;
+        const int64_t row = (int64_t)tok * a.q_heads + head * a.group + (row0 + r - tok * a.group);
         *reinterpret_cast<v4f *>(a.part_o + ((int64_t)split * a.total_rows + row) * D + dim) = o;
         if (dim == 0) reinterpret_cast<float2 *>(a.part_ml)[(int64_t)split * a.total_rows + row] = make_float2(best, l);
     }
 }
+
+// a / b of workgroup numbers, which rarely need 64 bits
+__device__ inline int64_t over(int64_t a, int b) { return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b); }
 
 // The prefix's workgroups first, which take longest, then the sequences' own pages: the one
 // waits for arithmetic, the other for memory.
@@ -360,15 +380,14 @@ __global__ __launch_bounds__(64 * kPrefixWaves, 2) void attention_shared_kernel(
     __shared__ float2 row_scale[kPrefixRows], jm[kPrefixWaves][kPrefixRows];
     int64_t group = first + blockIdx.x;
     if (group < prefix_groups) {
-        const int64_t unit = group / f.splits;
-        attention_prefix_tile<T, D>(f, unit / f.kv_heads, (int)(unit % f.kv_heads), (int)(group - unit * f.splits), lds, row_scale, jm);
+        const int64_t unit = over(group, f.splits), tile = over(unit, f.kv_heads);
+        attention_prefix_tile<T, D>(f, tile, (int)(unit - tile * f.kv_heads), (int)(group - unit * f.splits), lds, row_scale, jm);
         return;
     }
     group -= prefix_groups;
-    const int64_t unit = group / a.splits;
-    attention_cached_tile<T, D, RT, kPrefixWaves, false, kBehindPrefix>(a, (int)(unit / a.kv_heads), (int)(unit % a.kv_heads),
-                                                                       (int)(group - unit * a.splits), reinterpret_cast<uint32_t *>(lds),
-                                                                       reinterpret_cast<float *>(row_scale));
+    const int64_t unit = over(group, a.splits), tile = over(unit, a.kv_heads);
+    attention_cached_tile<T, D, RT, kPrefixWaves, false, kBehindPrefix>(a, (int)tile, (int)(unit - tile * a.kv_heads), (int)(group - unit * a.splits),
+                                                                       reinterpret_cast<uint32_t *>(lds), reinterpret_cast<float *>(row_scale));
 }
 
 // ---------------------------------------------------------------- launcher
@@ -412,7 +431,7 @@ hipError_t launch_attention_shared(const SharedProblem &p, void *ws, hipStream_t
     const SharedLayout L = shared_layout(p);
     char *base = static_cast<char *>(ws);
     PrefixArgs f{};
-    f.q = c.q; f.q_stride = c.q_stride; f.group = (int)(c.q_heads / c.kv_heads); f.rows = c.m * f.group;
+    f.q = c.q; f.q_stride = c.q_stride; f.group = (int)(c.q_heads / c.kv_heads); f.rows = (uint32_t)(c.m * f.group);
     f.q_heads = (int)c.q_heads; f.kv_heads = (int)c.kv_heads; f.splits = (int)prefix_splits(p);
     f.table = p.prefix_table; f.len = p.prefix_len; f.blocks = p.prefix_blocks; f.pages = c.pages; f.total_rows = c.m * c.q_heads;
     f.k_codes = c.k_codes; f.v_codes = c.v_codes; f.k_scale = c.k_scale; f.v_scale = c.v_scale; f.scale = c.scale * kLog2e;
