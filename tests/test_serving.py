@@ -312,6 +312,33 @@ def test_shared_prefix_of_a_sequence_itself(bl):  # noqa: F811
         np.testing.assert_allclose(_np(got), _np(whole), rtol=2e-5, atol=2e-5 * float(whole.abs().max()))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_outlier_channels_of_the_cache(bl, dtype):  # noqa: F811
+    """Channels that set a page's scale beside others whose codes are small: what the others hold counts."""
+    c, prefix = _behind(bl, length=500, d=128)
+    for codes, ours, place in ((c.cache.k, c.kc, c.place[0]), (c.cache.v, c.vc, c.place[1])):
+        ours[:] = np.clip(ours // 16, -7, 7)
+        ours[..., 3], ours[..., 77] = 127, -120
+        codes.copy_(torch.tensor(cached_ref.stored(ours, place)))
+    _check_shared(bl, c, prefix, 500, [70, 3], [2, 3], 8, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_many_rows_and_pages(bl, dtype):  # noqa: F811
+    """So many rows that a workgroup has the whole prefix and a wave more than 64 of its pages: every row as in a batch of
+    a few, whose prefix is split (each within its own tolerance of the definition, u = 2^-24 or 2^-8)."""
+    c, _ = _behind(bl, length=640, lens=(70,), new=(1,), hkv=1, d=64)
+    prefix = _i32(np.random.default_rng(3).integers(0, c.pages, 300))
+    few = _rand((3, 32, 64), 5, DTYPES[dtype], 1.5)
+    n = 270
+    out = [bl.attention_shared(few[torch.arange(m, device="cuda") % 3].contiguous(), c.cache, prefix, _i32([300 * 64 - 5]),
+                               _i32(c.table).expand(m, -1).contiguous(), _i32([70] * m)) for m in (n, 3)]
+    for i in range(3):
+        assert (out[0][i::3] == out[0][i]).all()
+    off = (out[0][:3].float() - out[1].float()).abs().max() / out[1].float().abs().max()
+    assert off < (2.0**-7 if dtype == "bf16" else 2e-5)
+
+
 # ---------------------------------------------------------------- bounds
 
 @pytest.mark.parametrize("hkv,d", [(5, 128), (1, 64), (3, 128)])
@@ -483,6 +510,25 @@ def test_selected_all_blocks_is_attention_over_the_cache(bl):  # noqa: F811
     sel = torch.arange(c.wide, dtype=torch.int32, device="cuda").expand(2, 2, c.wide).contiguous()
     assert torch.equal(bl.attention_selected(q, c.cache, _i32(c.table), _i32([700, 333]), sel),
                        bl.attention_cached(q, c.cache, _i32(c.table), _i32([700, 333])))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_selected_long_lists_of_many_rows(bl, dtype):  # noqa: F811
+    """So many rows that one workgroup has a whole list and a wave more than 64 of its blocks: every row as in a batch of a
+    few, whose lists are split."""
+    c = _Paged(bl, [1200], [1], 2, 64, 8)
+    c.table = np.tile(c.table, (1, 20))
+    few = _rand((3, 4, 64), 5, DTYPES[dtype], 1.5)
+    lists = torch.tensor(np.random.default_rng(3).integers(-1, c.table.shape[1], (3, 2, 300)), dtype=torch.int32).cuda()
+    out = []
+    for m in (300, 3):
+        i = torch.arange(m, device="cuda") % 3
+        out.append(bl.attention_selected(few[i].contiguous(), c.cache, _i32(c.table).expand(m, -1).contiguous(), _i32([64 * 300] * m),
+                                         lists[i].contiguous()))
+    for i in range(3):
+        assert (out[0][i::3] == out[0][i]).all()
+    off = (out[0][:3].float() - out[1].float()).abs().max() / out[1].float().abs().max()
+    assert off < (2.0**-7 if dtype == "bf16" else 2e-5)
 
 
 def test_selected_rows_that_are_not_finite(bl):  # noqa: F811
