@@ -3,19 +3,20 @@
 //
 // A softmax over the two together is their results joined by their maxima and sums, so
 // the prefix is read once for all sequences: their query rows of a kv head, m * group of
-// them, are the rows of one matrix product with it. The kernel here writes the prefix's
-// parts (maximum, sum and sum of values of every row), attention_cached_kernel adds them
-// to the results of the sequences' own pages as it stores them, or the joining launch
-// does where those come in parts too.
+// them, are the rows of one matrix product with it. One launch holds the prefix's
+// workgroups (32 rows and a part of the prefix each) and those of the sequences' own pages
+// (attention_cached_tile), a second one joins their parts.
 //
-// With 32 query rows a wave the arithmetic counts, not the bytes, so here the codes meet
-// the queries as fp16, on v_mfma_f32_32x32x16_f16: a code is an integer and exact, a row of
-// q times a power of two that puts its largest at 2^14 to 2^15 is exact in fp16 for bf16
-// elements down to 2^-31 of the largest, and in two fp16 parts good to 2^-22 for fp32
+// With 32 query rows a wave the arithmetic counts, not the bytes, so over the prefix the
+// codes meet the queries as fp16, on v_mfma_f32_32x32x16_f16: a code is an integer and exact,
+// a row of q times a power of two that puts its largest at 2^14 to 2^15 is exact in fp16 for
+// bf16 elements down to 2^-31 of the largest, and in two fp16 parts good to 2^-22 for fp32
 // (elements below 2^-17 of the largest: to 2^-39 of that). Weights are relative to a power
 // of two at or above their page's and row's largest, times 2^15: rounded to fp16 (2^-11)
-// for bf16 results, in two parts (2^-22) for fp32 ones. Sums are fp32, a page's scaled by
-// its V scale when they are added to the row's.
+// for bf16 results, in two parts (2^-22) for fp32 ones; their sum is that of the rounded
+// weights, by a product with ones. Sums are fp32, a page's scaled by its V scale when they are
+// added to the row's; for bf16 results V's codes are raised by 128 in them and the weights'
+// sum times 128 taken off at the end (their roundings count as of codes of 256).
 //
 // Layout: S^T = K Q^T has a query row per lane and 32 of a page's 64 tokens in its two
 // times 16 registers, which after the exponential are the second operand of O^T = V^T P^T
@@ -23,6 +24,16 @@
 //   16 * bit 2 + 8 * bit 4 + 4 * bit 3 + (bits 1, 0) of rho
 // of its 32, which gives a lane half h the 16 tokens that one 16-byte piece of V holds. The
 // dims of the first product are ordered likewise by 16-byte pieces of K.
+//
+// What bounds it: a page and 32 rows are 36 matrix instructions (1150 cycles) and about 490
+// vector ones (32 of them exponentials, 2300 cycles) in bf16, which take turns rather than
+// overlap: 3500 cycles a page measured with one wave per SIMD, as much for each of two. 64
+// tokens of 32/8 heads behind 16384, 300 to 700 of their own: 38 us, and 4.8 for the join
+// (prefix alone 31, own pages alone 18; one behind the other 52). One workgroup of the prefix
+// per CU leaves room for one of own pages, which wait for memory (two: 46 us in all). Not
+// kept: codes as fp16 through LDS for 128 rows, a barrier a page (40 us for the prefix); 64
+// rows per wave (35); K's codes raised by 128 too (2.5 us less, but a channel that sets a
+// page's scale would round the logits of the others).
 #include "attention_cached.hpp"
 
 namespace bl {
@@ -46,7 +57,7 @@ struct PrefixArgs {
 };
 
 // Eight codes as fp16. EXACT: 1024 + (code + 128) is the bits 0x6400 with the biased code in
-// the low byte. Otherwise those alone, (code + 128) 2^-24: two instructions of five fewer for
+// the low byte. Otherwise those alone, (code + 128) 2^-24: three instructions instead of five for
 // four codes, and a product with them is 2^-24 (sum + 128 * the sum of the other factor).
 template <bool EXACT>
 __device__ inline v8h codes_f16(uint32_t lo, uint32_t hi)
@@ -76,16 +87,16 @@ struct Weights {
     v8h hi[2][2], lo[2][2];
 };
 
-// Weights from sums s of products (times f, less `off`: the logits, in powers of two) of the
-// `left` tokens that the page holds (none without a page, of whose stand-in nothing may enter).
-// Returns their reference exponent.
+// Weights from sums s of products (times f: the logits, in powers of two) of the `left` tokens
+// that the page holds (none without a page, of whose stand-in nothing may enter). Returns
+// their reference exponent.
 template <int PARTS>
-__device__ inline float page_weights(v16f (&s)[2], float f, float off, int left, int half, Weights<PARTS> &w)
+__device__ inline float page_weights(v16f (&s)[2], float f, int left, int half, Weights<PARTS> &w)
 {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[t][r] = PARTS == 2 ? s[t][r] * f : __builtin_fmaf(s[t][r], f, off);
+        for (int r = 0; r < 16; ++r) s[t][r] *= f;
     if (left < kBlock)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -113,9 +124,9 @@ __device__ inline float page_weights(v16f (&s)[2], float f, float off, int left,
 }
 
 // A query row as fp16, row r of an operand of 32: an eighth of it by thread c of eight. Returns
-// the row's factor (NaN where it is not finite) and the sum of its elements.
+// the row's factor, NaN where it is not finite.
 template <typename T, int D, int PARTS>
-__device__ inline float2 query_row(const PrefixArgs &a, uint32_t row, int head, int r, int c, _Float16 *qh)
+__device__ inline float query_row(const PrefixArgs &a, uint32_t row, int head, int r, int c, _Float16 *qh)
 {
     constexpr int E = D / 8, U = D / 32;
     const bool there = row < a.rows;
@@ -142,7 +153,6 @@ __device__ inline float2 query_row(const PrefixArgs &a, uint32_t row, int head, 
     big = of8(big, [](float x, float y) { return fmaxf(x, y); });
     bad = of8(bad, [](float x, float y) { return fmaxf(x, y); });
     const int e = 14 - ((int)(__float_as_uint(fmaxf(big, 1e-30f)) >> 23) - 127);
-    float total = 0.0f;
     const float up = __uint_as_float((uint32_t)(127 + e) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
 #pragma unroll
     for (int g = 0; g < E / 8; ++g) {
@@ -154,13 +164,11 @@ __device__ inline float2 query_row(const PrefixArgs &a, uint32_t row, int head, 
             const float v = x[8 * g + i] * up;
             hi[i] = (_Float16)v;
             lo[i] = (_Float16)(v - (float)hi[i]);
-            total += (float)hi[i];
         }
         *reinterpret_cast<v8h *>(dst) = hi;
         if constexpr (PARTS == 2) *reinterpret_cast<v8h *>(dst + U * 2 * 64 * 8) = lo;
     }
-    total = of8(total, [](float x, float y) { return x + y; });
-    return make_float2(bad > 0.0f ? __builtin_nanf("") : __uint_as_float((uint32_t)(127 - e) << 23) * fabsf(a.scale), total);
+    return bad > 0.0f ? __builtin_nanf("") : __uint_as_float((uint32_t)(127 - e) << 23) * fabsf(a.scale);
 }
 
 // A workgroup has 32 query rows of a kv head and part of the prefix, whose pages go to its
@@ -174,7 +182,7 @@ struct PrefixLds {
 };
 
 template <typename T, int D>
-__device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, int head, int split, char *lds, float2 *row_scale,
+__device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, int head, int split, char *lds, float *row_scale,
                                              float2 (*jm)[kPrefixRows])
 {
     constexpr int W = kPrefixWaves, R = kPrefixRows;
@@ -224,12 +232,12 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
     }
 
     {
-        const float2 f = query_row<T, D, PARTS>(a, row0 + (tid >> 3), head, tid >> 3, tid & 7, reinterpret_cast<_Float16 *>(qh));
+        const float f = query_row<T, D, PARTS>(a, row0 + (tid >> 3), head, tid >> 3, tid & 7, reinterpret_cast<_Float16 *>(qh));
         if ((tid & 7) == 0) row_scale[tid >> 3] = f;
     }
     __syncthreads();
-    const bool poor = !(row_scale[col].x == row_scale[col].x);
-    const float qs = poor ? 0.0f : row_scale[col].x, qsum = row_scale[col].y;
+    const bool poor = !(row_scale[col] == row_scale[col]);
+    const float qs = poor ? 0.0f : row_scale[col];
     float top = kNegInf, sum = 0.0f, bias = 0.0f;  // bias: what the biased codes of V added to acc
     v16f acc[U];
 #pragma unroll
@@ -274,7 +282,7 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const uint4 c = kf[t][u >> 1];
-                    const v8h k8 = u & 1 ? codes_f16<EXACT>(c.z, c.w) : codes_f16<EXACT>(c.x, c.y);
+                    const v8h k8 = u & 1 ? codes_f16<true>(c.z, c.w) : codes_f16<true>(c.x, c.y);
                     if constexpr (PARTS == 2) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q1, s[t], 0, 0, 0);
                     s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q0, s[t], 0, 0, 0);
                 }
@@ -282,8 +290,7 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
             if (p + W < p1 && i < 63) load_k(i + 1);
 
             Weights<PARTS> w;
-            const float f = qs * ks;
-            const float ref = page_weights<PARTS>(s, EXACT ? f : f * 0x1p24f, -128.0f * qsum * f, left, half, w);
+            const float ref = page_weights<PARTS>(s, qs * ks, left, half, w);
             const float now = fmaxf(top, ref), to = now == kNegInf ? 0.0f : now;
             const float add = __builtin_amdgcn_exp2f(ref - to) * 0x1p-15f, g = add * vs;  // of the page's weights and sums
             if (__any(now != top)) {
@@ -377,7 +384,8 @@ __global__ __launch_bounds__(64 * kPrefixWaves, 2) void attention_shared_kernel(
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
     constexpr int kOwnBytes = CachedLds<D, RT, kPrefixWaves>::words * 4, kPrefixBytes = PrefixLds<D, PARTS>::bytes;
     __shared__ __align__(16) char lds[kPrefixBytes > kOwnBytes ? kPrefixBytes : kOwnBytes];
-    __shared__ float2 row_scale[kPrefixRows], jm[kPrefixWaves][kPrefixRows];
+    __shared__ float row_scale[kPrefixRows];
+    __shared__ float2 jm[kPrefixWaves][kPrefixRows];
     int64_t group = first + blockIdx.x;
     if (group < prefix_groups) {
         const int64_t unit = over(group, f.splits), tile = over(unit, f.kv_heads);
@@ -387,7 +395,7 @@ __global__ __launch_bounds__(64 * kPrefixWaves, 2) void attention_shared_kernel(
     group -= prefix_groups;
     const int64_t unit = over(group, a.splits), tile = over(unit, a.kv_heads);
     attention_cached_tile<T, D, RT, kPrefixWaves, false, kBehindPrefix>(a, (int)tile, (int)(unit - tile * a.kv_heads), (int)(group - unit * a.splits),
-                                                                       reinterpret_cast<uint32_t *>(lds), reinterpret_cast<float *>(row_scale));
+                                                                       reinterpret_cast<uint32_t *>(lds), row_scale);
 }
 
 // ---------------------------------------------------------------- launcher
