@@ -4,16 +4,21 @@
 //   x^ = (x * r) * gain,  r = 1 / sqrt(mean_d x^2 + eps)          (where a gain is given)
 //   (a, b) -> magnitude * (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
 //
-// for the pairs i of the head's first rotary_dim elements; the others pass. Bound by HBM
-// with many tokens (every element read once and written once), by one token's latency with
-// few. A wave works on one token: its 64 lanes compute the token's angles once, for all of
-// its heads, and exchange the cosines and sines through LDS; a lane then holds the same two
-// 16-byte pieces of every head that it gets, both elements of each pair among them, so a
-// norm is one reduction over 4 to 16 neighbouring lanes and a rotation none.
+// for the pairs i of the head's first rotary_dim elements; the others pass. A wave works on
+// one token: its 64 lanes compute the token's angles once, for all of its heads, and exchange
+// the cosines and sines through LDS; a lane then holds the same two 16-byte pieces of every
+// head that it gets, both elements of each pair among them, so a norm is one reduction over 4
+// to 16 neighbouring lanes and a rotation none.
 //
 // The angle in 64 bits: the product of a position and an fp32 frequency by its rounded value
 // and the remainder, less the multiple of pi / 2 next to it (two constants, 106 bits of
 // pi / 2), so positions up to 2^31 cost no digits; its cosine and sine are rounded to fp32.
+//
+// Bound by HBM with many tokens: 8192 of 32/8 heads of 128 in bf16, normed, 168 MB in 32.5 us
+// (5.2 TB/s; 27.5 where the inputs are in the last-level cache; without the next round's heads
+// on their way and one set of gains for both sides 34.1 and 29.7), by a launch and its chain of
+// loads with few: one token 2.7 us, 192 tokens of 20/5 heads in fp32 3.9 (a wave per round of
+// heads there).
 #include "attention.hpp"
 
 namespace bl {
@@ -57,42 +62,60 @@ __device__ inline float2 turn(int64_t position, float freq)
     return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter >= 2 ? -b : b);
 }
 
+// 1 / sqrt(v): the hardware's (1 ulp) and a step of Newton's; by its definition in lanes whose v
+// may be below the numbers that the hardware takes, or is none (a head's bits do not depend on
+// another's)
+__device__ inline float inverse_root(float v)
+{
+    const float r = __builtin_amdgcn_rsqf(v);
+    const float fine = __builtin_fmaf(0.5f * r, __builtin_fmaf(-v * r, r, 1.0f), r);
+    const bool usual = v >= 1e-30f && v <= 1e38f;
+    if (__any(!usual)) return usual ? fine : 1.0f / sqrtf(v);
+    return fine;
+}
+
 template <typename T, int D, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int first)
 {
     constexpr int E = 16 / sizeof(T);  // elements of a piece
     constexpr int LANES = D / (2 * E);  // of a head
-    constexpr int HEADS = 64 / LANES;   // of a wave at once
+    constexpr int HEADS = 64 / LANES;   // of a wave at once: a round
     __shared__ __align__(16) float2 turns[4][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t item = ((int64_t)first + blockIdx.x) * 4 + wave;
     const int64_t row = item / a.parts;
     const int part = (int)(item - row * a.parts);
     if (row >= a.m) return;
-    int seq, place, begin;
-    if (!find_row(a.cu, a.begin, a.seqs, a.m, row, seq, place, begin) || begin < 0) return;  // negative: an unused slot
-    const int slot = lane % LANES, heads = a.q_heads + a.kv_heads;
+    const int slot = lane % LANES;
     const bool rotary = slot * E < a.pairs;
     // elements of a lane: `lo` .. lo+E-1 and `hi` .. hi+E-1 of the head
     const int lo = INTERLEAVED ? 2 * E * slot : rotary ? E * slot : 2 * E * slot;
     const int hi = INTERLEAVED ? lo + E : rotary ? a.pairs + lo : lo + E;
 
-    float gq[2 * E], gk[2 * E];
-    auto gains = [&](const float *g, float (&out)[2 * E]) {
-#pragma unroll
-        for (int i = 0; i < E; i += 4) {
-            const v4f u = g ? *reinterpret_cast<const v4f *>(g + lo + i) : v4f{1.0f, 1.0f, 1.0f, 1.0f};
-            const v4f v = g ? *reinterpret_cast<const v4f *>(g + hi + i) : v4f{1.0f, 1.0f, 1.0f, 1.0f};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                out[i + j] = u[j];
-                out[E + i + j] = v[j];
-            }
-        }
+    // rounds 0 .. q_rounds-1 are of q, the others of k; a round is on its way while the one before is worked on
+    const int q_rounds = (a.q_heads + HEADS - 1) / HEADS, rounds = q_rounds + (a.kv_heads + HEADS - 1) / HEADS;
+    struct Round {
+        int head;
+        bool is_q, there;
+        uint4 lo, hi;
     };
-    gains(a.q_gain, gq);
-    gains(a.k_gain, gk);
+    auto load = [&](int i) {
+        Round r;
+        r.is_q = i < q_rounds;
+        r.head = (r.is_q ? i : i - q_rounds) * HEADS + lane / LANES;
+        r.there = r.head < (r.is_q ? a.q_heads : a.kv_heads);
+        r.lo = r.hi = make_uint4(0, 0, 0, 0);
+        if (r.there) {
+            const T *src = static_cast<const T *>(r.is_q ? a.q : a.k) + row * (r.is_q ? a.q_stride : a.k_stride) + (int64_t)r.head * D;
+            r.lo = *reinterpret_cast<const uint4 *>(src + lo);
+            r.hi = *reinterpret_cast<const uint4 *>(src + hi);
+        }
+        return r;
+    };
+    Round next = load(part);
 
+    int seq, place, begin;
+    if (!find_row(a.cu, a.begin, a.seqs, a.m, row, seq, place, begin) || begin < 0) return;  // negative: an unused slot
     if (lane < a.pairs) {
         const float2 t = turn((int64_t)begin + place, a.inv_freq[lane]);
         turns[wave][lane] = make_float2(t.x * a.magnitude, t.y * a.magnitude);
@@ -107,44 +130,51 @@ __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int first)
         si[i] = t.y;
     }
 
-    for (int h0 = part * HEADS; h0 < heads; h0 += a.parts * HEADS) {
-        const int h = h0 + lane / LANES;
-        const bool there = h < heads, is_q = h < a.q_heads;
-        const int at = is_q ? h : h - a.q_heads;
-        T x[2 * E];
-        const T *src = static_cast<const T *>(is_q ? a.q : a.k) + row * (is_q ? a.q_stride : a.k_stride) + (int64_t)at * D;
-        if (there) {
-            *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(src + lo);
-            *reinterpret_cast<uint4 *>(x + E) = *reinterpret_cast<const uint4 *>(src + hi);
+    float gain[2 * E];
+    const float *held = nullptr;  // whose elements `gain` has
+    for (int i = part; i < rounds; i += a.parts) {
+        const Round r = next;
+        if (i + a.parts < rounds) next = load(i + a.parts);
+        const float *g = r.is_q ? a.q_gain : a.k_gain;
+        if (g && g != held) {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                *reinterpret_cast<v4f *>(gain + e) = *reinterpret_cast<const v4f *>(g + lo + e);
+                *reinterpret_cast<v4f *>(gain + E + e) = *reinterpret_cast<const v4f *>(g + hi + e);
+            }
+            held = g;
         }
+        T x[2 * E];
+        *reinterpret_cast<uint4 *>(x) = r.lo;
+        *reinterpret_cast<uint4 *>(x + E) = r.hi;
         float f[2 * E];
 #pragma unroll
-        for (int i = 0; i < 2 * E; ++i) f[i] = there ? to_f32(x[i]) : 0.0f;
-        if ((is_q ? a.q_gain : a.k_gain) != nullptr) {
+        for (int e = 0; e < 2 * E; ++e) f[e] = to_f32(x[e]);
+        if (g) {
             float ss = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2 * E; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
+            for (int e = 0; e < 2 * E; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
             ss += __int_as_float(dpp_mov<kDppQuadXor1>(__float_as_int(ss)));
             ss += __int_as_float(dpp_mov<kDppQuadXor2>(__float_as_int(ss)));
             if constexpr (LANES >= 8) ss += __int_as_float(dpp_mov<kDppRowHalfMirror>(__float_as_int(ss)));
             if constexpr (LANES >= 16) ss += __int_as_float(dpp_mov<kDppRowMirror>(__float_as_int(ss)));
-            const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+            const float s = inverse_root(ss * (1.0f / D) + a.eps);
 #pragma unroll
-            for (int i = 0; i < 2 * E; ++i) f[i] = (f[i] * r) * (is_q ? gq[i] : gk[i]);
+            for (int e = 0; e < 2 * E; ++e) f[e] = (f[e] * s) * gain[e];
         }
         if (rotary) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                float &u = f[INTERLEAVED ? 2 * i : i], &v = f[INTERLEAVED ? 2 * i + 1 : E + i];
+            for (int e = 0; e < E; ++e) {
+                float &u = f[INTERLEAVED ? 2 * e : e], &v = f[INTERLEAVED ? 2 * e + 1 : E + e];
                 const float a0 = u, b0 = v;
-                u = __builtin_fmaf(a0, co[i], -(b0 * si[i]));
-                v = __builtin_fmaf(b0, co[i], a0 * si[i]);
+                u = __builtin_fmaf(a0, co[e], -(b0 * si[e]));
+                v = __builtin_fmaf(b0, co[e], a0 * si[e]);
             }
         }
-        if (!there) continue;
+        if (!r.there) continue;
 #pragma unroll
-        for (int i = 0; i < 2 * E; ++i) store_out(&x[i], f[i]);
-        T *dst = static_cast<T *>(is_q ? a.q_out : a.k_out) + row * (is_q ? a.q_out_stride : a.k_out_stride) + (int64_t)at * D;
+        for (int e = 0; e < 2 * E; ++e) store_out(&x[e], f[e]);
+        T *dst = static_cast<T *>(r.is_q ? a.q_out : a.k_out) + row * (r.is_q ? a.q_out_stride : a.k_out_stride) + (int64_t)r.head * D;
         *reinterpret_cast<uint4 *>(dst + lo) = *reinterpret_cast<const uint4 *>(x);
         *reinterpret_cast<uint4 *>(dst + hi) = *reinterpret_cast<const uint4 *>(x + E);
     }
@@ -158,8 +188,9 @@ hipError_t launch_rotate(const RotateProblem &p, hipStream_t st)
     a.m = p.m; a.q_heads = (int)p.q_heads; a.kv_heads = (int)p.kv_heads; a.seqs = (int)p.seqs; a.pairs = (int)p.rotary_dim / 2;
     a.cu = p.cu; a.begin = p.begin; a.inv_freq = p.inv_freq; a.q_gain = p.q_gain; a.k_gain = p.k_gain;
     a.eps = p.eps; a.magnitude = p.magnitude;
-    // few tokens: a wave for every 64 lanes' worth of heads
-    const int64_t rounds = ceil_div((p.q_heads + p.kv_heads) * p.head_dim * (p.bf16 ? 2 : 4), 64 * 32);
+    // few tokens: a wave for every round of heads
+    const int64_t per_round = 64 * 32 / (p.head_dim * (p.bf16 ? 2 : 4));
+    const int64_t rounds = ceil_div(p.q_heads, per_round) + ceil_div(p.kv_heads, per_round);
     a.parts = p.m * rounds <= 2048 ? (int)rounds : 1;
     in_launches(ceil_div(p.m * a.parts, 4), [&](int first, unsigned n) {
         auto go = [&](auto type, auto width) {

@@ -113,6 +113,9 @@ def test_rotate_values_that_are_not_finite_stay_in_their_head(bl):  # noqa: F811
     for c, y, b in zip(clean, dirty, bad):
         assert torch.equal(c[~b], y[~b]) and not torch.isfinite(y[b]).all()
     assert torch.isnan(dirty[0][1, 2]).all()
+    q[0, 0, 7] = 3e20  # its square passes fp32's range: the head's factor is 0
+    huge = bl.rotate(q, k, f, at, cu, q_gain=gain, k_gain=gain)
+    assert (huge[0][0, 0] == 0).all() and torch.equal(huge[0][0, 1:], clean[0][0, 1:])
     zero = bl.rotate(torch.zeros_like(q), torch.zeros_like(k), f, at, cu, q_gain=gain, k_gain=gain)
     assert (zero[0] == 0).all() and (zero[1] == 0).all()
 
