@@ -14,11 +14,12 @@
 // and the remainder, less the multiple of pi / 2 next to it (two constants, 106 bits of
 // pi / 2), so positions up to 2^31 cost no digits; its cosine and sine are rounded to fp32.
 //
-// Bound by HBM with many tokens: 8192 of 32/8 heads of 128 in bf16, normed, 168 MB in 32.5 us
-// (5.2 TB/s; 27.5 where the inputs are in the last-level cache; without the next round's heads
-// on their way and one set of gains for both sides 34.1 and 29.7), by a launch and its chain of
-// loads with few: one token 2.7 us, 192 tokens of 20/5 heads in fp32 3.9 (a wave per round of
-// heads there).
+// Bound by HBM with many tokens: 8192 of 32/8 heads of 128 in bf16, normed, 168 MB in 31 us
+// (5.4 TB/s; without the next round's heads on their way and one set of gains for both sides
+// 5 % more), by a launch and its chain of loads with few: one token 2.7 us, 192 tokens of 20/5
+// heads in fp32 3.9 (a wave per round of heads there). The loads pass the caches by, which
+// keep what is stored for the append and the attention that read it: 31.1 us beside 36.6 with
+// plain loads, with an append behind it 45.2 beside 46.3 (with stores that pass them by too 50.5).
 #include "attention.hpp"
 
 namespace bl {
@@ -107,8 +108,8 @@ __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int first)
         r.lo = r.hi = make_uint4(0, 0, 0, 0);
         if (r.there) {
             const T *src = static_cast<const T *>(r.is_q ? a.q : a.k) + row * (r.is_q ? a.q_stride : a.k_stride) + (int64_t)r.head * D;
-            r.lo = *reinterpret_cast<const uint4 *>(src + lo);
-            r.hi = *reinterpret_cast<const uint4 *>(src + hi);
+            r.lo = load_nt16(src + lo);
+            r.hi = load_nt16(src + hi);
         }
         return r;
     };
