@@ -9,8 +9,10 @@
 namespace bl {
 
 // What the kernels of this file walk over: a sequence's whole table; the blocks listed
-// for one row; the whole table, to be joined with the results of a shared prefix.
-enum CachedMode { kWhole, kSelected, kBehindPrefix };
+// for one row (kSelectedPast: read past the caches); the whole table, to be joined with the
+// results of a shared prefix.
+enum CachedMode { kWhole, kSelected, kSelectedPast, kBehindPrefix };
+constexpr bool listed(CachedMode m) { return m == kSelected || m == kSelectedPast; }
 
 constexpr float kDigitMax = 8355711.0f;  // 0x7F7F7F: every digit within -128..127
 
@@ -67,7 +69,7 @@ struct CachedArgs {
     float *part_ml;   // [splits][m * q_heads][2]: reference exponent, sum
     float *stat;      // [m * q_heads][max_blocks][2]: a page's largest exponent, sum
     float *final_ml;  // [m * q_heads][2]: a row's reference exponent, 1 / sum (0: adds no weight)
-    // kSelected: [m][kv_heads][keep] blocks
+    // listed: [m][kv_heads][keep] blocks
     const int32_t *selected;
     int64_t keep;
     // kBehindPrefix: the prefix's parts, laid out as part_o and part_ml, and what gives their number
@@ -98,13 +100,13 @@ __device__ inline int prefix_parts(const CachedArgs &a)
 }
 
 // tiles of 4*RT query rows: row r of a sequence is token r / group, head r % group.
-// kSelected: a token's tiles hold no rows of the next one, whose blocks are others; t is
+// Listed: a token's tiles hold no rows of the next one, whose blocks are others; t is
 // that token alone, `tok` its place in the sequence
 template <int RT, CachedMode MODE>
 __device__ inline bool find_rows(const CachedArgs &a, int idx, SeqTile &t, int &tok)
 {
     tok = 0;
-    if (MODE == kSelected && a.cu) {
+    if (listed(MODE) && a.cu) {
         t.begin = idx / a.tiles_per_seq;
         t.tile = idx % a.tiles_per_seq;
         t.n = 1;
@@ -127,6 +129,13 @@ __device__ inline bool find_rows(const CachedArgs &a, int idx, SeqTile &t, int &
 
 // what a row adds to the blocks' weights: nothing if it sees nothing or is not finite
 __device__ inline float2 final_of(float top, float l) { return make_float2(top, l > 0.0f ? 1.0f / l : 0.0f); }
+
+template <CachedMode MODE>
+__device__ inline v4i codes_at(const uint4 *p)
+{
+    if constexpr (MODE == kSelectedPast) return __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p));
+    else return *reinterpret_cast<const v4i *>(p);
+}
 
 // words of LDS that a workgroup of attention_cached_tile needs: digits of q in operand
 // order, [row tile][step][lane][16 bytes]; per wave the digits of p, [16 rows][16 dwords of
@@ -153,12 +162,12 @@ __device__ inline void attention_cached_tile(const CachedArgs &a, int idx, int h
     int at_tok;
     if (!find_rows<RT, MODE>(a, idx, t, at_tok)) return;
     const int32_t *table = a.table + (int64_t)t.seq * a.max_blocks;
-    const int32_t *chosen = MODE == kSelected ? a.selected + (t.begin * a.kv_heads + head) * a.keep : nullptr;
+    const int32_t *chosen = listed(MODE) ? a.selected + (t.begin * a.kv_heads + head) * a.keep : nullptr;
     // one split: the wave's pages do not depend on the length, which is on its way
-    int ids = -1, blocks = 0;  // kSelected: which block of the sequence a page is
-    if (MODE != kSelected && a.splits == 1 && wave + W * lane < a.max_blocks) ids = table[wave + W * lane];
+    int ids = -1, blocks = 0;  // listed: which block of the sequence a page is
+    if (!listed(MODE) && a.splits == 1 && wave + W * lane < a.max_blocks) ids = table[wave + W * lane];
     const int64_t have = a.lens[t.seq] + (int64_t)at_tok;
-    const int npages = MODE == kSelected ? (int)a.keep : pages_of(have, t.n, a.max_blocks);
+    const int npages = listed(MODE) ? (int)a.keep : pages_of(have, t.n, a.max_blocks);
     const int chunk = pages_per_split(npages, a.splits, W);
     const int p0 = split * chunk, p1 = p0 + chunk < npages ? p0 + chunk : npages;
     if (p0 >= npages && split > 0) return;  // the join knows; split 0 writes rows that see nothing
@@ -177,7 +186,7 @@ __device__ inline void attention_cached_tile(const CachedArgs &a, int idx, int h
     float my_ks = 0.0f, my_vs = 0.0f;
     auto fetch_ids = [&](int base) {
         const int mine = base + W * lane;
-        if constexpr (MODE == kSelected) {
+        if constexpr (listed(MODE)) {
             blocks = mine < p1 ? chosen[mine] : -1;
             // entries that name no block, or one behind the row, hold nothing that it sees
             const bool sees = blocks >= 0 && blocks < a.max_blocks && (int64_t)blocks * kBlock <= have;
@@ -201,7 +210,7 @@ __device__ inline void attention_cached_tile(const CachedArgs &a, int idx, int h
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-            for (int h = 0; h < H; ++h) kf[tt][h] = *reinterpret_cast<const v4i *>(kp + (tt * H + h) * 64);
+            for (int h = 0; h < H; ++h) kf[tt][h] = codes_at<MODE>(kp + (tt * H + h) * 64);
     };
     // K of a page is asked for as soon as the one before has been used, the first while
     // the query rows are made ready (one token over 1024, 20/5 heads: 6.3 us beside 6.7);
@@ -299,15 +308,15 @@ __device__ inline void attention_cached_tile(const CachedArgs &a, int idx, int h
         for (int p = base, i = 0; p < p1 && i < 64; p += W, ++i) {
             bool there;
             const uint4 *vp = reinterpret_cast<const uint4 *>(a.v_codes + page_at(i, there)) + lane;
-            if (MODE == kSelected && !there) {
+            if (listed(MODE) && !there) {
                 if (EARLY && p + W < p1 && i < 63) load_k(i + 1);
                 continue;
             }
-            const int block = MODE == kSelected ? __builtin_amdgcn_readlane(blocks, i) : p;
+            const int block = listed(MODE) ? __builtin_amdgcn_readlane(blocks, i) : p;
             if (!EARLY) load_k(i);
             v4i vf[N];
 #pragma unroll
-            for (int n = 0; n < N; ++n) vf[n] = *reinterpret_cast<const v4i *>(vp + n * 64);
+            for (int n = 0; n < N; ++n) vf[n] = codes_at<MODE>(vp + n * 64);
             const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_ks), i)) / 127.0f;
             const float vs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_vs), i)) / 127.0f;
 #pragma unroll
@@ -521,7 +530,7 @@ __global__ __launch_bounds__(512) void attention_join_kernel(CachedArgs a, float
     }
     const int64_t have = a.lens[t.seq];
     if (have < 0) return;
-    const int own = parts_of(MODE == kSelected ? (int)a.keep : pages_of(have, t.n, a.max_blocks), a.splits, a.waves);
+    const int own = parts_of(listed(MODE) ? (int)a.keep : pages_of(have, t.n, a.max_blocks), a.splits, a.waves);
     const int parts = MODE == kBehindPrefix ? own + prefix_parts(a) : own;
     const float2 *own_ml = reinterpret_cast<const float2 *>(a.part_ml) + row;
     const float *own_o = a.part_o + row * D + dim;
@@ -694,7 +703,7 @@ inline void launch_tiles(const CachedProblem &p, const CachedArgs &a, const Shap
             }
             hipLaunchKernelGGL((attention_cached_kernel<T, D, RT, W, false, MODE>), grid, dim3(64 * W), 0, st, a, first);
         }, kMostInZ);
-        if (a.splits > 1) launch_join<MODE, T, D>(p, a, a.splits, st);
+        if (a.splits > 1) launch_join<MODE == kSelectedPast ? kSelected : MODE, T, D>(p, a, a.splits, st);
     };
     auto go = [&](auto type, auto width, auto tiles) {
         constexpr int RT = decltype(tiles)::value;

@@ -45,7 +45,12 @@ hipError_t launch_attention_selected(const SelectedProblem &p, void *ws, hipStre
         a.part_o = static_cast<float *>(ws);
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(ws) + selected_layout(r).part_ml);
     }
-    launch_tiles<kSelected>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, st);
+    // Lists of more than a quarter of the last-level cache are read past it (40 tokens' 32 blocks
+    // of 32/8 heads of 128, 168 MB: 33.4 us beside 38.7); shorter ones may be in it still (one
+    // token's 64 blocks, 8 MB read again: 10.7 us beside 10.0)
+    const int64_t bytes = p.c.m * p.c.kv_heads * p.keep * 2 * kBlock * p.c.head_dim;
+    if (bytes >= (int64_t)64 << 20) launch_tiles<kSelectedPast>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, st);
+    else launch_tiles<kSelected>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, st);
     return hipGetLastError();
 }
 

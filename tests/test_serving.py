@@ -517,21 +517,22 @@ def test_selected_all_blocks_is_attention_over_the_cache(bl):  # noqa: F811
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_selected_long_lists_of_many_rows(bl, dtype):  # noqa: F811
-    """So many rows that one workgroup has a whole list and a wave more than 64 of its blocks: every row as in a batch of a
-    few, whose lists are split."""
+    """So many rows that one workgroup has a whole list and a wave more than 64 of its blocks, and some whose lists are
+    split, both read past the caches: every row as in a batch of a few."""
     c = _Paged(bl, [1200], [1], 2, 64, 8)
     c.table = np.tile(c.table, (1, 20))
     few = _rand((3, 4, 64), 5, DTYPES[dtype], 1.5)
     lists = torch.tensor(np.random.default_rng(3).integers(-1, c.table.shape[1], (3, 2, 300)), dtype=torch.int32).cuda()
     out = []
-    for m in (300, 3):
+    for m in (300, 40, 3):
         i = torch.arange(m, device="cuda") % 3
         out.append(bl.attention_selected(few[i].contiguous(), c.cache, _i32(c.table).expand(m, -1).contiguous(), _i32([64 * 300] * m),
                                          lists[i].contiguous()))
-    for i in range(3):
-        assert (out[0][i::3] == out[0][i]).all()
-    off = (out[0][:3].float() - out[1].float()).abs().max() / out[1].float().abs().max()
-    assert off < (2.0**-7 if dtype == "bf16" else 2e-5)
+    for many in out[:2]:
+        for i in range(3):
+            assert (many[i::3] == many[i]).all()
+        off = (many[:3].float() - out[2].float()).abs().max() / out[2].float().abs().max()
+        assert off < (2.0**-7 if dtype == "bf16" else 2e-5)
 
 
 def test_selected_rows_that_are_not_finite(bl):  # noqa: F811
