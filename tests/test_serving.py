@@ -572,6 +572,28 @@ def test_offsets_past_32_bits(bl):  # noqa: F811
 
 # ---------------------------------------------------------------- the calls themselves
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_outside_the_sequences(bl, dtype):  # noqa: F811
+    """Rows before the first and behind the last sequence, NaN among them: not written, and nothing of them enters."""
+    c, prefix = _behind(bl)
+    q = _rand((11, 8, 64), 3, DTYPES[dtype])
+    inner = q[2:7].contiguous()
+    q[:2], q[7:] = float("nan"), float("inf")
+    table, lens, cu, inside = _i32(c.table), _i32([70, 3]), _i32([2, 4, 7]), _starts([2, 3])
+    sel = _i32(np.random.default_rng(1).integers(-1, c.wide, (11, 2, 3)))
+    bounds = bl.bounds_alloc(c.cache)
+    bl.cache_bounds(c.cache, bounds, table, _i32([0, 0]), _starts([72, 6]), 78)
+    for call, shape, fill in (
+        (lambda x, s, o, off: bl.attention_shared(x, c.cache, _i32(prefix), _i32([150]), table, lens, off, out=o), (512,), 7.0),
+        (lambda x, s, o, off: bl.attention_selected(x, c.cache, table, lens, s, off, out=o), (512,), 7.0),
+        (lambda x, s, o, off: bl.block_select(x, bounds, c.cache.k_scale, table, lens, 1, off, out=o), (2, 1), 7),
+    ):
+        type_ = torch.int32 if isinstance(fill, int) else DTYPES[dtype]
+        out = call(q, sel, torch.full((11, *shape), fill, dtype=type_, device="cuda"), cu)
+        alone = call(inner, sel[2:7].contiguous(), torch.full((5, *shape), fill, dtype=type_, device="cuda"), inside)
+        assert torch.equal(out[2:7], alone) and (out[:2] == fill).all() and (out[7:] == fill).all()
+
+
 def test_binding_refusals(bl):  # noqa: F811
     """What the tensors themselves get wrong, before anything is enqueued."""
     q, k = _rand((6, 4, 64), 1, torch.bfloat16), _rand((6, 2, 64), 2, torch.bfloat16)
