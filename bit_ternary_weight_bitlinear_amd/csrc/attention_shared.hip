@@ -401,16 +401,19 @@ __global__ __launch_bounds__(64 * kPrefixWaves, 2) void attention_shared_kernel(
 // ---------------------------------------------------------------- launcher
 
 // Workgroups per unit, a tile of rows and a kv head: of the prefix, and of the sequences' own
-// pages, each about one per CU in all and with a page per wave at least
+// pages, about `target` in all and with a page per wave at least
 static int64_t splits_of(int64_t units, int64_t blocks, int64_t target)
 {
     const int64_t most = ceil_div(blocks, kPrefixWaves), s = target / units < most ? target / units : most;
     return s < 1 ? 1 : s > 256 ? 256 : s;
 }
+// About one per CU
 static int64_t prefix_splits(const SharedProblem &p)
 {
     return splits_of(ceil_div(p.c.m * (p.c.q_heads / p.c.kv_heads), kPrefixRows) * p.c.kv_heads, p.prefix_blocks, 256);
 }
+// Two per CU: 64 rows of 32/8 heads behind 16384 tokens take 41.1 us in all, with
+// a target of 256 41.9 and of 1024 43.7
 static int64_t own_splits(const CachedProblem &c)
 {
     return splits_of(units_of(c, row_tiles(c)), c.max_blocks, 512);
