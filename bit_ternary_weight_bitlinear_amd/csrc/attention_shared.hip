@@ -108,9 +108,21 @@ __device__ inline float page_weights(v16f (&s)[2], float f, int left, int half, 
 #pragma unroll
         for (int r = 0; r < 16; ++r) big = fmaxf(big, s[t][r]);
     big = fmaxf(big, __shfl_xor(big, 32));
-    // raised by more than the rounding of its difference to 15, so that no weight passes 2^15
-    const float ref = left > 0 ? ceilf(__builtin_fmaf(fabsf(big), 0x1p-22f, big)) : kNegInf;
-    const float shift = left > 0 ? 15.0f - ref : 0.0f;
+    // No weight passes 2^15: below 2^22 the difference to 15 is exact, and a sum with it that rounds
+    // rounds to 15 at most. Beyond, where it would not be, the logits lose their reference before
+    // (exact near it), and are raised by 15 then.
+    const float ref = ceilf(big);
+    float shift = ref == kNegInf ? 0.0f : 15.0f - ref;
+    const bool far = fabsf(ref) >= 0x1p22f && ref != kNegInf;
+    if (__any(far)) {
+        asm volatile("");  // a branch, not 32 more differences
+        const float less = far ? ref : 0.0f;
+        shift = far ? 15.0f : shift;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[t][r] -= less;
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
