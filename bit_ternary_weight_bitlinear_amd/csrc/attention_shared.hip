@@ -15,8 +15,7 @@
 // of two at or above their page's and row's largest, times 2^15: rounded to fp16 (2^-11)
 // for bf16 results, in two parts (2^-22) for fp32 ones; their sum is that of the rounded
 // weights, by a product with ones. Sums are fp32, a page's scaled by its V scale when they are
-// added to the row's; for bf16 results V's codes are raised by 128 in them and the weights'
-// sum times 128 taken off at the end (their roundings count as of codes of 256).
+// added to the row's.
 //
 // Layout: S^T = K Q^T has a query row per lane and 32 of a page's 64 tokens in its two
 // times 16 registers, which after the exponential are the second operand of O^T = V^T P^T
@@ -56,10 +55,7 @@ struct PrefixArgs {
     float *part_o, *part_ml;
 };
 
-// Eight codes as fp16. EXACT: 1024 + (code + 128) is the bits 0x6400 with the biased code in
-// the low byte. Otherwise those alone, (code + 128) 2^-24: three instructions instead of five for
-// four codes, and a product with them is 2^-24 (sum + 128 * the sum of the other factor).
-template <bool EXACT>
+// Eight codes as fp16: 1024 + (code + 128) is the bits 0x6400 with the biased code in the low byte.
 __device__ inline v8h codes_f16(uint32_t lo, uint32_t hi)
 {
     union {
@@ -67,7 +63,7 @@ __device__ inline v8h codes_f16(uint32_t lo, uint32_t hi)
         v2h h[4];
         v8h v;
     } u;
-    constexpr uint32_t kTop = EXACT ? 0x64646464u : 0u;
+    constexpr uint32_t kTop = 0x64646464u;
     lo ^= 0x80808080u;
     hi ^= 0x80808080u;
     u.w[0] = __builtin_amdgcn_perm(kTop, lo, 0x04010400u);
@@ -75,9 +71,8 @@ __device__ inline v8h codes_f16(uint32_t lo, uint32_t hi)
     u.w[2] = __builtin_amdgcn_perm(kTop, hi, 0x04010400u);
     u.w[3] = __builtin_amdgcn_perm(kTop, hi, 0x04030402u);
     const v2h bias = {(_Float16)-1152.0f, (_Float16)-1152.0f};
-    if constexpr (EXACT)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u.h[i] += bias;
+    for (int i = 0; i < 4; ++i) u.h[i] += bias;
     return u.v;
 }
 
@@ -199,7 +194,6 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
 {
     constexpr int W = kPrefixWaves, R = kPrefixRows;
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
-    constexpr bool EXACT = PARTS == 2;
     constexpr int U = D / 32;  // pairs of 16-dim pieces of K; 32-dim tiles of the output
     constexpr int kStride = PrefixLds<D, PARTS>::stride;
     v8h *qh = reinterpret_cast<v8h *>(lds);  // [part][2 * pair + s][lane], in operand order
@@ -250,7 +244,7 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
     __syncthreads();
     const bool poor = !(row_scale[col] == row_scale[col]);
     const float qs = poor ? 0.0f : row_scale[col];
-    float top = kNegInf, sum = 0.0f, bias = 0.0f;  // bias: what the biased codes of V added to acc
+    float top = kNegInf, sum = 0.0f;
     v16f acc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -294,7 +288,7 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const uint4 c = kf[t][u >> 1];
-                    const v8h k8 = u & 1 ? codes_f16<true>(c.z, c.w) : codes_f16<true>(c.x, c.y);
+                    const v8h k8 = u & 1 ? codes_f16(c.z, c.w) : codes_f16(c.x, c.y);
                     if constexpr (PARTS == 2) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q1, s[t], 0, 0, 0);
                     s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, q0, s[t], 0, 0, 0);
                 }
@@ -309,7 +303,6 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
                 asm volatile("");  // a branch, not 64 products and a choice
                 const float keep = __builtin_amdgcn_exp2f(top - to);
                 sum *= keep;
-                bias *= keep;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -329,7 +322,6 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
 #pragma unroll
                 for (int b = 0; b < 2; ++b) all = product(ones, t, b, all);
             sum = __builtin_fmaf(all[0], add, sum);
-            if (!EXACT) bias = __builtin_fmaf(all[0], g, bias);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 v16f o;
@@ -339,7 +331,7 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
-                        o = product(b ? codes_f16<EXACT>(vf[u][t].z, vf[u][t].w) : codes_f16<EXACT>(vf[u][t].x, vf[u][t].y), t, b, o);
+                        o = product(b ? codes_f16(vf[u][t].z, vf[u][t].w) : codes_f16(vf[u][t].x, vf[u][t].y), t, b, o);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[u][r] = __builtin_fmaf(o[r], g, acc[u][r]);
             }
@@ -349,14 +341,13 @@ __device__ inline void attention_prefix_tile(const PrefixArgs &a, int64_t tile, 
     // ---- join the waves, in wave order
     __syncthreads();
     float *jo = reinterpret_cast<float *>(lds);  // [wave][row][kStride]
-    const float less = 128.0f * bias;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int r = 0; r < 16; r += 4) {
             v4f o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = EXACT ? acc[u][r + i] : __builtin_fmaf(acc[u][r + i], 0x1p24f, -less);
+            for (int i = 0; i < 4; ++i) o[i] = acc[u][r + i];
             *reinterpret_cast<v4f *>(jo + (wave * R + col) * kStride + 32 * u + 2 * r + 4 * half) = o;
         }
     if (half == 0) jm[wave][col] = make_float2(top, poor ? __builtin_nanf("") : sum);

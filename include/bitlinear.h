@@ -517,10 +517,10 @@ size_t bitlinear_attention_shared_workspace_size(int64_t m, int64_t q_heads, int
  * Over the prefix q is held to 2^-22 of itself (fp32; elements below 2^-17 of their
  * row's largest, or of 1e-30, to 2^-39 of that) or exactly (bf16, to 2^-39 of the
  * largest), and the softmax weights to 2^-22 (fp32) or 2^-11 (bf16) of themselves, or 2^-39
- * of the largest of their block and row; sums are fp32 (bf16: those of values round, and
- * pass fp32's range, as if a block's codes of V were 256). The rest is as in bitlinear_attention_cached: rows that
- * see nothing, rows of q that are not finite, unused slots and rows outside the sequences
- * among it. Results do not depend on the order of execution.
+ * of the largest of their block and row; sums are fp32. The rest is as in
+ * bitlinear_attention_cached: rows that see nothing, rows of q that are not finite, logits or
+ * sums that pass fp32's range, unused slots and rows outside the sequences among it. Results
+ * do not depend on the order of execution.
  * BL_ERR_SHAPE also where m * q_heads / kv_heads passes 2^31 - 1024.
  *   workspace  >= bitlinear_attention_shared_workspace_size() bytes
  */

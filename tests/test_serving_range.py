@@ -130,3 +130,23 @@ def test_shared_infinite_keys(bl, bad, dtype):  # noqa: F811
     for h in takes:
         off = (got.view(8, d)[h].float() - held[h // 4]).abs()
         assert (off <= (2.0**-20 + HALF[dtype]) * held[h // 4].abs() + 1e-30).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, 1e37])
+def test_shared_infinite_values(bl, bad, dtype):  # noqa: F811
+    """An infinity of V, held as the largest finite number, and a large one: what the other dims hold is theirs still, as in
+    attention over the whole cache."""
+    hkv, d, n = 2, 64, 500
+    k, v = (_rand((n, hkv, d), i, DTYPES[dtype]) for i in (1, 2))
+    v[200, :, 5] = bad
+    table = _i32(np.random.default_rng(1).permutation(8)[None])
+    cache = _split(bl, k, v, table, 8, n, hkv, d)
+    q = _rand((1, 8, d), 3, DTYPES[dtype])
+    got = bl.attention_shared(q, cache, table[0, :6].contiguous(), _i32([384]), table[:, 6:].contiguous(), _i32([n - 1 - 384])).view(8, d)
+    whole = bl.attention_cached(q, cache, table, _i32([n - 1])).view(8, d)
+    rest = torch.arange(d, device="cuda") != 5
+    assert torch.isfinite(whole[:, rest]).all()
+    rel = 2**-7 if dtype == "bf16" else 2e-5
+    np.testing.assert_allclose(_np(got)[:, rest.cpu().numpy()], _np(whole)[:, rest.cpu().numpy()], rtol=rel, atol=rel * float(whole[:, rest].abs().max()))
+    np.testing.assert_allclose(_np(got)[:, 5], _np(whole)[:, 5], rtol=rel)
