@@ -503,7 +503,7 @@ __device__ inline void add_weights(const CachedArgs &a, int s, int chunk64, floa
 constexpr int kFewSplits = 16;
 
 template <typename T, int D, bool FEW, CachedMode MODE = kWhole>
-__global__ __launch_bounds__(512) void attention_join_kernel(CachedArgs a, float *__restrict__ weights, int blocks64)
+__global__ __launch_bounds__(512) void attention_join_kernel(CachedArgs a, float *__restrict__ weights, int blocks64, int64_t first)
 {
     constexpr int G = 512 / D;
     __shared__ float factor[512], jo[512];
@@ -511,12 +511,13 @@ __global__ __launch_bounds__(512) void attention_join_kernel(CachedArgs a, float
     __shared__ float2 fin[128];
     const int tid = threadIdx.x, wave = tid >> 6, dim = tid % D;
     const int64_t total_rows = a.m * a.q_heads, groups = FEW ? (total_rows + G - 1) / G : total_rows;
-    if (blockIdx.x >= groups) {
-        const int w = (int)(blockIdx.x - groups);
+    const int64_t group = first + blockIdx.x;
+    if (group >= groups) {
+        const int w = (int)(group - groups);
         add_weights<8, true>(a, w / blocks64, w % blocks64, weights, fin, jo);
         return;
     }
-    const int64_t row = FEW ? (int64_t)blockIdx.x * G + tid / D : blockIdx.x;
+    const int64_t row = FEW ? group * G + tid / D : group;
     if (row >= total_rows) return;
     SeqTile t;
     const int tok = (int)(row / a.q_heads);
@@ -673,17 +674,19 @@ inline CachedArgs cached_args(const CachedProblem &p, const Shape &shape, int rt
     return a;
 }
 
-// The joining launch; most_parts: a bound of the results that it joins
+// The joining launch (launches, where there are more rows than one may have threads for);
+// most_parts: a bound of the results that it joins
 template <CachedMode MODE, typename T, int D>
 inline void launch_join(const CachedProblem &p, const CachedArgs &a, int64_t most_parts, hipStream_t st)
 {
+    const bool few = most_parts <= kFewSplits;
     const int64_t rows = p.m * p.q_heads, blocks64 = ceil_div(p.max_blocks, 64), extra = p.weights ? p.seqs * blocks64 : 0;
-    if (most_parts <= kFewSplits)
-        hipLaunchKernelGGL((attention_join_kernel<T, D, true, MODE>), dim3((unsigned)(ceil_div(rows, 512 / D) + extra)), dim3(512), 0, st, a,
-                           p.weights, (int)blocks64);
-    else
-        hipLaunchKernelGGL((attention_join_kernel<T, D, false, MODE>), dim3((unsigned)(rows + extra)), dim3(512), 0, st, a, p.weights,
-                           (int)blocks64);
+    const int64_t groups = (few ? ceil_div(rows, 512 / D) : rows) + extra;
+    for (int64_t first = 0; first < groups; first += kMostGroups) {
+        const dim3 grid((unsigned)(groups - first < kMostGroups ? groups - first : kMostGroups));
+        if (few) hipLaunchKernelGGL((attention_join_kernel<T, D, true, MODE>), grid, dim3(512), 0, st, a, p.weights, (int)blocks64, first);
+        else hipLaunchKernelGGL((attention_join_kernel<T, D, false, MODE>), grid, dim3(512), 0, st, a, p.weights, (int)blocks64, first);
+    }
 }
 
 // The kernel over `tiles_in_all` tiles per head, and the joining launch where there are splits

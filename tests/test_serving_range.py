@@ -150,3 +150,21 @@ def test_shared_infinite_values(bl, bad, dtype):  # noqa: F811
     rel = 2**-7 if dtype == "bf16" else 2e-5
     np.testing.assert_allclose(_np(got)[:, rest.cpu().numpy()], _np(whole)[:, rest.cpu().numpy()], rtol=rel, atol=rel * float(whole[:, rest].abs().max()))
     np.testing.assert_allclose(_np(got)[:, 5], _np(whole)[:, 5], rtol=rel)
+
+
+def test_shared_more_rows_than_one_launch_joins(bl):  # noqa: F811
+    """2^25 query rows of 128, which are joined by a thread per element: every row as in a batch of four tokens."""
+    m, hq, hkv, d = 2**19, 64, 8, 128
+    if torch.cuda.get_device_properties(0).total_memory < 100e9:
+        pytest.skip("needs 52 GB")
+    c, prefix = _behind(bl, length=50, lens=(1000,), new=(4,), hkv=hkv, d=d)
+    table = _i32(c.table[:, :1])  # the tokens past it do not exist: every row sees the same
+    few = _rand((4, hq, d), 5, torch.bfloat16, 1.5)
+    args = (c.cache, _i32(prefix[:1]), _i32([50]), table, _i32([1000]))
+    want = bl.attention_shared(few, *args, _starts([4]))
+    out = bl.attention_shared(few.repeat(m // 4, 1, 1), *args, _starts([m])).view(-1, 4, hq * d)
+    for part in out.split(2**14):
+        assert (part == out[0]).all()
+    assert (out[0].float() - want.float()).abs().max() <= 2.0**-7 * want.float().abs().max()
+    del out
+    torch.cuda.empty_cache()
