@@ -45,11 +45,14 @@ hipError_t launch_attention_selected(const SelectedProblem &p, void *ws, hipStre
         a.part_o = static_cast<float *>(ws);
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(ws) + selected_layout(r).part_ml);
     }
-    // Lists of more than a quarter of the last-level cache are read past it (40 tokens' 32 blocks
-    // of 32/8 heads of 128, 168 MB: 33.4 us beside 38.7); shorter ones may be in it still (one
-    // token's 64 blocks, 8 MB read again: 10.7 us beside 10.0)
+    // Lists of more than a third of the last-level cache, of one row per sequence, are read past
+    // it: 32 blocks of 32/8 heads of 128 for 16 rows (64 MB) 19.1 us beside 15.8 through it, for 20
+    // rows 18.9 and 19.0, 24 rows 19.5 and 19.8, 64 rows 45.1 and 47.9, 128 rows 84.5 and 92.4 (other
+    // inputs from call to call). Rows of one sequence mostly list the same blocks, which the cache
+    // holds for them: 10 x 4 rows, 8 of their 32 blocks common 31.0 and 28.9, 24 of them 26.4 and
+    // 21.8; 8 x 32 rows 78.6 and 61.8
     const int64_t bytes = p.c.m * p.c.kv_heads * p.keep * 2 * kBlock * p.c.head_dim;
-    if (bytes >= (int64_t)64 << 20) launch_tiles<kSelectedPast>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, st);
+    if (p.c.m == p.c.seqs && bytes >= (int64_t)96 << 20) launch_tiles<kSelectedPast>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, st);
     else launch_tiles<kSelected>(p.c, a, shape, rt, p.c.m * a.tiles_per_seq, st);
     return hipGetLastError();
 }

@@ -754,3 +754,25 @@ def test_another_stream(bl):  # noqa: F811
     torch.cuda.synchronize()
     for i, got in enumerate(outs):
         assert all(torch.equal(a, b) for a, b in zip(got, alone[i % 2]))
+
+
+# ---------------------------------------------------------------- the launch rules' other sides
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_selected_long_lists_of_one_sequences_rows(bl, dtype):  # noqa: F811
+    """Rows of one sequence whose lists are long together and share blocks: every row as in a batch of a few, and those
+    as the definition has them."""
+    c = _Paged(bl, [4096], [303], 2, 64, 8)
+    rng = np.random.default_rng(3)
+    sel = np.sort(rng.integers(0, 64, (3, 2, 64)), -1)
+    _, _ = _check_selected(bl, c, [4096], [3], 4, sel, dtype)
+    q = _rand((3, 4, 64), 5, DTYPES[dtype], 1.5)
+    lists, table, lens = _i32(sel), _i32(c.table), _i32([4096])
+    few = bl.attention_selected(q, c.cache, table, lens, lists, _starts([3]))
+    for m in (303, 60):
+        i = torch.arange(m, device="cuda") % 3
+        many = bl.attention_selected(q[i].contiguous(), c.cache, table, lens, lists[i].contiguous(), _starts([m]))
+        for r in range(3):
+            assert (many[r::3] == many[r]).all()
+        off = (many[:3].float() - few.float()).abs().max() / few.float().abs().max()
+        assert off < (2.0**-7 if dtype == "bf16" else 2e-5)
