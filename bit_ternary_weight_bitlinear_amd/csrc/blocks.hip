@@ -509,12 +509,19 @@ hipError_t launch_cache_bounds(const CacheBounds &p, hipStream_t st)
 }
 
 // One workgroup reads a head's bounds at 64 bytes a cycle and takes 6 us of arithmetic for
-// 2048 blocks: where rows and heads leave CUs idle, the scores are a launch of their own. Of 8 heads, 4 rows
-// each: 2048 blocks of one token 12.6 us in two launches and 17.4 in one, of 8 tokens 14.5 and
-// 18.5, of 32 tokens 24.2 and 18.6; 300 blocks of one token 10.6 and 8.7, 600 within noise.
+// 2048 blocks: where rows and heads leave CUs idle, the scores are a launch of their own. On the
+// device, of 8 heads with 4 rows each (m x heads: two launches and one, us):
+//   550 blocks   16: 10.2, 10.1   64: 11.3, 11.0   96: 14.0, 12.2
+//   1000         32: 11.5, 12.3   64: 13.3, 14.2   96: 15.6, 14.5   192: 18.8, 17.3
+//   1100         64: 14.7, 15.7   96: 15.5, 16.1   128: 17.3, 16.8  192: 20.5, 19.0
+//   1500         64: 15.3, 17.3   96: 17.8, 18.1   160: 20.8, 20.6  192: 23.3, 22.5
+//   2048         8: 11.2, 17.1    64: 16.7, 21.0   96: 19.3, 21.9   192: 29.8, 31.0   256: 39.0, 37.9
+//   4096         64: 22.8, 29.6   96: 30.6, 43.4   192: 52.3, 53.6  256: 65.3, 64.6
+//   8192         64: 43.2, 79.1   128: 68.6, 87.1  192: 93.7, 100.9
+// 300 blocks of one token 10.6 and 8.7.
 static bool two_launches(int64_t m, int64_t kv_heads, int64_t max_blocks)
 {
-    return max_blocks > kKeysInLds || (max_blocks > 512 && m * kv_heads <= 64);
+    return max_blocks > kKeysInLds || (max_blocks > 512 && m * kv_heads <= (max_blocks < 1500 ? 64 : 192));
 }
 
 int64_t block_select_workspace(int64_t m, int64_t kv_heads, int64_t max_blocks)
@@ -550,8 +557,8 @@ hipError_t launch_block_select(const SelectProblem &p, void *ws, hipStream_t st)
         for (int64_t first = 0; first < items; first += kMostGroups) {
             const int64_t end = first + kMostGroups < items ? first + kMostGroups : items;
             const dim3 grid((unsigned)round_up(end - first, 8));
-            // Small workgroups overlap each other's waits: 512 of 500 blocks take 18.7 us with 256
-            // threads and 31.9 with 1024, before the later steps; of 2048 blocks either is as fast
+            // Small workgroups overlap each other's waits: 512 of 500 blocks take 15.7 us with 256
+            // threads and 26.0 with 1024, of 1000 blocks 24.2 and 36.7, of 2000 41.6 and 47.6
             if (p.max_blocks <= 2048) hipLaunchKernelGGL((block_select_kernel<T, D, 256, 2048>), grid, dim3(256), 0, st, a, first, end);
             else hipLaunchKernelGGL((block_select_kernel<T, D, 1024, kKeysInLds>), grid, dim3(1024), 0, st, a, first, end);
         }

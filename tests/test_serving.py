@@ -776,3 +776,18 @@ def test_selected_long_lists_of_one_sequences_rows(bl, dtype):  # noqa: F811
             assert (many[r::3] == many[r]).all()
         off = (many[:3].float() - few.float()).abs().max() / few.float().abs().max()
         assert off < (2.0**-7 if dtype == "bf16" else 2e-5)
+
+
+@pytest.mark.parametrize("m,wide", [(130, 700), (40, 1400), (48, 1500), (97, 1500), (64, 2100), (97, 2100), (98, 2049), (97, 8192)])
+def test_select_many_rows_of_wide_tables(bl, m, wide):  # noqa: F811
+    """Two heads of so many rows and blocks that the scores are a launch of their own, and that they are not, with the keys
+    of either size of workgroup: three rows against the definition, the others as these."""
+    ends = [64 * wide - 1, 64 * (wide - 37) + 5, 64 * 520]
+    c = _Bounds(bl, ends, [1] * 3, 2, 64, 3, wide=wide, pages=400)
+    c.ks = (0.5 + 2 * np.random.default_rng(4).random(c.ks.shape)).astype(np.float32)
+    q = _rand((3, 4, 64), 8, torch.bfloat16, 1.5)
+    few = c.check(bl, q, ends, 40, None, 1, 2)
+    i = torch.arange(m, device="cuda") % 3
+    many = bl.block_select(q[i].contiguous(), torch.tensor(c.bounds).cuda(), torch.tensor(c.ks).cuda(), _i32(c.table)[i].contiguous(),
+                           _i32(ends)[i].contiguous(), 40, first=1, recent=2)
+    assert torch.equal(many, few[i])
