@@ -791,3 +791,16 @@ def test_select_many_rows_of_wide_tables(bl, m, wide):  # noqa: F811
     many = bl.block_select(q[i].contiguous(), torch.tensor(c.bounds).cuda(), torch.tensor(c.ks).cuda(), _i32(c.table)[i].contiguous(),
                            _i32(ends)[i].contiguous(), 40, first=1, recent=2)
     assert torch.equal(many, few[i])
+
+
+def test_select_beside_rows_outside_the_sequences(bl):  # noqa: F811
+    """Rows of NaN and infinities before and behind the sequences, where scores decide: not written, nothing of them enters."""
+    lens, new, cu = [64 * 40 + 3, 64 * 25], [2, 3], _i32([2, 4, 7])
+    c = _Bounds(bl, lens, new, 2, 64, 3)
+    q = _rand((11, 8, 64), 3, torch.float32)
+    inner = q[2:7].contiguous()
+    q[:2], q[7:] = float("nan"), float("inf")
+    want = c.check(bl, inner, lens, 9, _starts(new), 1, 2)
+    got = c.check(bl, q, lens, 9, cu, 1, 2)
+    assert torch.equal(got[2:7], want) and (got[:2] == 77).all() and (got[7:] == 77).all()
+    assert (want[:, :, 1:] > 0).all() and not torch.equal(want[0, 0], want[0, 1])  # by scores, which differ
