@@ -804,3 +804,9 @@ def test_select_beside_rows_outside_the_sequences(bl):  # noqa: F811
     got = c.check(bl, q, lens, 9, cu, 1, 2)
     assert torch.equal(got[2:7], want) and (got[:2] == 77).all() and (got[7:] == 77).all()
     assert (want[:, :, 1:] > 0).all() and not torch.equal(want[0, 0], want[0, 1])  # by scores, which differ
+
+
+@pytest.mark.parametrize("m", [1714, 1715])
+def test_rotate_waves_of_a_token(bl, m):  # noqa: F811
+    """Seven rounds of heads by a wave each, and by one wave."""
+    _check_rotate(bl, [m - 5, 0, 5], [3, 0, 900], 20, 5, 128, 64, "f32")
