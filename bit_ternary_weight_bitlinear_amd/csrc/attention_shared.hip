@@ -410,16 +410,22 @@ static int64_t splits_of(int64_t units, int64_t blocks, int64_t target)
     const int64_t most = ceil_div(blocks, kPrefixWaves), s = target / units < most ? target / units : most;
     return s < 1 ? 1 : s > 256 ? 256 : s;
 }
-// About one per CU
+// About one per CU. With targets of 128, 256 and 512: 64 rows of 32/8 heads behind 16384 tokens
+// 63.4, 42.8 and 49.5 us in bf16, 77.5, 53.8 and 58.8 in fp32; 12 x 4 of 20/5 behind 6001, fp32
+// 25.4, 23.2 and 30.5; 16 of 32/8 behind 32768 38.2, 29.6 and 35.0. Hundreds of rows per
+// sequence leave no splits (8 x 64 of 32/8 behind 8000, bf16: 147 us with any)
 static int64_t prefix_splits(const SharedProblem &p)
 {
     return splits_of(ceil_div(p.c.m * (p.c.q_heads / p.c.kv_heads), kPrefixRows) * p.c.kv_heads, p.prefix_blocks, 256);
 }
-// Two per CU: 64 rows of 32/8 heads behind 16384 tokens take 41.1 us in all, with
-// a target of 256 41.9 and of 1024 43.7
+// About one per CU: beside a workgroup of the prefix there is room for one. With targets of 128, 256
+// and 512: 64 rows of 32/8 heads behind 16384, up to 700 of their own, 42.4, 42.5 and 42.5 us; 12 x 4 of
+// 20/5 behind 6001 20.4, 20.4 and 21.9 in fp32, 19.7, 19.6 and 21.8 in bf16; 16 of 32/8 behind 32768, 1500
+// own, 32.7, 31.0 and 31.4; 4 behind 8000, 8000 own, 19.1, 18.6 and 20.8; 20 x 2 behind 3000, 1000
+// own, 21.9, 21.8 and 25.5; 48 of 12/4 heads of 64 behind 5000 13.0, 13.1 and 15.2
 static int64_t own_splits(const CachedProblem &c)
 {
-    return splits_of(units_of(c, row_tiles(c)), c.max_blocks, 512);
+    return splits_of(units_of(c, row_tiles(c)), c.max_blocks, 256);
 }
 
 struct SharedLayout {
