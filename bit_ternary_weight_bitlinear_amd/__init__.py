@@ -567,7 +567,8 @@ def attention_shared(q: torch.Tensor, cache: KVCache, prefix_table: torch.Tensor
                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """attention_cached of a batch whose sequences share a prefix: every row sees the prefix's tokens (pages
     prefix_table int32 [prefix_blocks], prefix_len int32 [1] of them) and its own sequence's up to itself. lens and
-    block_table count and hold the sequences' own tokens only."""
+    block_table count and hold the sequences' own tokens only. For bf16 queries the softmax weights over the prefix are
+    rounded to fp16 (2^-11 of themselves; attention_cached holds 23 bits, as this call does for fp32)."""
     return (_native or _attention_calls()).attention_shared(q, cache, prefix_table, prefix_len, block_table, lens, cu_seqlens, scale,
                                                             out, workspace)
 

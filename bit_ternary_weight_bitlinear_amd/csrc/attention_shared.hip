@@ -24,15 +24,19 @@
 // of its 32, which gives a lane half h the 16 tokens that one 16-byte piece of V holds. The
 // dims of the first product are ordered likewise by 16-byte pieces of K.
 //
-// What bounds it: a page and 32 rows are 36 matrix instructions (1150 cycles) and about 490
-// vector ones (32 of them exponentials, 2300 cycles) in bf16, which take turns rather than
-// overlap: 3500 cycles a page measured with one wave per SIMD, as much for each of two. 64
-// tokens of 32/8 heads behind 16384, 300 to 700 of their own: 38 us, and 4.8 for the join
-// (prefix alone 31, own pages alone 18; one behind the other 52). One workgroup of the prefix
-// per CU leaves room for one of own pages, which wait for memory (two: 46 us in all). Not
-// kept: codes as fp16 through LDS for 128 rows, a barrier a page (40 us for the prefix); 64
-// rows per wave (35); K's codes raised by 128 too (2.5 us less, but a channel that sets a
-// page's scale would round the logits of the others).
+// What bounds it: a page and 32 rows are 36 matrix instructions (1150 cycles) and about 550
+// vector ones (32 of them exponentials, 2600 cycles) in bf16, which take turns rather than
+// overlap: 1.85 us a page (16 pages a wave beside 8), 2.4 in fp32. 64 tokens of 32/8 heads behind
+// 16384, up to 700 of their own: 40.4 us with the join (with one of their own each 40.8, without
+// the prefix 16.9; prefix and own pages in launches one behind the other 52). One workgroup of
+// the prefix per CU leaves room for one of own pages, which wait for memory. Not
+// kept, beside 31 us for the prefix then: codes as fp16 through LDS for 128 rows, a barrier a page
+// (40); 64 rows per wave (35). Codes raised by 128 (K's 2.5 us less in all, V's 0.5), but a
+// channel that sets a page's scale would round the logits of the others, and the largest finite
+// number in V would turn every dim into an infinity. For bf16 results weights in two
+// parts, 49.0 us beside 41.6: the results' rms error against 64 bits is 1.675e-3 of their rms with
+// one part, and 1.663e-3 with two, with fp32 weights or by attention_cached.hip's digits, the
+// rounding to bf16 being that.
 #include "attention_cached.hpp"
 
 namespace bl {

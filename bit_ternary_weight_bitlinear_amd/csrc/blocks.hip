@@ -25,8 +25,8 @@ __device__ inline uint32_t v2s_bits(v2s v) { return __builtin_bit_cast(uint32_t,
 
 // One wave per (reached block, kv head). A lane's 16-byte pieces are 16 dims of the tokens
 // that share its place in a tile, so what is left are 16 neighbouring lanes. Bound by HBM
-// where there are many blocks (55059 tokens of 8 heads of 128: 12.7 us, 4.6 TB/s), by latency
-// with a token per sequence (32 of them: 4.2 us).
+// where there are many blocks (55059 tokens of 8 heads of 128: 12.7 us a call, 4.6 TB/s), by
+// latency with a token per sequence (32 of them: 3.7 us on the device, 4.2 a call).
 template <int D>
 __global__ __launch_bounds__(64) void cache_bounds_kernel(const int8_t *__restrict__ k_codes, int8_t *__restrict__ bounds, int64_t pages,
                                                           int64_t m, const int32_t *__restrict__ cu, const int32_t *__restrict__ lens,

@@ -16,8 +16,8 @@
 //
 // Bound by HBM with many tokens: 8192 of 32/8 heads of 128 in bf16, normed, 168 MB in 31 us
 // (5.4 TB/s; without the next round's heads on their way and one set of gains for both sides
-// 5 % more), by a launch and its chain of loads with few: one token 2.7 us, 192 tokens of 20/5
-// heads in fp32 3.9 (a wave per round of heads there). The loads pass the caches by, which
+// 5 % more), by a launch and its chain of loads with few: one token 2.7 us on the device, 192 tokens
+// of 20/5 heads in fp32 3.9 (a wave per round of heads there; a call takes 5.4). The loads pass the caches by, which
 // keep what is stored for the append and the attention that read it: 31.1 us beside 36.6 with
 // plain loads, with an append behind it 45.2 beside 46.3 (with stores that pass them by too 50.5).
 #include "attention.hpp"
@@ -35,8 +35,9 @@ struct RotateArgs {
     int parts;  // waves per token
 };
 
-// Cosine and sine of position * freq: Taylor's series to r^15 on |r| <= pi / 4 (off by
-// less than 1e-16 of 1), rounded to fp32 once.
+// Cosine and sine of position * freq: Taylor's series to r^14 and r^15 on |r| <= pi / 4 (the
+// cosine's next term is 1.0e-15, the sine's 5e-17; beside exact values both are off by at most
+// 1e-15 up to |t| = 2^45 and by 1.4e-14 up to 2^50), rounded to fp32 once.
 __device__ inline float2 turn(int64_t position, float freq)
 {
     const double p = (double)position, f = freq, t = p * f, rest = __builtin_fma(p, f, -t);

@@ -483,8 +483,8 @@ bl_status bitlinear_cache_evict(const int32_t *block_table, const int32_t *lens,
  *   (a, b) -> (a * cs - b * sn, b * cs + a * sn),  cs = magnitude * cos t, sn = magnitude * sin t
  * with (a, b) = (y[2i], y[2i + 1]) if `interleaved`, (y[i], y[i + rotary_dim / 2]) if not;
  * elements from rotary_dim on stay y. One rounding to `dtype` at the end. Angles are
- * exact up to rounding of cs and sn to fp32, whatever the position. A head whose squares
- * pass fp32's range has r = 0.
+ * exact up to rounding of cs and sn to fp32, whatever the position, while |t| < 2^50. A
+ * head whose squares pass fp32's range has r = 0.
  *   q, k            as in bitlinear_attention
  *   inv_freq        fp32 [rotary_dim / 2], 4-byte aligned
  *   rotary_dim      16 .. head_dim, a multiple of 16 (BL_ERR_SHAPE otherwise)
